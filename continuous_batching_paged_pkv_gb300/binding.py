@@ -34,6 +34,7 @@ PKV_NO_ALLOC_SCRATCH_BYTES = 32 << 20
 PKV_WORK_WORDS_PER_ITEM = 4
 PKV_STEP_IN_PLACE = 1
 PKV_STEP_IN_PLACE_MAX_BYTES = 1 << 20
+PKV_ROPE_NONE, PKV_ROPE_LINEAR, PKV_ROPE_NTK, PKV_ROPE_BY_PARTS, PKV_ROPE_YARN = range(5)
 
 
 class PkvError(RuntimeError):
@@ -64,6 +65,17 @@ class PoolStats(ctypes.Structure):
                 ("max_slots", ctypes.c_int32), ("free_blocks", ctypes.c_int64),
                 ("owned_blocks", ctypes.c_int64), ("live_slots", ctypes.c_int32),
                 ("live_tokens", ctypes.c_int64), ("shared_blocks", ctypes.c_int64)]
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_len", ctypes.c_int64), ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
+
+
+class RopeTable(ctypes.Structure):
+    _fields_ = [("phases", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
 
 
 class Segment(ctypes.Structure):
@@ -113,6 +125,12 @@ def _lib():
             "pkv_cache_write_q4": ([p, p, p, i64, p, p, p, p, i64, i32, i32, i32, p, p], ctypes.c_int),
             "pkv_attention_q4": ([p, p, i32, i64, p, p, p, i32, i32, i32, p, p, p, p, i64, i32, i32, i32, f32, p,
                                   ctypes.POINTER(WorkInfo), p, p, u64, p, p], ctypes.c_int),
+            "pkv_rope_plan": ([ctypes.POINTER(RopeConfig), p, p, ctypes.POINTER(f32)], ctypes.c_int),
+            "pkv_rope_phases": ([p, i32, p], ctypes.c_int),
+            "pkv_plan_positions": ([p, i32, p, p, i32, p, i64], ctypes.c_int),
+            "pkv_rope": ([p, i64, p, ctypes.POINTER(RopeTable), i64, i32, i32, p, i64, p], ctypes.c_int),
+            "pkv_rope_cache_write": ([p, i64, p, i64, p, i64, p, p, ctypes.POINTER(RopeTable), i64, i32, i32, i32, p,
+                                      i64, p, p, i64, i32, p, p], ctypes.c_int),
             "pkv_stage_layout_init": ([ctypes.POINTER(StageLayout), i64, i32, i32, i32, i32, i32, i32], ctypes.c_int),
             "pkv_step": ([ctypes.POINTER(StageLayout), p, u64, p, u64, p, p, i64, i32, f32, p, u64, p, p, p, p,
                           ctypes.POINTER(WorkInfo), ctypes.c_uint32], ctypes.c_int),
@@ -270,6 +288,53 @@ def pkv_plan_work(cu_seqlens_q, seq_slot, context_lens, *, max_slots: int, max_b
     return work, info
 
 
+def pkv_plan_positions(cu_seqlens_q, seq_slot, context_lens) -> np.ndarray:
+    """Position of every packed row of a lowered step (int32)."""
+    cu = np.ascontiguousarray(cu_seqlens_q, dtype=np.int32)
+    ss = np.ascontiguousarray(seq_slot, dtype=np.int32)
+    cl = np.ascontiguousarray(context_lens, dtype=np.int32)
+    if len(ss) != len(cu) - 1:
+        raise ValueError("seq_slot must have one entry per segment")
+    out = np.empty(max(int(cu[-1]), 0), np.int32)
+    _check(_lib().pkv_plan_positions(_np_ptr(cu), len(cu) - 1, _np_ptr(ss), _np_ptr(cl), len(cl), _np_ptr(out),
+                                     len(out)), "pkv_plan_positions")
+    return out
+
+
+@dataclass
+class RopePlan:
+    rot_dim: int
+    frequencies: np.ndarray  # float64 [rot_dim / 2], radians per position
+    phases: np.ndarray       # uint64 [rot_dim / 2], fractions of a turn per position
+    magnitude: float
+
+    def phase_tensor(self, device):
+        """The phases on the device, as the int64 tensor that the device calls take."""
+        import torch
+
+        return torch.from_numpy(self.phases.view(np.int64)).to(device)
+
+
+def pkv_rope_plan(rot_dim: int, *, base: float = 10000.0, scaling: int = PKV_ROPE_NONE, factor: float = 1.0,
+                  original_len: int = 0, low: float = 1.0, high: float = 32.0) -> RopePlan:
+    if rot_dim < 0:
+        raise PkvError(1, "pkv_rope_plan")
+    cfg = RopeConfig(rot_dim, scaling, base, factor, original_len, low, high)
+    n = rot_dim // 2
+    freqs, phases, mag = np.empty(n, np.float64), np.empty(n, np.uint64), ctypes.c_float(0)
+    _check(_lib().pkv_rope_plan(ctypes.byref(cfg), _np_ptr(freqs), _np_ptr(phases), ctypes.byref(mag)),
+           "pkv_rope_plan")
+    return RopePlan(rot_dim, freqs, phases, mag.value)
+
+
+def pkv_rope_phases(frequencies) -> np.ndarray:
+    """uint64 phases of frequencies of the caller's own (radians per position)."""
+    f = np.ascontiguousarray(frequencies, dtype=np.float64)
+    out = np.empty(len(f), np.uint64)
+    _check(_lib().pkv_rope_phases(_np_ptr(f), len(f), _np_ptr(out)), "pkv_rope_phases")
+    return out
+
+
 # ---------------------------------------------------------------------------
 # Device calls (torch tensors on the GPU).
 # ---------------------------------------------------------------------------
@@ -332,6 +397,114 @@ def pkv_attention_no_alloc(q, cu_seqlens_q, seq_slot, context_lens, block_tables
                                          bs, _t_ptr(k_pool), _t_ptr(v_pool), nb, q.shape[1], hkv, d, float(scale),
                                          _t_ptr(work), ctypes.byref(info), _t_ptr(out), _t_ptr(device_status),
                                          _stream(stream)), "pkv_attention_no_alloc")
+
+
+def _need_on(device, *tensors):
+    """Every tensor on `device`, which must be the current one (the library launches on the current device)."""
+    import torch
+
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on {device}, got one on {t.device}")
+
+
+def _need_rows(t, tokens, what: str):
+    """bf16 [tokens, heads, head_dim] whose rows may lie apart, each of them dense; returns (heads, head_dim, stride)."""
+    if t is None or not t.is_cuda or str(t.dtype) != "torch.bfloat16" or t.dim() != 3 or \
+            (tokens is not None and t.shape[0] != tokens):
+        raise ValueError(f"{what} must be a CUDA tensor of torch.bfloat16, [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    if n and h and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{what}: the heads of a token must lie one behind the other")
+    return h, d, (t.stride(0) if n > 1 else -(-h * d // 8) * 8)
+
+
+def _rope_table(phases, rot_dim, interleaved, magnitude):
+    _need(phases, "torch.int64", "phases")
+    if phases.numel() != rot_dim // 2:
+        raise ValueError(f"phases must hold rot_dim / 2 = {rot_dim // 2} values, got {phases.numel()}")
+    return RopeTable(phases.data_ptr(), int(rot_dim), 1 if interleaved else 0, float(magnitude))
+
+
+class _BoundCall:
+    """A device call with its arguments checked and marshalled once, for a loop that reuses the same buffers.
+
+    The buffers must stay in place while the object is used; it holds references to them. With
+    ``stream=None`` every call runs on the stream that is current then."""
+
+    def _bind(self, name, args, keep, stream):
+        self._fn, self._name, self._args = getattr(_lib(), name), name, args
+        self._keep, self._on = keep, None if stream is None else _stream(stream)
+
+    def __call__(self) -> None:
+        rc = self._fn(*self._args, _stream(None) if self._on is None else self._on)
+        if rc != PKV_OK:
+            raise PkvError(rc, self._name)
+
+
+class RopeCall(_BoundCall):
+    """``pkv_rope`` bound once."""
+
+    def __init__(self, x, positions, phases, out, *, rot_dim: int, interleaved: bool = False, magnitude: float = 1.0,
+                 stream=None):
+        h, d, xs = _need_rows(x, None, "x")
+        t = x.shape[0]
+        if _need_rows(out, t, "out")[:2] != (h, d):
+            raise ValueError("out must have x's shape")
+        _need(positions, "torch.int32", "positions")
+        if positions.numel() != t:
+            raise ValueError("positions must have one entry per token")
+        table = _rope_table(phases, rot_dim, interleaved, magnitude)
+        _need_on(x.device, positions, phases, out)
+        self._bind("pkv_rope", (_t_ptr(x), xs, _t_ptr(positions), ctypes.byref(table), t, h, d, _t_ptr(out),
+                                _need_rows(out, t, "out")[2]), (x, positions, phases, out, table), stream)
+
+
+class RopeCacheWriteCall(_BoundCall):
+    """``pkv_rope_cache_write`` bound once."""
+
+    def __init__(self, q, k_new, v_new, positions, phases, slot_mapping, q_out, k_pool, v_pool, *, rot_dim: int,
+                 interleaved: bool = False, magnitude: float = 1.0, device_status=None, stream=None):
+        hq, d, qs = _need_rows(q, None, "q")
+        t = q.shape[0]
+        hkv, dk, ks = _need_rows(k_new, t, "k_new")
+        hv, dv, vs = _need_rows(v_new, t, "v_new")
+        ho, do, os_ = _need_rows(q_out, t, "q_out")
+        if (ho, do) != (hq, d) or (hv, dv) != (hkv, d) or dk != d:
+            raise ValueError("q_out must have q's shape, v_new k_new's, all one head_dim")
+        _need(k_pool, "torch.bfloat16", "k_pool")
+        _need(v_pool, "torch.bfloat16", "v_pool")
+        if k_pool.dim() != 4 or k_pool.shape[1] != hkv or k_pool.shape[3] != d or v_pool.shape != k_pool.shape:
+            raise ValueError("k_pool and v_pool must be [blocks, kv heads, block_size, head_dim]")
+        nb, _, bs, _ = k_pool.shape
+        _need(positions, "torch.int32", "positions")
+        _need(slot_mapping, "torch.int64", "slot_mapping")
+        if positions.numel() != t or slot_mapping.numel() != t:
+            raise ValueError("positions and slot_mapping must have one entry per token")
+        table = _rope_table(phases, rot_dim, interleaved, magnitude)
+        _need_on(q.device, k_new, v_new, positions, phases, slot_mapping, q_out, k_pool, v_pool, device_status)
+        self._bind("pkv_rope_cache_write",
+                   (_t_ptr(q), qs, _t_ptr(k_new), ks, _t_ptr(v_new), vs, _t_ptr(positions), _t_ptr(slot_mapping),
+                    ctypes.byref(table), t, hq, hkv, d, _t_ptr(q_out), os_, _t_ptr(k_pool), _t_ptr(v_pool), nb, bs,
+                    _t_ptr(device_status)),
+                   (q, k_new, v_new, positions, phases, slot_mapping, q_out, k_pool, v_pool, device_status, table),
+                   stream)
+
+
+def pkv_rope(x, positions, phases, out, *, rot_dim: int, interleaved: bool = False, magnitude: float = 1.0,
+             stream=None) -> None:
+    """Rotate ``x`` [tokens, heads, head_dim] into ``out`` (which may be ``x``); ``phases`` from a RopePlan."""
+    RopeCall(x, positions, phases, out, rot_dim=rot_dim, interleaved=interleaved, magnitude=magnitude,
+             stream=stream)()
+
+
+def pkv_rope_cache_write(q, k_new, v_new, positions, phases, slot_mapping, q_out, k_pool, v_pool, *, rot_dim: int,
+                         interleaved: bool = False, magnitude: float = 1.0, device_status=None, stream=None) -> None:
+    """Rotate a step's queries into ``q_out`` and its keys into the pool beside its values, in one pass."""
+    RopeCacheWriteCall(q, k_new, v_new, positions, phases, slot_mapping, q_out, k_pool, v_pool, rot_dim=rot_dim,
+                       interleaved=interleaved, magnitude=magnitude, device_status=device_status, stream=stream)()
 
 
 def _need_quant_pool(k_codes, k_scales, v_codes, v_scales, bits: int):

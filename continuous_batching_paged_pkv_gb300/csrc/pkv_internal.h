@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -68,6 +69,22 @@ cudaError_t launch_cache_write(const void *k_new, const void *v_new, const int64
                                int64_t num_tokens, void *k_pool, void *v_pool, int64_t num_blocks,
                                int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
                                uint32_t *status, cudaStream_t stream);
+
+// Rotation of a step's rows (pkv_rope.cu): q rows to q_out; with kv heads, k
+// rows rotated and v rows copied into the pool rows of slot_mapping.
+struct RopeArgs {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16 *q_out, *k_pool, *v_pool;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;  // elements between tokens
+  const int32_t *positions;
+  const int64_t *slot_mapping;
+  const uint64_t *phases;  // [rot_dim / 2] fractions of a turn per position
+  int64_t num_tokens, num_blocks;
+  int32_t num_q_heads, num_kv_heads, head_dim, rot_dim, interleaved, block_size;
+  float magnitude;
+  uint32_t *status;
+};
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream);
 
 cudaError_t launch_copy_blocks(const int32_t *pairs, int64_t num_pairs, void *const *arrays,
                                const int64_t *block_bytes, int32_t num_arrays, int64_t num_blocks, uint32_t *status,

@@ -391,6 +391,94 @@ pkv_status pkv_attention_no_alloc(const void *q, const int32_t *cu_seqlens_q, in
                                   void *out, uint32_t *device_status, pkv_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Rotary positions. The pages leave positions to the model; a step whose
+ * model rotates queries and keys does so right before the cache write.
+ * ---------------------------------------------------------------------- */
+
+/* How the rotation speeds of a head are stretched for a longer context. */
+typedef enum pkv_rope_scaling {
+    PKV_ROPE_NONE = 0,     /* f_i = base^(-2 i / rot_dim) */
+    PKV_ROPE_LINEAR = 1,   /* f_i / factor (positions interpolated) */
+    PKV_ROPE_NTK = 2,      /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+    PKV_ROPE_BY_PARTS = 3, /* f_i (g + (1 - g) / factor), g = (turns - low) / (high - low) clamped to
+                              [0, 1], turns = original_len f_i / 2 pi */
+    PKV_ROPE_YARN = 4      /* f_i (1 - g + g / factor), g = (i - a) / (b - a) clamped to [0, 1] over
+                              the pair indices a, b that make high and low turns over original_len
+                              (a rounded down and at least 0, b up and at most rot_dim - 1; b - a at
+                              least 0.001), magnitude 0.1 ln(factor) + 1 for factor > 1 */
+} pkv_rope_scaling;
+
+typedef struct pkv_rope_config {
+    int32_t rot_dim;      /* rotated elements of a head: even, the first rot_dim of head_dim */
+    int32_t scaling;      /* pkv_rope_scaling */
+    double base;          /* > 1 */
+    double factor;        /* > 0; ignored by PKV_ROPE_NONE */
+    int64_t original_len; /* context the model was trained on (BY_PARTS, YARN) */
+    double low, high;     /* turns over original_len, 0 < low < high (BY_PARTS, YARN) */
+} pkv_rope_config;
+
+/* What the device calls take. */
+typedef struct pkv_rope_table {
+    const uint64_t *phases; /* device [rot_dim / 2], from pkv_rope_plan or pkv_rope_phases */
+    int32_t rot_dim;        /* even, 2 .. head_dim */
+    int32_t interleaved;    /* pair i: 0 elements (i, i + rot_dim / 2), 1 elements (2 i, 2 i + 1) */
+    float magnitude;        /* factor of the rotated elements, finite */
+} pkv_rope_table;
+
+/*
+ * Rotation speeds of the rot_dim / 2 pairs (host only): `frequencies`
+ * (nullable) in radians per position, `phases` (nullable) as 64-bit fractions
+ * of a turn per position, `magnitude` (nullable) the factor of the rotated
+ * elements (1 but for YARN). The speeds are computed in double precision.
+ */
+pkv_status pkv_rope_plan(const pkv_rope_config *config, double *frequencies, uint64_t *phases, float *magnitude);
+
+/* The phases of frequencies of the caller's own (finite radians per position). */
+pkv_status pkv_rope_phases(const double *frequencies, int32_t num_pairs, uint64_t *phases);
+
+/*
+ * Position of every packed row of a lowered step (host only): row i of
+ * segment s (n rows, slot c) sits at context_lens[c] - n + i. `positions`
+ * holds `capacity` int32 entries, at least cu_seqlens_q[num_seqs].
+ */
+pkv_status pkv_plan_positions(const int32_t *cu_seqlens_q, int32_t num_seqs, const int32_t *seq_slot,
+                              const int32_t *context_lens, int32_t max_slots, int32_t *positions,
+                              int64_t capacity);
+
+/*
+ * Rotate rows: x (device, bf16, num_tokens rows of [num_heads][head_dim]
+ * starting x_stride elements apart) into out (out_stride apart), every head
+ * of token t by positions[t] (device, int32, any value). Computed in fp32 from
+ * exact angles, rounded once (nearest even); elements from rot_dim on are
+ * copied. out may be x itself with the same stride; any other overlap is
+ * refused, but the two may be different columns of one buffer. Strides are
+ * multiples of 8 elements, pointers 16-byte aligned. With a pool in 8 or 4
+ * bits, rotate the keys with this call and append them with
+ * pkv_cache_write_q8 / _q4.
+ */
+pkv_status pkv_rope(const void *x, int64_t x_stride, const int32_t *positions, const pkv_rope_table *rope,
+                    int64_t num_tokens, int32_t num_heads, int32_t head_dim, void *out, int64_t out_stride,
+                    pkv_stream_t stream);
+
+/*
+ * pkv_rope of the step's queries and keys and pkv_cache_write in one pass:
+ *   q      rows of [num_q_heads][head_dim], rotated into q_out
+ *   k_new  rows of [num_kv_heads][head_dim], rotated into k_pool at slot_mapping
+ *   v_new  rows of [num_kv_heads][head_dim], copied into v_pool at slot_mapping
+ * with the strides, positions and results of pkv_rope (q, k_new and v_new may
+ * be the parts of one fused row per token; q_out may be q) and the pool, the
+ * slot mapping (< 0: the token's key and value are not kept; its query is
+ * rotated all the same), the device status and the ordering rules of
+ * pkv_cache_write. pkv_attention may follow directly on q_out and the pool.
+ */
+pkv_status pkv_rope_cache_write(const void *q, int64_t q_stride, const void *k_new, int64_t k_stride,
+                                const void *v_new, int64_t v_stride, const int32_t *positions,
+                                const int64_t *slot_mapping, const pkv_rope_table *rope, int64_t num_tokens,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, void *q_out,
+                                int64_t q_out_stride, void *k_pool, void *v_pool, int64_t num_blocks,
+                                int32_t block_size, uint32_t *device_status, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * 8-bit block-scaled KV pool.
  * [LB] §Qwen3.8-27B DFlash2 on the R9700 (vs llama.cpp) and §DeepSeek V4
  * Flash on Strix Halo and two GPUs: the pages serve from 8-bit and 4-bit KV
