@@ -49,7 +49,14 @@ class WorkInfo(ctypes.Structure):
                 ("work_words", ctypes.c_int64), ("workspace_bytes", ctypes.c_uint64),
                 ("decode_rows_max", ctypes.c_int32), ("num_scratch_items", ctypes.c_int32),
                 ("scratch_blocks", ctypes.c_int64), ("workspace_bytes_q8", ctypes.c_uint64),
-                ("num_long_combine_items", ctypes.c_int32)]
+                ("num_long_combine_items", ctypes.c_int32), ("modified", ctypes.c_int32)]
+
+
+class ScoreModArgs(ctypes.Structure):
+    """``pkv_score_mod``."""
+
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("alibi_slopes", ctypes.c_void_p),
+                ("key_begin", ctypes.c_void_p), ("key_end", ctypes.c_void_p)]
 
 
 class StageLayout(ctypes.Structure):
@@ -125,6 +132,11 @@ def _lib():
             "pkv_cache_write_q4": ([p, p, p, i64, p, p, p, p, i64, i32, i32, i32, p, p], ctypes.c_int),
             "pkv_attention_q4": ([p, p, i32, i64, p, p, p, i32, i32, i32, p, p, p, p, i64, i32, i32, i32, f32, p,
                                   ctypes.POINTER(WorkInfo), p, p, u64, p, p], ctypes.c_int),
+            "pkv_plan_work_mod": ([p, i32, p, p, i32, i32, i32, i32, i32, i32, ctypes.POINTER(ScoreModArgs), p, i64,
+                                   ctypes.POINTER(WorkInfo)], ctypes.c_int),
+            "pkv_attention_mod": ([p, p, i32, i64, p, p, p, i32, i32, i32, p, p, i64, i32, i32, i32, f32,
+                                   ctypes.POINTER(ScoreModArgs), p, ctypes.POINTER(WorkInfo), p, p, u64, p, p],
+                                  ctypes.c_int),
             "pkv_rope_plan": ([ctypes.POINTER(RopeConfig), p, p, ctypes.POINTER(f32)], ctypes.c_int),
             "pkv_rope_phases": ([p, i32, p], ctypes.c_int),
             "pkv_plan_positions": ([p, i32, p, p, i32, p, i64], ctypes.c_int),
@@ -135,6 +147,10 @@ def _lib():
             "pkv_step": ([ctypes.POINTER(StageLayout), p, u64, p, u64, p, p, i64, i32, f32, p, u64, p, p, p, p,
                           ctypes.POINTER(WorkInfo), ctypes.c_uint32], ctypes.c_int),
         }
+        for bits in (8, 4):
+            sig[f"pkv_attention_mod_q{bits}"] = ([p, p, i32, i64, p, p, p, i32, i32, i32, p, p, p, p, i64, i32, i32, i32,
+                                                  f32, ctypes.POINTER(ScoreModArgs), p, ctypes.POINTER(WorkInfo), p, p,
+                                                  u64, p, p], ctypes.c_int)
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
@@ -285,6 +301,30 @@ def pkv_plan_work(cu_seqlens_q, seq_slot, context_lens, *, max_slots: int, max_b
         _check(rc, "pkv_plan_work")
     work = np.zeros(max(info.work_words, PKV_WORK_WORDS_PER_ITEM), np.int32)
     _check(_lib().pkv_plan_work(*args, _np_ptr(work), len(work), ctypes.byref(info)), "pkv_plan_work")
+    return work, info
+
+
+def pkv_plan_work_mod(cu_seqlens_q, seq_slot, context_lens, *, max_slots: int, max_blocks_per_slot: int,
+                      block_size: int, num_q_heads: int, num_kv_heads: int, head_dim: int, window: int = 0,
+                      key_begin=None, key_end=None):
+    """``pkv_plan_work`` for modified scores: (work int32 array, WorkInfo). ``key_begin`` / ``key_end``: int32, one
+    entry per packed row, on the host."""
+    cu = np.ascontiguousarray(cu_seqlens_q, dtype=np.int32)
+    ss = np.ascontiguousarray(seq_slot, dtype=np.int32)
+    cl = np.ascontiguousarray(context_lens, dtype=np.int32)
+    kb, ke = (None if a is None else np.ascontiguousarray(a, dtype=np.int32) for a in (key_begin, key_end))
+    for a, nm in ((kb, "key_begin"), (ke, "key_end")):
+        if a is not None and a.shape != (int(cu[-1]),):
+            raise ValueError(f"{nm} must have one entry per packed row ({int(cu[-1])}), got {a.shape}")
+    mod = ScoreModArgs(0.0, window, None, _np_ptr(kb), _np_ptr(ke))
+    info = WorkInfo()
+    args = (_np_ptr(cu), len(cu) - 1, _np_ptr(ss), _np_ptr(cl), max_slots, max_blocks_per_slot, block_size,
+            num_q_heads, num_kv_heads, head_dim, ctypes.byref(mod))
+    rc = _lib().pkv_plan_work_mod(*args, None, 0, ctypes.byref(info))
+    if rc != PKV_ERR_WORKSPACE_TOO_SMALL:
+        _check(rc, "pkv_plan_work_mod")
+    work = np.zeros(max(info.work_words, PKV_WORK_WORDS_PER_ITEM), np.int32)
+    _check(_lib().pkv_plan_work_mod(*args, _np_ptr(work), len(work), ctypes.byref(info)), "pkv_plan_work_mod")
     return work, info
 
 
@@ -505,6 +545,94 @@ def pkv_rope_cache_write(q, k_new, v_new, positions, phases, slot_mapping, q_out
     """Rotate a step's queries into ``q_out`` and its keys into the pool beside its values, in one pass."""
     RopeCacheWriteCall(q, k_new, v_new, positions, phases, slot_mapping, q_out, k_pool, v_pool, rot_dim=rot_dim,
                        interleaved=interleaved, magnitude=magnitude, device_status=device_status, stream=stream)()
+
+
+@dataclass
+class ScoreMod:
+    """``pkv_score_mod`` on the device: cap, window and, as contiguous CUDA tensors, slopes (float32, one per q head)
+    and the rows' key bounds (int32, one per packed row; the values that ``pkv_plan_work_mod`` saw)."""
+
+    softcap: float = 0.0
+    window: int = 0
+    alibi_slopes: object = None
+    key_begin: object = None
+    key_end: object = None
+
+    def marshal(self, num_q_heads: int, total_q: int) -> ScoreModArgs:
+        for t, nm, dtype, n in ((self.alibi_slopes, "alibi_slopes", "torch.float32", num_q_heads),
+                                (self.key_begin, "key_begin", "torch.int32", total_q),
+                                (self.key_end, "key_end", "torch.int32", total_q)):
+            if t is not None:
+                _need(t, dtype, nm)
+                if t.numel() != n:
+                    raise ValueError(f"{nm} must hold {n} values, got {t.numel()}")
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        return ScoreModArgs(float(self.softcap), int(self.window), ptr(self.alibi_slopes), ptr(self.key_begin),
+                            ptr(self.key_end))
+
+
+class AttentionModCall(_BoundCall):
+    """``pkv_attention_mod`` (``kv="bf16"``, ``pool`` = (k_pool, v_pool)) or ``pkv_attention_mod_q8`` / ``_q4``
+    (``kv="q8"`` / ``"q4"``, ``pool`` = (k_codes, k_scales, v_codes, v_scales)) bound once."""
+
+    def __init__(self, q, cu_seqlens_q, seq_slot, context_lens, block_tables, pool, work, info: WorkInfo, out,
+                 workspace=None, *, mod: ScoreMod, kv: str = "bf16", scale: float = 0.0, device_status=None, stream=None):
+        _need(q, "torch.bfloat16", "q")
+        _need(out, "torch.bfloat16", "out")
+        if q.dim() != 3 or out.shape != q.shape:
+            raise ValueError("q and out must be [rows, q heads, head_dim], alike")
+        for t, nm in ((cu_seqlens_q, "cu_seqlens_q"), (seq_slot, "seq_slot"), (context_lens, "context_lens"),
+                      (block_tables, "block_tables"), (work, "work")):
+            _need(t, "torch.int32", nm)
+        if kv not in ("bf16", "q8", "q4") or len(pool) != (2 if kv == "bf16" else 4):
+            raise ValueError(f"a pool is 2 (bf16) or 4 (q8, q4) tensors, got {len(pool)} as {kv!r}")
+        if kv == "bf16":
+            for t, nm in zip(pool, ("k_pool", "v_pool")):
+                _need(t, "torch.bfloat16", nm)
+            nb, hkv, bs, d = pool[0].shape
+            if pool[1].shape != pool[0].shape:
+                raise ValueError("k_pool and v_pool must have one shape")
+        else:
+            nb, hkv, bs, d = _need_quant_pool(*pool, int(kv[1]))
+        ms, mbps = block_tables.shape
+        if q.shape[2] != d:
+            raise ValueError(f"q's head_dim {q.shape[2]} is not the pool's ({d})")
+        if context_lens.numel() != ms or seq_slot.numel() < cu_seqlens_q.numel() - 1:
+            raise ValueError("context_lens must have one entry per slot, seq_slot one per segment")
+        if work.numel() < info.work_words:
+            raise ValueError(f"work holds {work.numel()} words, info names {info.work_words}")
+        args = mod.marshal(q.shape[1], q.shape[0])
+        info = WorkInfo.from_buffer_copy(info)
+        _need_on(q.device, out, cu_seqlens_q, seq_slot, context_lens, block_tables, work, workspace, device_status,
+                 *pool, mod.alibi_slopes, mod.key_begin, mod.key_end)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        self._bind("pkv_attention_mod" + ("" if kv == "bf16" else f"_{kv}"),
+                   (_t_ptr(q), _t_ptr(cu_seqlens_q), cu_seqlens_q.numel() - 1, q.shape[0], _t_ptr(seq_slot),
+                    _t_ptr(context_lens), _t_ptr(block_tables), ms, mbps, bs, *map(_t_ptr, pool), nb, q.shape[1], hkv, d,
+                    float(scale), ctypes.byref(args), _t_ptr(work), ctypes.byref(info), _t_ptr(out), _t_ptr(workspace),
+                    ws_bytes, _t_ptr(device_status)),
+                   (q, cu_seqlens_q, seq_slot, context_lens, block_tables, tuple(pool), work, info, out, workspace, mod,
+                    args, (mod.alibi_slopes, mod.key_begin, mod.key_end), device_status), stream)
+
+
+def pkv_attention_mod(q, cu_seqlens_q, seq_slot, context_lens, block_tables, k_pool, v_pool, work, info: WorkInfo, out,
+                      workspace=None, *, mod: ScoreMod, scale: float = 0.0, device_status=None, stream=None) -> None:
+    AttentionModCall(q, cu_seqlens_q, seq_slot, context_lens, block_tables, (k_pool, v_pool), work, info, out, workspace,
+                     mod=mod, scale=scale, device_status=device_status, stream=stream)()
+
+
+def pkv_attention_mod_q8(q, cu_seqlens_q, seq_slot, context_lens, block_tables, k_codes, k_scales, v_codes, v_scales,
+                         work, info: WorkInfo, out, workspace=None, *, mod: ScoreMod, scale: float = 0.0,
+                         device_status=None, stream=None) -> None:
+    AttentionModCall(q, cu_seqlens_q, seq_slot, context_lens, block_tables, (k_codes, k_scales, v_codes, v_scales), work,
+                     info, out, workspace, mod=mod, kv="q8", scale=scale, device_status=device_status, stream=stream)()
+
+
+def pkv_attention_mod_q4(q, cu_seqlens_q, seq_slot, context_lens, block_tables, k_codes, k_scales, v_codes, v_scales,
+                         work, info: WorkInfo, out, workspace=None, *, mod: ScoreMod, scale: float = 0.0,
+                         device_status=None, stream=None) -> None:
+    AttentionModCall(q, cu_seqlens_q, seq_slot, context_lens, block_tables, (k_codes, k_scales, v_codes, v_scales), work,
+                     info, out, workspace, mod=mod, kv="q4", scale=scale, device_status=device_status, stream=stream)()
 
 
 def _need_quant_pool(k_codes, k_scales, v_codes, v_scales, bits: int):

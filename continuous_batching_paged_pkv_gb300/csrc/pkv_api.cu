@@ -130,6 +130,24 @@ bool encode_q(CUtensorMap *m, const void *q, int64_t total_q, int32_t hq, int32_
 
 uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
+// Scores' modification and a work list made with (or without) one.
+bool bad_mod(const pkv_score_mod *mod, const pkv_work_info *info) {
+  if (info->modified != (mod ? 1 : 0)) return true;
+  if (!mod) return false;
+  return !(mod->softcap >= 0.f) || std::isinf(mod->softcap) || mod->window < 0 || !aligned(mod->alibi_slopes, 4) ||
+         !aligned(mod->key_begin, 4) || !aligned(mod->key_end, 4);
+}
+
+void set_mod(pkv::StepArgs &a, const pkv_score_mod *mod) {
+  if (!mod) return;
+  a.modified = 1;
+  a.softcap = mod->softcap;
+  a.window = mod->window;
+  a.alibi_slopes = mod->alibi_slopes;
+  a.key_begin = mod->key_begin;
+  a.key_end = mod->key_end;
+}
+
 }  // namespace
 
 extern "C" {
@@ -171,7 +189,7 @@ pkv_status pkv::attention(const void *q, const int32_t *cu_seqlens_q, int32_t nu
                           const void *v_pool, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
                           int32_t head_dim, float scale, const int32_t *work, const pkv_work_info *info, void *out,
                           void *workspace, uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream,
-                          bool out_on_host) {
+                          bool out_on_host, const pkv_score_mod *mod) {
   if (!info || num_seqs < 0 || total_q < 0 || max_slots <= 0 || max_blocks_per_slot <= 0 || num_blocks <= 0)
     return PKV_ERR_INVALID_ARG;
   if (!supported_shape(block_size, num_q_heads, num_kv_heads, head_dim)) return PKV_ERR_UNSUPPORTED;
@@ -183,6 +201,7 @@ pkv_status pkv::attention(const void *q, const int32_t *cu_seqlens_q, int32_t nu
       info->num_scratch_items < 0 || info->num_partials < 0 ||
       info->work_words != items * PKV_WORK_WORDS_PER_ITEM)
     return PKV_ERR_INVALID_ARG;
+  if (bad_mod(mod, info)) return PKV_ERR_INVALID_ARG;
   if (items == 0 || total_q == 0) return PKV_OK;
   if (!q || !cu_seqlens_q || !seq_slot || !context_lens || !block_tables || !k_pool || !v_pool || !work || !out)
     return PKV_ERR_INVALID_ARG;
@@ -221,6 +240,7 @@ pkv_status pkv::attention(const void *q, const int32_t *cu_seqlens_q, int32_t nu
   a.group = num_q_heads / num_kv_heads;
   a.head_dim = head_dim;
   a.decode_rows_max = info->decode_rows_max;
+  set_mod(a, mod);
   const float s = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
   a.scale_log2 = s * 1.4426950408889634f;
   a.work = work;
@@ -232,6 +252,10 @@ pkv_status pkv::attention(const void *q, const int32_t *cu_seqlens_q, int32_t nu
   a.task_counter =
       need ? reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + acc_bytes + ml_bytes) : nullptr;
 
+  if (mod) {
+    const cudaError_t e = pkv::launch_score_mod(a, nullptr, nullptr, 16, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  }
   CUtensorMap tk, tv, tq, tks;
   if (!encode_pool(&tk, k_pool, rows, head_dim) || !encode_pool(&tv, v_pool, rows, head_dim))
     return PKV_ERR_CUDA;
@@ -333,7 +357,8 @@ static pkv_status attention_quant(int32_t bits, const void *q, const int32_t *cu
                                   const int8_t *v_codes, const void *v_scales, int64_t num_blocks,
                                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
                                   const int32_t *work, const pkv_work_info *info, void *out, void *workspace,
-                                  uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream) {
+                                  uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream,
+                                  const pkv_score_mod *mod = nullptr) {
   if (!info || num_seqs < 0 || total_q < 0 || max_slots <= 0 || max_blocks_per_slot <= 0 || num_blocks <= 0)
     return PKV_ERR_INVALID_ARG;
   if (!supported_shape(block_size, num_q_heads, num_kv_heads, head_dim) || (bits == 4 && head_dim != 128))
@@ -347,6 +372,7 @@ static pkv_status attention_quant(int32_t bits, const void *q, const int32_t *cu
       info->work_words != items * PKV_WORK_WORDS_PER_ITEM ||
       (info->num_prefill_items > 0) != (info->num_scratch_items > 0))
     return PKV_ERR_INVALID_ARG;
+  if (bad_mod(mod, info)) return PKV_ERR_INVALID_ARG;
   if (items == 0 || total_q == 0) return PKV_OK;
   if (!q || !cu_seqlens_q || !seq_slot || !context_lens || !block_tables || !k_codes || !v_codes || !k_scales ||
       !v_scales || !work || !out)
@@ -391,6 +417,7 @@ static pkv_status attention_quant(int32_t bits, const void *q, const int32_t *cu
   a.group = num_q_heads / num_kv_heads;
   a.head_dim = head_dim;
   a.decode_rows_max = info->decode_rows_max;
+  set_mod(a, mod);
   const float s = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
   a.scale_log2 = s * 1.4426950408889634f;
   a.work = work;
@@ -401,6 +428,11 @@ static pkv_status attention_quant(int32_t bits, const void *q, const int32_t *cu
   a.status = device_status;
   a.task_counter = info->num_partials ? reinterpret_cast<uint32_t *>(ws + acc_bytes + ml_bytes) : nullptr;
 
+  if (mod) {
+    const cudaError_t e =
+        pkv::launch_score_mod(a, k_scales, v_scales, bits, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  }
   // The chunk kernel reads a bf16 scratch pool: the chunk segments' histories,
   // widened block by block, with a scratch block table in the same shape.
   pkv::StepArgs c = a;
@@ -484,6 +516,50 @@ pkv_status pkv_attention_q4(const void *q, const int32_t *cu_seqlens_q, int32_t 
                          max_blocks_per_slot, block_size, reinterpret_cast<const int8_t *>(k_codes), k_scales,
                          reinterpret_cast<const int8_t *>(v_codes), v_scales, num_blocks, num_q_heads, num_kv_heads,
                          head_dim, scale, work, info, out, workspace, workspace_bytes, device_status, stream);
+}
+
+pkv_status pkv_attention_mod(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                             const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                             int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size, const void *k_pool,
+                             const void *v_pool, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                             int32_t head_dim, float scale, const pkv_score_mod *mod, const int32_t *work,
+                             const pkv_work_info *info, void *out, void *workspace, uint64_t workspace_bytes,
+                             uint32_t *device_status, pkv_stream_t stream) {
+  if (!mod) return PKV_ERR_INVALID_ARG;
+  return pkv::attention(q, cu_seqlens_q, num_seqs, total_q, seq_slot, context_lens, block_tables, max_slots,
+                        max_blocks_per_slot, block_size, k_pool, v_pool, num_blocks, num_q_heads, num_kv_heads,
+                        head_dim, scale, work, info, out, workspace, workspace_bytes, device_status, stream, false,
+                        mod);
+}
+
+pkv_status pkv_attention_mod_q8(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                                const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                                int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size,
+                                const int8_t *k_codes, const void *k_scales, const int8_t *v_codes,
+                                const void *v_scales, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float scale, const pkv_score_mod *mod, const int32_t *work,
+                                const pkv_work_info *info, void *out, void *workspace, uint64_t workspace_bytes,
+                                uint32_t *device_status, pkv_stream_t stream) {
+  if (!mod) return PKV_ERR_INVALID_ARG;
+  return attention_quant(8, q, cu_seqlens_q, num_seqs, total_q, seq_slot, context_lens, block_tables, max_slots,
+                         max_blocks_per_slot, block_size, k_codes, k_scales, v_codes, v_scales, num_blocks,
+                         num_q_heads, num_kv_heads, head_dim, scale, work, info, out, workspace, workspace_bytes,
+                         device_status, stream, mod);
+}
+
+pkv_status pkv_attention_mod_q4(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                                const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                                int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size,
+                                const uint8_t *k_codes, const void *k_scales, const uint8_t *v_codes,
+                                const void *v_scales, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float scale, const pkv_score_mod *mod, const int32_t *work,
+                                const pkv_work_info *info, void *out, void *workspace, uint64_t workspace_bytes,
+                                uint32_t *device_status, pkv_stream_t stream) {
+  if (!mod) return PKV_ERR_INVALID_ARG;
+  return attention_quant(4, q, cu_seqlens_q, num_seqs, total_q, seq_slot, context_lens, block_tables, max_slots,
+                         max_blocks_per_slot, block_size, reinterpret_cast<const int8_t *>(k_codes), k_scales,
+                         reinterpret_cast<const int8_t *>(v_codes), v_scales, num_blocks, num_q_heads, num_kv_heads,
+                         head_dim, scale, work, info, out, workspace, workspace_bytes, device_status, stream, mod);
 }
 
 pkv_status pkv_check_device_status(uint32_t *device_status, pkv_stream_t stream, uint32_t *bits_out) {

@@ -339,15 +339,41 @@ pkv_status pkv_plan_lower(pkv_pool *p, const pkv_segment *plan, int32_t num_segm
   return PKV_OK;
 }
 
-pkv_status pkv_plan_work(const int32_t *cu, int32_t num_seqs, const int32_t *seq_slot,
-                         const int32_t *context_lens, int32_t max_slots,
-                         int32_t max_blocks_per_slot, int32_t block_size, int32_t num_q_heads,
-                         int32_t num_kv_heads, int32_t head_dim, int32_t *work,
-                         int64_t work_capacity, pkv_work_info *info) {
+}  // extern "C"
+
+namespace {
+
+struct KeyRange {
+  int64_t lo, hi;  // keys [lo, hi); lo >= hi: none
+};
+
+// The keys that some of rows [i0, i1) of a segment sees (packed rows row0 + i,
+// position first + i, context L): pkv_score_mod's bounds, on the host.
+KeyRange rows_see(const pkv_score_mod *mod, int64_t row0, int64_t first, int64_t L, int64_t i0, int64_t i1) {
+  KeyRange u{INT64_MAX, 0};
+  for (int64_t i = i0; i < i1; ++i) {
+    const int64_t p = first + i;
+    int64_t lo = mod->key_begin ? std::max<int64_t>(0, mod->key_begin[row0 + i]) : 0;
+    if (mod->window > 0) lo = std::max<int64_t>(lo, p - mod->window + 1);
+    const int64_t hi = mod->key_end ? std::min<int64_t>(L, mod->key_end[row0 + i]) : p + 1;
+    if (lo >= hi) continue;
+    u.lo = std::min(u.lo, lo);
+    u.hi = std::max(u.hi, hi);
+  }
+  if (u.lo >= u.hi) u = {0, 0};
+  return u;
+}
+
+// The work list of a step: of pkv_plan_work without `mod`, of pkv_plan_work_mod with it.
+pkv_status plan_work(const int32_t *cu, int32_t num_seqs, const int32_t *seq_slot, const int32_t *context_lens,
+                     int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size, int32_t num_q_heads,
+                     int32_t num_kv_heads, int32_t head_dim, const pkv_score_mod *mod, int32_t *work,
+                     int64_t work_capacity, pkv_work_info *info) {
   if (!info || num_seqs < 0 || !cu || (num_seqs > 0 && (!seq_slot || !context_lens)) ||
       max_slots <= 0 || max_blocks_per_slot <= 0)
     return PKV_ERR_INVALID_ARG;
   std::memset(info, 0, sizeof(*info));
+  info->modified = mod ? 1 : 0;
   if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0)
     return PKV_ERR_INVALID_ARG;
   const int32_t group = num_q_heads / num_kv_heads;
@@ -391,7 +417,34 @@ pkv_status pkv_plan_work(const int32_t *cu, int32_t num_seqs, const int32_t *seq
     if (static_cast<int64_t>(L) > static_cast<int64_t>(max_blocks_per_slot) * block_size)
       return PKV_ERR_OUT_OF_RANGE;
     if (n == 0) continue;
-    if (n <= decode_rows) {
+    if (mod && n <= decode_rows) {
+      // Spans that hold a key some row sees, each with its first sub-tile and
+      // its sub-tiles; the partial entry of (span, row i) is word 3 + i.
+      const KeyRange u = rows_see(mod, cu[s], static_cast<int64_t>(L) - n, L, 0, n);
+      if (u.hi == 0) {
+        dec_short.push_back({{s, slot, 0, -1}, 0});
+      } else {
+        const int64_t sp0 = u.lo / PKV_SPLIT_KEYS, sp1 = (u.hi - 1) / PKV_SPLIT_KEYS;
+        const int32_t spans = static_cast<int32_t>(sp1 - sp0 + 1);
+        if (sp1 >= (1 << 23) || spans >= (1 << 16)) return PKV_ERR_UNSUPPORTED;
+        if (static_cast<int64_t>(partials) + static_cast<int64_t>(spans) * n > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+        for (int64_t sp = sp0; sp <= sp1; ++sp) {
+          const int64_t k0 = std::max(u.lo, sp * PKV_SPLIT_KEYS) / pkv::kSubKeys;
+          const int64_t k1 = ceil_div(std::min(u.hi, (sp + 1) * PKV_SPLIT_KEYS), pkv::kSubKeys);
+          const uint32_t sub = PKV_SPLIT_KEYS / pkv::kSubKeys;
+          const uint32_t w = static_cast<uint32_t>(sp) | (static_cast<uint32_t>(k0) % sub) << 23 |
+                             static_cast<uint32_t>(k1 - k0) << 27;
+          const int32_t first = spans > 1 ? partials + static_cast<int32_t>(sp - sp0) * n : -1;
+          (k1 - k0 == sub ? dec : dec_short).push_back({{s, slot, static_cast<int32_t>(w), first}, k1 - k0});
+        }
+        if (spans > 1) {
+          for (int32_t i = 0; i < n; ++i)
+            comb.push_back({{s, slot, spans | (i << 16) | ((n - 1) << 24), partials + i}, spans});
+          partials += spans * n;
+        }
+      }
+      rows_max = std::max(rows_max, n);
+    } else if (n <= decode_rows) {
       // Partial entry of (span sp, row i): base + sp * n + i. One merge item per
       // row: spans | row << 16 | (n - 1) << 24, and that row's first entry.
       const int32_t spans = static_cast<int32_t>(ceil_div(L, PKV_SPLIT_KEYS));
@@ -408,10 +461,14 @@ pkv_status pkv_plan_work(const int32_t *cu, int32_t num_seqs, const int32_t *seq
       }
       rows_max = std::max(rows_max, n);
     } else {
-      // The 8-bit pool's chunk path first widens the segment's whole history
-      // into scratch blocks [first, first + blocks) of a bf16 scratch pool.
-      const int64_t nblk = ceil_div(L, block_size);
-      scr.push_back({{s, slot, static_cast<int32_t>(scratch_blocks), static_cast<int32_t>(nblk)}, 0});
+      // The 8-bit pool's chunk path first widens the segment's whole history (with
+      // modified scores: the blocks some row sees) into scratch blocks [first,
+      // first + blocks) of a bf16 scratch pool.
+      const int64_t pos0 = static_cast<int64_t>(L) - n;
+      const KeyRange all = mod ? rows_see(mod, cu[s], pos0, L, 0, n) : KeyRange{0, L};
+      const int64_t blk0 = all.lo / block_size, nblk = ceil_div(all.hi, block_size) - blk0;
+      scr.push_back({{s, mod ? static_cast<int32_t>(blk0) : slot, static_cast<int32_t>(scratch_blocks),
+                      static_cast<int32_t>(nblk)}, 0});
       scratch_blocks += nblk;
       if (scratch_blocks > INT32_MAX) return PKV_ERR_UNSUPPORTED;
       // head_dim 128 runs tiles in pairs on two SMs (the second may be past the segment's end).
@@ -420,10 +477,14 @@ pkv_status pkv_plan_work(const int32_t *cu, int32_t num_seqs, const int32_t *seq
       for (int32_t t = 0; t < tiles; t += step) {
         const int32_t count = std::min(step, tiles - t);
         const int64_t last_row = std::min<int64_t>(n, static_cast<int64_t>(t + count) * rows_per_tile);
-        pre.push_back({{s, slot, t, count}, L - n + last_row});
+        const KeyRange u = mod ? rows_see(mod, cu[s], pos0, L, static_cast<int64_t>(t) * rows_per_tile, last_row)
+                               : KeyRange{0, pos0 + last_row};
+        pre.push_back({{s, slot, t, count}, u.hi - u.lo});
       }
     }
   }
+  // The scratch pool of a step whose chunk rows all see nothing keeps one block, so that it can be described.
+  if (!scr.empty() && scratch_blocks == 0) scratch_blocks = 1;
   // Longest first, ties in their original order: the long items start early
   // and the short tails fill in behind them.
   auto by_cost = [](const Item &a, const Item &b) { return a.cost > b.cost; };
@@ -466,6 +527,28 @@ pkv_status pkv_plan_work(const int32_t *cu, int32_t num_seqs, const int32_t *seq
       w += PKV_WORK_WORDS_PER_ITEM;
     }
   return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_plan_work(const int32_t *cu, int32_t num_seqs, const int32_t *seq_slot,
+                         const int32_t *context_lens, int32_t max_slots,
+                         int32_t max_blocks_per_slot, int32_t block_size, int32_t num_q_heads,
+                         int32_t num_kv_heads, int32_t head_dim, int32_t *work,
+                         int64_t work_capacity, pkv_work_info *info) {
+  return plan_work(cu, num_seqs, seq_slot, context_lens, max_slots, max_blocks_per_slot, block_size, num_q_heads,
+                   num_kv_heads, head_dim, nullptr, work, work_capacity, info);
+}
+
+pkv_status pkv_plan_work_mod(const int32_t *cu, int32_t num_seqs, const int32_t *seq_slot,
+                             const int32_t *context_lens, int32_t max_slots, int32_t max_blocks_per_slot,
+                             int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                             const pkv_score_mod *mod, int32_t *work, int64_t work_capacity, pkv_work_info *info) {
+  if (!mod || mod->window < 0) return PKV_ERR_INVALID_ARG;
+  return plan_work(cu, num_seqs, seq_slot, context_lens, max_slots, max_blocks_per_slot, block_size, num_q_heads,
+                   num_kv_heads, head_dim, mod, work, work_capacity, info);
 }
 
 }  // extern "C"

@@ -47,17 +47,24 @@ struct StepArgs {
   // which the host link carries at its copy rate (one 16-byte piece of 32
   // different rows per store it carries far slower).
   int32_t out_on_host;
+  // Modified scores (pkv_score_mod; all zero for plain attention).
+  int32_t modified;
+  float softcap;
+  int32_t window;
+  const float *alibi_slopes;
+  const int32_t *key_begin, *key_end;
 };
 
 // pkv_attention with the output's location: out_on_host marks `out` as host
 // memory (pkv_step's output written straight to the caller's host buffer).
+// `mod`: the scores' modification (pkv_attention_mod), or nullptr.
 pkv_status attention(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
                      const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
                      int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size, const void *k_pool,
                      const void *v_pool, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
                      int32_t head_dim, float scale, const int32_t *work, const pkv_work_info *info, void *out,
                      void *workspace, uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream,
-                     bool out_on_host);
+                     bool out_on_host, const pkv_score_mod *mod = nullptr);
 
 // Rows of more spans than this are merged with four lanes per column.
 constexpr int kLongMergeSpans = 64;
@@ -115,6 +122,10 @@ cudaError_t launch_widen_quant(const StepArgs &a, const void *k_codes, const voi
                             const void *v_scales, void *k_out, void *v_out, int32_t *scratch_table,
                             int64_t scratch_blocks, int32_t num_items, const int32_t *items, int32_t bits,
                             cudaStream_t stream);
+
+// Attention with modified scores, pool of `bits` (16: bf16) with its scales, every row of the step.
+cudaError_t launch_score_mod(const StepArgs &a, const void *k_scales, const void *v_scales, int32_t bits,
+                             cudaStream_t stream);
 
 cudaError_t launch_prefill(const StepArgs &a, const CUtensorMap &tmap_q, int32_t rows_per_tile,
                            int32_t num_items, const int32_t *items, cudaStream_t stream);

@@ -46,6 +46,16 @@ def _i64(a, device):
     return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int64)).to(device)
 
 
+def _score_mod(mod: B.ScoreMod, device) -> B.ScoreMod:
+    """The same modification with its host arrays on the device."""
+    import torch
+
+    slopes = None if mod.alibi_slopes is None else torch.from_numpy(
+        np.ascontiguousarray(mod.alibi_slopes, dtype=np.float32)).to(device)
+    begin, end = (None if a is None else _i32(a, device) for a in (mod.key_begin, mod.key_end))
+    return B.ScoreMod(mod.softcap, mod.window, slopes, begin, end)
+
+
 def empty_pool(num_blocks, num_kv_heads, block_size, head_dim, device):
     import torch
 
@@ -97,17 +107,20 @@ class DeviceStep:
     kv: str = "bf16"          # pool format: "bf16", "q8" or "q4" (k_pool/v_pool hold the codes)
     k_scales: object = None
     v_scales: object = None
+    mod: B.ScoreMod | None = None  # modified scores (the work list is then pkv_plan_work_mod's)
 
     @property
     def scale(self) -> float:
         return self.w.scale
 
 
-def prepare(w, device="cuda", *, pools=None, kv: str = "bf16") -> DeviceStep:
+def prepare(w, device="cuda", *, pools=None, kv: str = "bf16", mod: B.ScoreMod | None = None) -> DeviceStep:
     """Build the pool state before the step and upload the step's inputs.
 
     ``kv="q8"`` / ``kv="q4"`` keep the pool in the 8-bit / 4-bit block-scaled
-    format (history written through ``pkv_cache_write_q8`` / ``_q4``)."""
+    format (history written through ``pkv_cache_write_q8`` / ``_q4``). ``mod``:
+    modified scores, its arrays still on the host (numpy); the step's attention
+    is then ``pkv_attention_mod`` / ``_q8`` / ``_q4``."""
     import torch
 
     pool = B.Pool(w.num_blocks, w.block_size, w.max_slots, w.max_blocks_per_slot)
@@ -139,9 +152,14 @@ def prepare(w, device="cuda", *, pools=None, kv: str = "bf16") -> DeviceStep:
                               k_pool, v_pool, device_status=status)
 
     low = pool.lower([(s.slot, s.q_len) for s in w.segments])
-    work, info = B.pkv_plan_work(low.cu_seqlens_q, low.seq_slot, low.context_lens, max_slots=w.max_slots,
-                                 max_blocks_per_slot=w.max_blocks_per_slot, block_size=w.block_size,
-                                 num_q_heads=w.num_q_heads, num_kv_heads=w.num_kv_heads, head_dim=w.head_dim)
+    shape = dict(max_slots=w.max_slots, max_blocks_per_slot=w.max_blocks_per_slot, block_size=w.block_size,
+                 num_q_heads=w.num_q_heads, num_kv_heads=w.num_kv_heads, head_dim=w.head_dim)
+    if mod is None:
+        work, info = B.pkv_plan_work(low.cu_seqlens_q, low.seq_slot, low.context_lens, **shape)
+    else:
+        work, info = B.pkv_plan_work_mod(low.cu_seqlens_q, low.seq_slot, low.context_lens, window=mod.window,
+                                         key_begin=mod.key_begin, key_end=mod.key_end, **shape)
+        mod = _score_mod(mod, device)
     ws = None
     ws_bytes = int(info.workspace_bytes_q8 if kv in ("q8", "q4") else info.workspace_bytes)
     if ws_bytes:
@@ -154,7 +172,7 @@ def prepare(w, device="cuda", *, pools=None, kv: str = "bf16") -> DeviceStep:
         slot_mapping=_i64(low.slot_mapping, device), cu_seqlens_q=_i32(low.cu_seqlens_q, device),
         seq_slot=_i32(low.seq_slot, device), context_lens=_i32(low.context_lens, device),
         block_tables=_i32(pool.block_tables(), device), work=_i32(work, device), info=info, workspace=ws,
-        out=out, status=status, kv=kv, k_scales=k_scales, v_scales=v_scales)
+        out=out, status=status, kv=kv, k_scales=k_scales, v_scales=v_scales, mod=mod)
 
 
 def run_cache_write(ds: DeviceStep, stream=None) -> None:
@@ -168,7 +186,12 @@ def run_cache_write(ds: DeviceStep, stream=None) -> None:
 
 
 def run_attention(ds: DeviceStep, stream=None) -> None:
-    if ds.kv in ("q8", "q4"):
+    if ds.mod is not None:
+        attend = {"bf16": B.pkv_attention_mod, "q8": B.pkv_attention_mod_q8, "q4": B.pkv_attention_mod_q4}[ds.kv]
+        pool = (ds.k_pool, ds.v_pool) if ds.kv == "bf16" else (ds.k_pool, ds.k_scales, ds.v_pool, ds.v_scales)
+        attend(ds.q, ds.cu_seqlens_q, ds.seq_slot, ds.context_lens, ds.block_tables, *pool, ds.work, ds.info, ds.out,
+               ds.workspace, mod=ds.mod, scale=ds.scale, device_status=ds.status, stream=stream)
+    elif ds.kv in ("q8", "q4"):
         attend = B.pkv_attention_q8 if ds.kv == "q8" else B.pkv_attention_q4
         attend(ds.q, ds.cu_seqlens_q, ds.seq_slot, ds.context_lens, ds.block_tables, ds.k_pool, ds.k_scales,
                ds.v_pool, ds.v_scales, ds.work, ds.info, ds.out, ds.workspace, scale=ds.scale,

@@ -261,6 +261,7 @@ typedef struct pkv_work_info {
     int64_t scratch_blocks;    /* bf16 scratch blocks those items widen the chunks' histories into */
     uint64_t workspace_bytes_q8; /* device workspace pkv_attention_q8 needs (may be 0) */
     int32_t num_long_combine_items; /* the first merge items, whose rows have more than 64 spans */
+    int32_t modified;               /* 1: a list of pkv_plan_work_mod, for pkv_attention_mod and its kin alone */
 } pkv_work_info;
 
 /*
@@ -586,6 +587,91 @@ pkv_status pkv_attention_q4(const void *q, const int32_t *cu_seqlens_q, int32_t 
                             int32_t head_dim, float scale, const int32_t *work, const pkv_work_info *info,
                             void *out, void *workspace, uint64_t workspace_bytes, uint32_t *device_status,
                             pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention with modified scores. The pages leave the scores to the model;
+ * models cap them, bias them by distance or let a row see only part of its
+ * slot's history. Row i of segment s (n rows, slot c, L = context_lens[c])
+ * sits at position p = L - n + i, as in pkv_attention; packed row r =
+ * cu_seqlens_q[s] + i, q head h. With x_j = scale * q . k_j for key j:
+ *   softcap > 0       x_j = softcap * tanh(x_j / softcap)
+ *   alibi_slopes      x_j = x_j - alibi_slopes[h] * |p - j|      (after the cap)
+ *   the row sees key j when first <= j < last, with
+ *     first = max(0, key_begin[r], p - window + 1)   (the parts that are given)
+ *     last  = min(L, key_end[r]), or p + 1 (causal) without key_end
+ *   softmax over the keys it sees; a row that sees none gives zeros.
+ * window: a sliding window of `window` keys, the row's own among them (local
+ * layers). key_begin: documents packed behind one another in one slot (each
+ * row's document's first position). key_end: a bidirectional prefix (the
+ * larger of p + 1 and the prefix's length), or 0 for padding rows. Keys that no
+ * row of a segment sees are not read, at the granularity of 16 keys: their
+ * blocks may have been given back, and their table entries may be anything. A
+ * key or value that is not finite reaches the rows that see it, and through
+ * 0 * infinity may reach other rows of the same segment; one that no row of
+ * the segment's tile sees reaches none.
+ * ---------------------------------------------------------------------- */
+typedef struct pkv_score_mod {
+    float softcap;             /* 0: none; else finite and > 0 */
+    int32_t window;            /* 0: none; else >= 1 */
+    const float *alibi_slopes; /* float [num_q_heads], or NULL; finite */
+    const int32_t *key_begin;  /* int32 [total_q], or NULL */
+    const int32_t *key_end;    /* int32 [total_q], or NULL */
+} pkv_score_mod;
+
+/*
+ * pkv_plan_work for a step whose rows see only the keys that `mod` leaves them
+ * (key_begin and key_end are HOST copies here; softcap and alibi_slopes are
+ * not looked at). The key spans of the decode path and the tiles of the chunk
+ * path cover the keys that some row of the segment (of the tile pair) sees,
+ * and nothing else; spans stay cut at multiples of PKV_SPLIT_KEYS. Same
+ * validation, sizes and errors as pkv_plan_work, and PKV_ERR_INVALID_ARG for a
+ * negative window. info->modified is 1.
+ *
+ * Item words: decode (segment, slot, span | first 16-key sub-tile << 23 |
+ * sub-tiles << 27 (0: the segment sees nothing), the span's first partial or
+ * -1); prefill and merge as for pkv_plan_work (merge: the spans that are in the
+ * list); scratch (segment, first logical block, first scratch block, blocks).
+ */
+pkv_status pkv_plan_work_mod(const int32_t *cu_seqlens_q, int32_t num_seqs, const int32_t *seq_slot,
+                             const int32_t *context_lens, int32_t max_slots, int32_t max_blocks_per_slot,
+                             int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                             const pkv_score_mod *mod, int32_t *work, int64_t work_capacity, pkv_work_info *info);
+
+/*
+ * pkv_attention with modified scores: same arguments, results, workspace and
+ * ordering rules, but for `mod` (its pointers are device memory, with the
+ * values that pkv_plan_work_mod saw) and a work list and info from
+ * pkv_plan_work_mod. A row whose bounds reach past the keys that the list
+ * covers sets PKV_DEV_BAD_SEGMENT (decode path).
+ */
+pkv_status pkv_attention_mod(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                             const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                             int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size, const void *k_pool,
+                             const void *v_pool, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                             int32_t head_dim, float scale, const pkv_score_mod *mod, const int32_t *work,
+                             const pkv_work_info *info, void *out, void *workspace, uint64_t workspace_bytes,
+                             uint32_t *device_status, pkv_stream_t stream);
+
+/* pkv_attention_mod over an 8-bit pool, as pkv_attention_q8 is to pkv_attention (chunks widen only the blocks
+ * that some row of the segment sees). */
+pkv_status pkv_attention_mod_q8(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                                const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                                int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size,
+                                const int8_t *k_codes, const void *k_scales, const int8_t *v_codes,
+                                const void *v_scales, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float scale, const pkv_score_mod *mod, const int32_t *work,
+                                const pkv_work_info *info, void *out, void *workspace, uint64_t workspace_bytes,
+                                uint32_t *device_status, pkv_stream_t stream);
+
+/* The same over a 4-bit pool; PKV_ERR_UNSUPPORTED unless head_dim is 128. */
+pkv_status pkv_attention_mod_q4(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                                const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                                int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size,
+                                const uint8_t *k_codes, const void *k_scales, const uint8_t *v_codes,
+                                const void *v_scales, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float scale, const pkv_score_mod *mod, const int32_t *work,
+                                const pkv_work_info *info, void *out, void *workspace, uint64_t workspace_bytes,
+                                uint32_t *device_status, pkv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Host-staged step: a whole step from host memory in one call.
