@@ -252,10 +252,6 @@ pkv_status pkv::attention(const void *q, const int32_t *cu_seqlens_q, int32_t nu
   a.task_counter =
       need ? reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + acc_bytes + ml_bytes) : nullptr;
 
-  if (mod) {
-    const cudaError_t e = pkv::launch_score_mod(a, nullptr, nullptr, 16, reinterpret_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
-  }
   CUtensorMap tk, tv, tq, tks;
   if (!encode_pool(&tk, k_pool, rows, head_dim) || !encode_pool(&tv, v_pool, rows, head_dim))
     return PKV_ERR_CUDA;

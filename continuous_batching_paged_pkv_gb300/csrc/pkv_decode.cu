@@ -45,6 +45,12 @@
 // order. Nothing depends on timing or on other segments: results are
 // deterministic and independent of the rest of the batch.
 //
+// With modified scores (MOD) a work item names the 16-key sub-tiles of its span
+// that some row of the segment sees; each column masks the keys outside its own
+// row's interval, and the logits take the cap and the distance bias before the
+// softmax. A few more instructions per 16-key sub-tile; the kernel stays bound by
+// HBM.
+//
 // Keys past the context in a partly filled block are masked to -inf in S and
 // their V values zeroed in registers, so stale or NaN pool rows never reach
 // the output.
@@ -107,7 +113,7 @@ __device__ __forceinline__ void load_q(uint32_t (&qf)[NT][D / 16][2], const Task
 // sub-tiles is latency-bound (its ring's bytes per HBM round trip), so steps
 // with fewer tasks than warps run fewer warps with deeper rings; the math of
 // a task does not depend on them.
-template <int D, int NT, bool MULTI, int NW, int NS>
+template <int D, int NT, bool MULTI, bool MOD, int NW, int NS>
 __global__ void __launch_bounds__(NW * 32, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const StepArgs a, const int32_t *__restrict__ items, int num_items) {
@@ -147,15 +153,15 @@ __global__ void __launch_bounds__(NW * 32, 1)
   uint32_t *const counter = a.task_counter;
   Task A, B;
   int4 rawC = make_int4(0, 0, 0, 0);
-  expand(A, t0, load_item(items, t0, hkv), a, lane);
+  expand<MOD>(A, t0, load_item(items, t0, hkv), a, lane);
   int tC;
   {
     const int t1 = t0 + stride;
-    expand(B, t1 < num_tasks ? t1 : -1, t1 < num_tasks ? load_item(items, t1, hkv) : rawC, a, lane);
+    expand<MOD>(B, t1 < num_tasks ? t1 : -1, t1 < num_tasks ? load_item(items, t1, hkv) : rawC, a, lane);
     tC = t1 + stride;
     if (tC < num_tasks) rawC = load_item(items, tC, hkv);
   }
-  finalize(A, a, lane, 8 * NT, kMaxRows);
+  finalize<MOD>(A, a, lane, 8 * NT, kMaxRows);
   uint32_t qA[NT][KT][2], qB[NT][KT][2];
   if (A.ok) load_q<D, NT, MULTI>(qA, A, a, lane);
   bool qB_loaded = false;
@@ -196,7 +202,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
     if (B.t >= 0) {
       if (!B.finalized) {
-        finalize(B, a, lane, 8 * NT, kMaxRows);
+        finalize<MOD>(B, a, lane, 8 * NT, kMaxRows);
         if (B.ok) {
           load_q<D, NT, MULTI>(qB, B, a, lane);
           qB_loaded = true;
@@ -231,6 +237,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
   const int ka = lane >> 2, kb = ka + 8, k0 = (lane & 3) * 2;
   int cstage = 0;
   uint32_t cphase = 0;  // (C / NST) & 1
+  const Cap cap(MOD ? a.softcap : 0.f);
+  const bool bias = MOD && a.alibi_slopes;
 
   while (A.t >= 0) {
     // Claim the task after tC now; the answer is needed only when A is done.
@@ -253,7 +261,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     // row and so see every key.
     const int nrows = MULTI ? A.nrows : 1;
     uint32_t colrow = 0;
-    if (MULTI) {
+    if (MULTI && !MOD) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -264,6 +272,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
         }
     }
 
+    TaskMod<NT, MULTI> tm;
+    if constexpr (MOD) tm.set(A, a, lane);
+
     for (int u = 0; u < A.units; ++u) {
       const int stage = cstage;
       if (!mbar_wait(full + stage, cphase)) {
@@ -273,7 +284,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
       const int row = __shfl_sync(kFull, A.row, u);
       const int kbase = A.key0 + u * kSubKeys;
       // keys of the sub-tile that take part (0 for a block ID outside the pool)
-      const int v = row >= 0 ? min(kSubKeys, A.key1 - kbase) : 0;
+      int v = row >= 0 ? min(kSubKeys, A.key1 - kbase) : 0, v0 = 0;
+      if constexpr (MOD) {  // [v0, v): the keys that some row sees
+        v0 = max(0, tm.u_lo - kbase);
+        v = min(v, tm.u_hi - kbase);
+      }
       const int vis0 = A.L - nrows - kbase + 1;  // keys of the sub-tile row 0 sees
       const uint32_t kaddr = ring_addr + stage * Cfg::kStageBytes;
 
@@ -301,10 +316,15 @@ __global__ void __launch_bounds__(NW * 32, 1)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          // causal limit of this column's row (a single row sees the whole span)
-          const int vis = MULTI ? min(v, vis0 + static_cast<int>((colrow >> (8 * (nt * 2 + c))) & 0xFF)) : v;
-          x[nt][c][0] = ka < vis ? (s0[nt][c] + s1[nt][c]) * sl2 : -INFINITY;
-          x[nt][c][1] = kb < vis ? (s0[nt][c + 2] + s1[nt][c + 2]) * sl2 : -INFINITY;
+          if constexpr (MOD) {
+            x[nt][c][0] = tm.logit((s0[nt][c] + s1[nt][c]) * sl2, kbase + ka, nt, c, ka < v, cap, bias);
+            x[nt][c][1] = tm.logit((s0[nt][c + 2] + s1[nt][c + 2]) * sl2, kbase + kb, nt, c, kb < v, cap, bias);
+          } else {
+            // causal limit of this column's row (a single row sees the whole span)
+            const int vis = MULTI ? min(v, vis0 + static_cast<int>((colrow >> (8 * (nt * 2 + c))) & 0xFF)) : v;
+            x[nt][c][0] = ka < vis ? (s0[nt][c] + s1[nt][c]) * sl2 : -INFINITY;
+            x[nt][c][1] = kb < vis ? (s0[nt][c + 2] + s1[nt][c + 2]) * sl2 : -INFINITY;
+          }
           need |= fmaxf(x[nt][c][0], x[nt][c][1]) > m[nt][c] + kRescale;
         }
       if (__any_sync(kFull, need)) {
@@ -345,9 +365,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
       }
 
       // O^T += V^T P^T; V rows of keys that do not take part are zeroed.
-      const bool part = v < kSubKeys;
-      const uint32_t mlo = (k0 < v ? 0x0000FFFFu : 0u) | (k0 + 1 < v ? 0xFFFF0000u : 0u);
-      const uint32_t mhi = (k0 + 8 < v ? 0x0000FFFFu : 0u) | (k0 + 9 < v ? 0xFFFF0000u : 0u);
+      const bool part = v < kSubKeys || (MOD && v0 > 0);
+      auto used = [&](int k) { return k < v && (!MOD || k >= v0); };
+      const uint32_t mlo = (used(k0) ? 0x0000FFFFu : 0u) | (used(k0 + 1) ? 0xFFFF0000u : 0u);
+      const uint32_t mhi = (used(k0 + 8) ? 0x0000FFFFu : 0u) | (used(k0 + 9) ? 0xFFFF0000u : 0u);
 #pragma unroll
       for (int mt = 0; mt < KT; ++mt) {
         uint32_t af[4];
@@ -396,7 +417,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
               const int i = MULTI ? col / G : 0, hh = MULTI ? col % G : col;
               __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) +
                                    ((static_cast<size_t>(A.row0) + i) * a.num_q_heads + hbase) * D + (lane >> 2);
-              const float inv = 1.f / l[nt][c];
+              const float inv = MOD && l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];  // a row that sees nothing gives zeros
 #pragma unroll
               for (int mt = 0; mt < KT; ++mt) {
                 out[static_cast<size_t>(hh) * D + mt * 16] = __float2bfloat16_rn(acc[nt][mt][c] * inv);
@@ -413,7 +434,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             if (col < nrows * G) {
               // partial entry of (span, row i)
               const int i = MULTI ? col / G : 0, hh = MULTI ? col % G : col;
-              const size_t pi = static_cast<size_t>(A.pbase + A.span * nrows + i) * a.num_q_heads + hbase;
+              const size_t pi = static_cast<size_t>(A.pbase + (MOD ? 0 : A.span * nrows) + i) * a.num_q_heads + hbase;
               float *pacc = a.partial_acc + (pi + hh) * D + (lane >> 2);
 #pragma unroll
               for (int mt = 0; mt < KT; ++mt) {
@@ -445,7 +466,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     pa = pb;
     pb = 0;
     if (A.t >= 0) {
-      if (!A.finalized) finalize(A, a, lane, 8 * NT, kMaxRows);
+      if (!A.finalized) finalize<MOD>(A, a, lane, 8 * NT, kMaxRows);
       if (qB_loaded) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -459,7 +480,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       }
     }
     qB_loaded = false;
-    expand(B, next_t < num_tasks ? next_t : -1, rawC, a, lane);
+    expand<MOD>(B, next_t < num_tasks ? next_t : -1, rawC, a, lane);
     tC = after;
     if (tC < num_tasks) rawC = load_item(items, tC, hkv);
     while (P - C < NST && issue_next()) {
@@ -507,7 +528,9 @@ __device__ __forceinline__ MergeRow merge_row(const StepArgs &a, const int32_t *
     const int L = __ldg(a.context_lens + slot);
     r.row = row0 + ri;
     r.bad = __ldg(a.seq_slot + seg) != slot || __ldg(a.cu_seqlens_q + seg + 1) - row0 != r.nrows ||
-            (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS != r.spans || row0 < 0 || row0 + r.nrows > a.total_q ||
+            (a.modified ? (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS < r.spans
+                        : (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS != r.spans) ||
+            row0 < 0 || row0 + r.nrows > a.total_q ||
             r.nrows > L;
   }
   return r;
@@ -533,7 +556,7 @@ __device__ __forceinline__ void add_group(float &lt, float4 &at, float lg, const
 
 template <int D>
 __device__ __forceinline__ void store_merged(const StepArgs &a, int row, int h, int col, float lt, const float4 &at) {
-  const float inv = 1.f / lt;
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;  // 0 only where modified scores leave a row no key
   uint2 packed;
   packed.x = pack_bf16x2(__fmul_rn(at.x, inv), __fmul_rn(at.y, inv));
   packed.y = pack_bf16x2(__fmul_rn(at.z, inv), __fmul_rn(at.w, inv));
@@ -740,12 +763,12 @@ int sm_count() {
   return count[dev];
 }
 
-template <int D, int NT, bool MULTI, int NW = kWarps, int NS = 0>
+template <int D, int NT, bool MULTI, bool MOD, int NW = kWarps, int NS = 0>
 cudaError_t launch_decode_t(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int32_t num_items,
                             const int32_t *items, cudaStream_t stream) {
   constexpr int smem = DecodeCfg<D, NW, NS>::kSmem;
   static std::atomic<uint64_t> configured{0};  // one bit per device
-  if (const cudaError_t e = allow_smem_once(decode_kernel<D, NT, MULTI, NW, NS>, smem, configured);
+  if (const cudaError_t e = allow_smem_once(decode_kernel<D, NT, MULTI, MOD, NW, NS>, smem, configured);
       e != cudaSuccess)
     return e;
   const int64_t tasks = static_cast<int64_t>(num_items) * a.num_kv_heads;
@@ -759,22 +782,47 @@ cudaError_t launch_decode_t(const StepArgs &a, const CUtensorMap &tk, const CUte
   } else {
     b.task_counter = nullptr;
   }
-  return launch_pdl(decode_kernel<D, NT, MULTI, NW, NS>, dim3(grid), dim3(NW * 32), smem, stream, tk, tv, b, items,
+  return launch_pdl(decode_kernel<D, NT, MULTI, MOD, NW, NS>, dim3(grid), dim3(NW * 32), smem, stream, tk, tv, b, items,
                     num_items);
 }
 
 // Single-row decode at head_dim 128: with at most 4, 5 or 6 tasks per SM,
 // 4 warps x 6 stages, 5 x 5 or 6 x 4 (192-200 KiB of rings) keep more bytes
 // in flight per busy warp than 8 x 3.
-template <int NT>
+template <int NT, bool MOD>
 cudaError_t launch_decode_128(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int32_t num_items,
                               const int32_t *items, cudaStream_t stream) {
   const int64_t tasks = static_cast<int64_t>(num_items) * a.num_kv_heads;
   const int64_t per_sm = (tasks + sm_count() - 1) / sm_count();
-  if (per_sm <= 4) return launch_decode_t<128, NT, false, 4, 6>(a, tk, tv, num_items, items, stream);
-  if (per_sm == 5) return launch_decode_t<128, NT, false, 5, 5>(a, tk, tv, num_items, items, stream);
-  if (per_sm == 6) return launch_decode_t<128, NT, false, 6, 4>(a, tk, tv, num_items, items, stream);
-  return launch_decode_t<128, NT, false>(a, tk, tv, num_items, items, stream);
+  if (per_sm <= 4) return launch_decode_t<128, NT, false, MOD, 4, 6>(a, tk, tv, num_items, items, stream);
+  if (per_sm == 5) return launch_decode_t<128, NT, false, MOD, 5, 5>(a, tk, tv, num_items, items, stream);
+  if (per_sm == 6) return launch_decode_t<128, NT, false, MOD, 6, 4>(a, tk, tv, num_items, items, stream);
+  return launch_decode_t<128, NT, false, MOD>(a, tk, tv, num_items, items, stream);
+}
+
+template <bool MOD>
+cudaError_t launch_decode_m(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int32_t num_items,
+                            const int32_t *items, bool beside_chunk, cudaStream_t stream) {
+  // one column per (row, q head) of a segment: 8 columns per tile, 16 at most
+  const bool multi = a.decode_rows_max > 1;
+  const bool wide = a.group * (multi ? a.decode_rows_max : 1) > 8;
+  if (beside_chunk && a.head_dim == 128 && !wide) {
+    // one 8-column tile (at most ~208 registers): small enough to share an SM with a chunk CTA
+    constexpr int W = kDecodeWarpsBesideChunk, S = kDecodeStagesBesideChunk;
+    return multi ? launch_decode_t<128, 1, true, MOD, W, S>(a, tk, tv, num_items, items, stream)
+                 : launch_decode_t<128, 1, false, MOD, W, S>(a, tk, tv, num_items, items, stream);
+  }
+  const int v = (a.head_dim == 128 ? 4 : 0) + (wide ? 2 : 0) + (multi ? 1 : 0);
+  switch (v) {
+    case 0: return launch_decode_t<64, 1, false, MOD>(a, tk, tv, num_items, items, stream);
+    case 1: return launch_decode_t<64, 1, true, MOD>(a, tk, tv, num_items, items, stream);
+    case 2: return launch_decode_t<64, 2, false, MOD>(a, tk, tv, num_items, items, stream);
+    case 3: return launch_decode_t<64, 2, true, MOD>(a, tk, tv, num_items, items, stream);
+    case 4: return launch_decode_128<1, MOD>(a, tk, tv, num_items, items, stream);
+    case 5: return launch_decode_t<128, 1, true, MOD>(a, tk, tv, num_items, items, stream);
+    case 6: return launch_decode_128<2, MOD>(a, tk, tv, num_items, items, stream);
+    default: return launch_decode_t<128, 2, true, MOD>(a, tk, tv, num_items, items, stream);
+  }
 }
 
 }  // namespace
@@ -782,26 +830,8 @@ cudaError_t launch_decode_128(const StepArgs &a, const CUtensorMap &tk, const CU
 cudaError_t launch_decode(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int32_t num_items,
                           const int32_t *items, bool beside_chunk, cudaStream_t stream) {
   if (num_items <= 0) return cudaSuccess;
-  // one column per (row, q head) of a segment: 8 columns per tile, 16 at most
-  const bool multi = a.decode_rows_max > 1;
-  const bool wide = a.group * (multi ? a.decode_rows_max : 1) > 8;
-  if (beside_chunk && a.head_dim == 128 && !wide) {
-    // one 8-column tile (at most ~208 registers): small enough to share an SM with a chunk CTA
-    constexpr int W = kDecodeWarpsBesideChunk, S = kDecodeStagesBesideChunk;
-    return multi ? launch_decode_t<128, 1, true, W, S>(a, tk, tv, num_items, items, stream)
-                 : launch_decode_t<128, 1, false, W, S>(a, tk, tv, num_items, items, stream);
-  }
-  const int v = (a.head_dim == 128 ? 4 : 0) + (wide ? 2 : 0) + (multi ? 1 : 0);
-  switch (v) {
-    case 0: return launch_decode_t<64, 1, false>(a, tk, tv, num_items, items, stream);
-    case 1: return launch_decode_t<64, 1, true>(a, tk, tv, num_items, items, stream);
-    case 2: return launch_decode_t<64, 2, false>(a, tk, tv, num_items, items, stream);
-    case 3: return launch_decode_t<64, 2, true>(a, tk, tv, num_items, items, stream);
-    case 4: return launch_decode_128<1>(a, tk, tv, num_items, items, stream);
-    case 5: return launch_decode_t<128, 1, true>(a, tk, tv, num_items, items, stream);
-    case 6: return launch_decode_128<2>(a, tk, tv, num_items, items, stream);
-    default: return launch_decode_t<128, 2, true>(a, tk, tv, num_items, items, stream);
-  }
+  return a.modified ? launch_decode_m<true>(a, tk, tv, num_items, items, beside_chunk, stream)
+                    : launch_decode_m<false>(a, tk, tv, num_items, items, beside_chunk, stream);
 }
 
 cudaError_t launch_merge(const StepArgs &a, int32_t num_items, int32_t num_long, const int32_t *items,

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "pkv_internal.h"
+#include "pkv_score_mod.cuh"
 
 namespace pkv {
 namespace {
@@ -24,13 +25,18 @@ struct Task {
   int row;  // per lane: tensor-map row of sub-tile `lane`, -1 if its block ID is outside the pool
   bool raw_ok, finalized, ok;
   bool reads_new;  // the span reaches this step's rows (written by the kernel before in the stream)
+  // modified scores only
+  int subs;        // 16-key sub-tiles that the work item names (0: the segment sees nothing)
+  int begin, end;  // per lane: key_begin / key_end of row `lane` as given (finalize issues the loads)
 };
 
 __device__ __forceinline__ int4 load_item(const int32_t *items, int t, int hkv) {
   return __ldg(reinterpret_cast<const int4 *>(items) + t / hkv);
 }
 
-// Issue every load the task needs; nothing here waits for a result.
+// Issue every load the task needs; nothing here waits for a result. MOD:
+// modified scores, whose items name the sub-tiles of the span that some row sees.
+template <bool MOD = false>
 __device__ __forceinline__ void expand(Task &T, int t, int4 raw, const StepArgs &a, int lane) {
   T.t = t;
   T.finalized = false;
@@ -45,7 +51,14 @@ __device__ __forceinline__ void expand(Task &T, int t, int4 raw, const StepArgs 
   T.span = raw.z;
   T.pbase = raw.w;
   T.g = t % a.num_kv_heads;
-  T.key0 = T.span * PKV_SPLIT_KEYS;
+  if constexpr (MOD) {
+    const uint32_t w = static_cast<uint32_t>(raw.z);
+    T.span = static_cast<int>(w & 0x7FFFFFu);
+    T.key0 = T.span * PKV_SPLIT_KEYS + static_cast<int>((w >> 23) & 15u) * kSubKeys;
+    T.subs = static_cast<int>(w >> 27);
+  } else {
+    T.key0 = T.span * PKV_SPLIT_KEYS;
+  }
   T.raw_ok = T.seg >= 0 && T.seg < a.num_seqs && T.slot >= 0 && T.slot < a.max_slots && T.span >= 0;
   if (!T.raw_ok) return;
   T.row0 = __ldg(a.cu_seqlens_q + T.seg);
@@ -53,11 +66,13 @@ __device__ __forceinline__ void expand(Task &T, int t, int4 raw, const StepArgs 
   T.L = __ldg(a.context_lens + T.slot);
   T.sslot = __ldg(a.seq_slot + T.seg);
   const int64_t key = static_cast<int64_t>(T.key0) + lane * kSubKeys;
-  if (lane * kSubKeys < PKV_SPLIT_KEYS && key < static_cast<int64_t>(a.max_blocks_per_slot) * a.block_size)
+  if ((MOD ? lane < T.subs : lane * kSubKeys < PKV_SPLIT_KEYS) &&
+      key < static_cast<int64_t>(a.max_blocks_per_slot) * a.block_size)
     T.bid = __ldg(a.block_tables + static_cast<int64_t>(T.slot) * a.max_blocks_per_slot + key / a.block_size);
 }
 
 // Check the metadata against the work item and derive the key range.
+template <bool MOD = false>
 __device__ __forceinline__ void finalize(Task &T, const StepArgs &a, int lane, int max_cols, int max_rows) {
   if (T.finalized) return;
   T.finalized = true;
@@ -66,18 +81,76 @@ __device__ __forceinline__ void finalize(Task &T, const StepArgs &a, int lane, i
   T.ok = T.raw_ok && T.sslot == T.slot && T.nrows >= 1 && T.nrows <= max_rows && T.nrows * a.group <= max_cols && T.nrows <= T.L &&
          T.L >= 1 &&
          static_cast<int64_t>(T.L) <= static_cast<int64_t>(a.max_blocks_per_slot) * a.block_size &&
-         T.key0 < T.L && T.row0 >= 0 && static_cast<int64_t>(T.row0) + T.nrows <= a.total_q;
+         (T.key0 < T.L || (MOD && T.subs == 0)) && (!MOD || T.subs <= PKV_SPLIT_KEYS / kSubKeys) && T.row0 >= 0 &&
+         static_cast<int64_t>(T.row0) + T.nrows <= a.total_q;
   if (!T.ok) {
     if (lane == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
     return;
   }
-  T.key1 = min(T.L, T.key0 + PKV_SPLIT_KEYS);
+  if constexpr (MOD) {
+    T.key1 = T.subs == 0 ? T.key0 : T.key0 + min(T.L - T.key0, T.subs * kSubKeys);
+    T.begin = lane < T.nrows && a.key_begin ? __ldg(a.key_begin + T.row0 + lane) : 0;
+    T.end = lane < T.nrows && a.key_end ? __ldg(a.key_end + T.row0 + lane) : INT32_MAX;
+  } else {
+    T.key1 = min(T.L, T.key0 + PKV_SPLIT_KEYS);
+  }
   T.units = (T.key1 - T.key0 + kSubKeys - 1) / kSubKeys;
   T.reads_new = T.key1 > T.L - T.nrows;
   const bool in_pool = T.bid >= 0 && T.bid < a.num_blocks;
   T.row = in_pool ? (T.bid * a.num_kv_heads + T.g) * a.block_size + (T.key0 + lane * kSubKeys) % a.block_size : -1;
   if (lane < T.units && !in_pool && a.status) atomicOr(a.status, PKV_DEV_BAD_BLOCK);
 }
+
+// What the columns of a task see and how their scores change, set up when the
+// task becomes current (modified scores). A thread's columns are nt * 8 +
+// 2 (lane % 4) + c, each a (row, q head) pair; a single row needs one interval.
+template <int NT, bool MULTI>
+struct TaskMod {
+  static constexpr int N = MULTI ? NT : 1, C = MULTI ? 2 : 1;
+  int lo[N][C], hi[N][C];  // visible keys [lo, hi) of the column
+  int pos[N][C];           // position of the column's row
+  float slope[NT][2];      // distance bias per key, log2 units
+  int u_lo, u_hi;          // keys that some row of the segment sees
+
+  __device__ __forceinline__ void set(const Task &T, const StepArgs &a, int lane) {
+    const int n = T.ok ? T.nrows : 0;
+    int lo_l = INT32_MAX, hi_l = 0;
+    if (lane < n) {
+      visible_keys(a, T.begin, T.end, T.L - n + lane, T.L, lo_l, hi_l);
+      if (lo_l >= hi_l) lo_l = INT32_MAX, hi_l = 0;
+    }
+    u_lo = __reduce_min_sync(0xffffffffu, lo_l);
+    u_hi = __reduce_max_sync(0xffffffffu, hi_l);
+    // The rows' keys inside the span (all of them, if it is the only one) must be those the item names.
+    const int s0 = T.span * PKV_SPLIT_KEYS;
+    const int need0 = T.pbase < 0 ? u_lo : max(u_lo, s0), need1 = T.pbase < 0 ? u_hi : min(u_hi - s0, PKV_SPLIT_KEYS) + s0;
+    if (T.ok && need0 < need1 && (need0 < T.key0 || need1 > T.key1) && lane == 0 && a.status)
+      atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = nt * 8 + (lane & 3) * 2 + c;
+        const bool valid = col < n * a.group;
+        if (MULTI || (nt == 0 && c == 0)) {
+          const int i = MULTI && valid ? col / a.group : 0;
+          lo[nt][c] = __shfl_sync(0xffffffffu, lo_l, i);
+          hi[nt][c] = __shfl_sync(0xffffffffu, hi_l, i);
+          pos[nt][c] = T.L - n + i;
+        }
+        slope[nt][c] = valid && a.alibi_slopes
+                           ? __ldg(a.alibi_slopes + T.g * a.group + (MULTI ? col % a.group : col)) * 1.4426950408889634f
+                           : 0.f;
+      }
+  }
+  // The logit (log2 units) of the scaled score `x` (log2 units) at key j.
+  __device__ __forceinline__ float logit(float x, int j, int nt, int c, bool loaded, const Cap &cap, bool bias) const {
+    const int i = MULTI ? nt : 0, k = MULTI ? c : 0;
+    if (cap.on) x = cap(x);
+    if (bias) x = fmaf(-slope[nt][c], fabsf(static_cast<float>(pos[i][k] - j)), x);
+    return loaded && j >= lo[i][k] && j < hi[i][k] ? x : -INFINITY;
+  }
+};
 
 }  // namespace
 }  // namespace pkv

@@ -40,6 +40,11 @@
 // The rows past a segment's last tile (an odd tile count) belong to a CTA that
 // still loads its halves and runs the softmax, but stores nothing.
 //
+// With modified scores (MODE) the pair's tiles start at the 16-key sub-tile of
+// the first key that some row sees and end with the last such key; each softmax
+// thread turns its row's scores into capped, biased logits, masks the keys
+// outside its row's interval and starts its running max at its first visible key.
+//
 // TMEM columns (same in both CTAs): [128b, 128b+128) S/P buffer b for b < 3,
 // [384,512) O. Every mbarrier wait is
 // bounded; on expiry the CTA records PKV_DEV_TIMEOUT and both CTAs still meet
@@ -50,6 +55,7 @@
 
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
+#include "pkv_score_mod.cuh"
 
 namespace pkv {
 namespace {
@@ -103,7 +109,7 @@ struct Bars {
   static constexpr int kDrain = kPVDone + kSBufs;      // QK issuer's MMAs complete
   static constexpr int kDrainPV = kDrain + 1;          // PV issuer's MMAs complete
   static constexpr int kNumBars = kDrainPV + 1;
-  static_assert(kNumBars * 8 + 8 <= 256, "barriers, TMEM address and abort flag fit their 256 bytes");
+  static_assert(kNumBars * 8 + 16 <= 256, "barriers, TMEM address, abort flag and key range fit their 256 bytes");
 };
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
@@ -135,7 +141,7 @@ __device__ __forceinline__ bool warp_wait_or_abort(uint64_t *bar, uint32_t parit
   return __all_sync(kFull, wait_or_abort(bar, parity, abort));
 }
 
-template <int NST>
+template <int NST, int MODE>
 __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                                                    const __grid_constant__ CUtensorMap tmap_k,
                                                                    const __grid_constant__ CUtensorMap tmap_v,
@@ -190,8 +196,16 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
   const int pos0 = (present ? tile : tile0) * P;    // first query row of this CTA's tile
   const int rows = present ? min(P, n - pos0) : 0;
   const int last = min(tile0 + 1, q_tiles - 1);     // the pair's last present tile
-  const int kv_end = L - n + min(n, (last + 1) * P);  // keys [0, kv_end) are visible to some row of the pair
-  const int ntiles = (kv_end + kKeysPerTile - 1) / kKeysPerTile;
+  // keys [kv_begin, kv_end) are visible to some row of the pair; tiles start at their first 16-key sub-tile
+  int kv_begin = 0, kv_end = L - n + min(n, (last + 1) * P);
+  if constexpr (MODE != kModNone) {
+    int *u = const_cast<int *>(abort_flag) + 1;
+    rows_see(a, static_cast<int64_t>(row0) + tile0 * P, L - n + tile0 * P, min(n, (last + 1) * P) - tile0 * P, L, u);
+    kv_begin = min(u[0], u[1]);
+    kv_end = u[1];
+  }
+  const int base = kv_begin & ~(kSubKeys - 1);
+  const int ntiles = (kv_end - base + kKeysPerTile - 1) / kKeysPerTile;  // 0: no row of the pair sees a key
   const int32_t *bt_row = a.block_tables + static_cast<int64_t>(slot) * a.max_blocks_per_slot;
 
   if (threadIdx.x == 0) {
@@ -229,11 +243,11 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
     // pool: 0 when outside it, the status word reports it) only when that
     // group comes into use, so no block-table latency is ever waited on.
     auto group_ids = [&](int t0) -> int {
-      const int key = (t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
+      const int key = base + (t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
       return key < kv_end ? __ldg(bt_row + key / a.block_size) : 0;
     };
     auto group_rows = [&](int t0, int blk) -> int {
-      const int key = (t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
+      const int key = base + (t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
       if (key >= kv_end) return 0;
       if (blk < 0 || blk >= a.num_blocks) {
         if (a.status) atomicOr(a.status, PKV_DEV_BAD_BLOCK);
@@ -265,7 +279,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
         rows_cur = group_rows(j, ids_next);
         ids_next = group_ids(j + 4);
       }
-      const int kt0 = j * kKeysPerTile;
+      const int kt0 = base + j * kKeysPerTile;
       const int vs = min(kSubPerTile, (kv_end - kt0 + kSubKeys - 1) / kSubKeys);  // sub-tiles with a visible key
       const uint32_t kv_full = cluster_addr(bar + kKVFull + s, 0);
       // The pair loads 4 boxes per visible sub-tile: two K halves (one CTA) and two V halves (one each).
@@ -273,7 +287,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
       const int urow = __shfl_sync(kFull, rows_cur, (j & 3) * 8 + (u & 7));
       // wait for the kernel before: at the first tile holding rows the cache write appends, or at once
       // when that kernel wrote the whole K/V source
-      if (!waited && (a.kv_from_previous || (j + 1) * kKeysPerTile > L - n)) {
+      if (!waited && (a.kv_from_previous || kt0 + kKeysPerTile > L - n)) {
         grid_dependency_wait();
         waited = true;
       }
@@ -319,7 +333,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
         // P_j written by all eight softmax warps of the pair; V_j has landed (S_j used K_j of the same stage).
         if (!wait_or_abort<true>(bar + kPReady + sp, (j / kSBufs) & 1, abort_flag)) break;
         tc_fence_after();
-        const int valid = min(kKeysPerTile, kv_end - j * kKeysPerTile);
+        const int valid = min(kKeysPerTile, kv_end - base - j * kKeysPerTile);
         const int ksteps = (valid + kSubKeys - 1) / kSubKeys;
         const uint32_t v_base = smem_addr(sKV + (j % kStages) * Lay::kStageBytes + Lay::kKBytes);
         for (int ks = 0; ks < ksteps; ++ks) {
@@ -343,6 +357,13 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
     const int pos = mrow / G;
     const int p_row = L - n + pos0 + pos;  // last visible key of this row (inclusive)
     const float sl2 = a.scale_log2;
+    int lo = 0, hi = 0;  // visible keys of this row (modified scores)
+    float slope = 0.f;   // its bias per key, log2 units
+    const Cap cap((MODE & kModCap) ? a.softcap : 0.f);
+    if constexpr (MODE != kModNone) {
+      if (mrow < G * P && pos < rows) row_sees(a, static_cast<int64_t>(row0) + pos0 + pos, p_row, L, lo, hi);
+      if constexpr ((MODE & kModBias) != 0) slope = __ldg(a.alibi_slopes + g * G + mrow % G) * 1.4426950408889634f;
+    }
     const uint32_t p_ready0 = cluster_addr(bar + kPReady, 0);
     float m_used = -INFINITY;  // log2 units
     bool ok = true;
@@ -355,14 +376,23 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_base + s * 128 + c * 32, sv[c]);
       tmem_wait_ld();
-      // Causal / ragged edge: only tiles that reach past some row's last key need a mask.
-      const int lim = min(p_row, kv_end - 1) - j * kKeysPerTile;
-      if (!__all_sync(kFull, lim >= kKeysPerTile - 1)) {
+      const int kt0 = base + j * kKeysPerTile;
+      if constexpr ((MODE & (kModCap | kModBias)) != 0)
+        tile_logits<MODE>(sv, sl2, cap, slope, p_row - kt0,
+                          a.key_end != nullptr && __any_sync(kFull, min(hi, kt0 + kKeysPerTile) > p_row + 1));
+      // Edges: only tiles that reach past some row's keys need a mask (causal and ragged; both ends with modified scores).
+      if constexpr (MODE != kModNone) {
+        const int first = lo - kt0, lim = hi - 1 - kt0;
+        if (!__all_sync(kFull, first <= 0 && lim >= kKeysPerTile - 1)) mask_tile(sv, first, lim);
+      } else {
+        const int lim = min(p_row, kv_end - 1) - kt0;
+        if (!__all_sync(kFull, lim >= kKeysPerTile - 1)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c * 32 + i > lim) sv[c][i] = kNegInfBits;
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i > lim) sv[c][i] = kNegInfBits;
+        }
       }
       // Row max: three-input max, four independent chains.
       float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -371,10 +401,14 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 32; i += 2)
           mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(sv[c][i]), __uint_as_float(sv[c][i + 1]));
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+      // sv holds raw products, or logits where the scores were capped or biased
+      const float unit = (MODE & (kModCap | kModBias)) ? 1.f : sl2;
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * unit;
       const float m_new = fmaxf(m_used, mx);
-      const bool need = j > 0 && m_new > m_used + kRescaleThreshold;
-      if (j == 0) m_used = m_new;
+      // before a row's first visible key there is nothing to rescale
+      const bool fresh = MODE != kModNone ? m_used == -INFINITY : j == 0;
+      const bool need = !fresh && m_new > m_used + kRescaleThreshold;
+      if (fresh) m_used = m_new;
       if (__any_sync(kFull, need)) {
         // O must hold tile j-1's products before it is rescaled.
         if (!(ok = warp_wait_or_abort(bar + kPVDone + (j - 1) % kSBufs, ((j - 1) / kSBufs) & 1, abort_flag))) break;
@@ -393,25 +427,27 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
           tmem_st32(tmem + lane_base + kOCol + c * 32, ov);
         }
       }
-      const float nm = -m_used;
+      const float nm = MODE != kModNone && m_used == -INFINITY ? 0.f : -m_used;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float x0, x1;
-          fma2(x0, x1, __uint_as_float(sv[c][2 * i]), __uint_as_float(sv[c][2 * i + 1]), sl2, sl2, nm, nm);
+          fma2(x0, x1, __uint_as_float(sv[c][2 * i]), __uint_as_float(sv[c][2 * i + 1]), unit, unit, nm, nm);
           const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
           add2(l_sum, l_odd, p0, p1);
           pk[i] = pack_bf16x2(p0, p1);
         }
         tmem_st16(tmem + lane_base + s * 128 + c * 16, pk);
       }
+      // Zero this CTA's V rows past the last visible key inside the final 16-key
+      // step, and before the first visible one inside the first: a block may
+      // hold stale or NaN rows there, and 0 * NaN would reach O. The tile's data
+      // has landed (S_j exists).
+      bool wrote_v = j == ntiles - 1;
       if (j == ntiles - 1) {
-        // Zero this CTA's V rows past the last visible key inside the final
-        // 16-key step: a partly filled block may hold stale or NaN rows there,
-        // and 0 * NaN would reach O. The tile's data has landed (S_j exists).
-        const int valid = kv_end - j * kKeysPerTile;
+        const int valid = kv_end - kt0;
         const int tail = (kSubKeys - valid % kSubKeys) % kSubKeys;
         if (tail) {
           uint8_t *sV = sKV + (j % kStages) * Lay::kStageBytes + Lay::kKBytes;
@@ -420,20 +456,30 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
           fence_proxy_async_smem();
         }
       }
+      if (MODE != kModNone && j == 0 && kv_begin > base) {
+        uint8_t *sV = sKV + Lay::kKBytes;
+        for (int i = threadIdx.x; i < (kv_begin - base) * 8; i += 128)
+          *reinterpret_cast<uint4 *>(sV + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        wrote_v = true;
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      // Only the last tile also wrote shared memory (the V tail) for the MMA to read.
+      // Only these tiles also wrote shared memory (V rows) for the MMA to read.
       if (lane == 0) {
-        if (j == ntiles - 1)
+        if (wrote_v)
           mbar_arrive_cluster(p_ready0 + s * 8);
         else
           mbar_arrive_remote_cta_release(p_ready0 + s * 8);
       }
     }
-    if (ok && warp_wait_or_abort(bar + kPVDone + (ntiles - 1) % kSBufs, ((ntiles - 1) / kSBufs) & 1, abort_flag)) {
+    if (ok && (ntiles == 0 ||
+               warp_wait_or_abort(bar + kPVDone + (ntiles - 1) % kSBufs, ((ntiles - 1) / kSBufs) & 1, abort_flag))) {
       tc_fence_after();
       const float inv = 1.f / (l_sum + l_odd);
+      // a row that sees nothing gives zeros, whatever O holds (an empty pair's O was never written)
+      const bool none = MODE != kModNone && lo >= hi;
       constexpr int kRowBytes = D * 2, kChunks = kRowBytes / 16;
       if (!a.out_on_host) {
         // each thread stores its own row, 64 bytes per TMEM load (the loads are warp-wide)
@@ -450,7 +496,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              pk[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
+              pk[i] = none ? 0u : pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
 #pragma unroll
             for (int v = 0; v < 4; ++v)
               orow[c * 4 + v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
@@ -472,7 +518,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            pk[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
+            pk[i] = none ? 0u : pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
 #pragma unroll
           for (int v = 0; v < 4; ++v)
             *reinterpret_cast<uint4 *>(stage + lane * kRowBytes + (((c * 4 + v) ^ (lane & 15)) << 4)) =
@@ -504,12 +550,12 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
   }
 }
 
-template <int NST>
+template <int NST, int MODE>
 cudaError_t launch_pair_t(const StepArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           int32_t rows_per_tile, int32_t num_items, const int32_t *items, cudaStream_t stream) {
   constexpr int smem = Layout<NST>::kSmem;
   static std::atomic<uint64_t> configured{0};  // one bit per device
-  if (const cudaError_t e = allow_smem_once(prefill_pair_kernel<NST>, smem, configured); e != cudaSuccess) return e;
+  if (const cudaError_t e = allow_smem_once(prefill_pair_kernel<NST, MODE>, smem, configured); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * num_items), static_cast<unsigned>(a.num_kv_heads));
   cfg.blockDim = dim3(kThreads);
@@ -524,7 +570,22 @@ cudaError_t launch_pair_t(const StepArgs &a, const CUtensorMap &tq, const CUtens
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<NST>, tq, tk, tv, a, items, rows_per_tile);
+  return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<NST, MODE>, tq, tk, tv, a, items, rows_per_tile);
+}
+
+template <int NST>
+cudaError_t launch_pair_m(const StepArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                          int32_t rows_per_tile, int32_t num_items, const int32_t *items, cudaStream_t stream) {
+  switch (mode_of(a)) {
+    case kModNone: return launch_pair_t<NST, kModNone>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+    case kModMask: return launch_pair_t<NST, kModMask>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+    case kModMask | kModCap:
+      return launch_pair_t<NST, kModMask | kModCap>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+    case kModMask | kModBias:
+      return launch_pair_t<NST, kModMask | kModBias>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+    default:
+      return launch_pair_t<NST, kModMask | kModCap | kModBias>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+  }
 }
 
 }  // namespace
@@ -533,8 +594,8 @@ cudaError_t launch_prefill_pair(const StepArgs &a, const CUtensorMap &tq, const 
                                 const CUtensorMap &tv, int32_t rows_per_tile, int32_t num_items,
                                 const int32_t *items, bool beside_decode, cudaStream_t stream) {
   if (num_items <= 0) return cudaSuccess;
-  return beside_decode ? launch_pair_t<kPairStagesBesideDecode>(a, tq, tk, tv, rows_per_tile, num_items, items, stream)
-                       : launch_pair_t<6>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+  return beside_decode ? launch_pair_m<kPairStagesBesideDecode>(a, tq, tk, tv, rows_per_tile, num_items, items, stream)
+                       : launch_pair_m<6>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
 }
 
 }  // namespace pkv

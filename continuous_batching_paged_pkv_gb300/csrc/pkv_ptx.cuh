@@ -88,6 +88,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// 1 / x on the SFU (PTX rcp.approx, flush-to-zero); infinity gives 0.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Order this thread's generic-proxy shared-memory accesses before later
 // async-proxy (TMA, tcgen05.mma) accesses of the same memory.
 __device__ __forceinline__ void fence_proxy_async_smem() {
