@@ -424,11 +424,6 @@ static pkv_status attention_quant(int32_t bits, const void *q, const int32_t *cu
   a.status = device_status;
   a.task_counter = info->num_partials ? reinterpret_cast<uint32_t *>(ws + acc_bytes + ml_bytes) : nullptr;
 
-  if (mod) {
-    const cudaError_t e =
-        pkv::launch_score_mod(a, k_scales, v_scales, bits, reinterpret_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
-  }
   // The chunk kernel reads a bf16 scratch pool: the chunk segments' histories,
   // widened block by block, with a scratch block table in the same shape.
   pkv::StepArgs c = a;

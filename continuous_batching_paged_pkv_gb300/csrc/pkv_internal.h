@@ -123,10 +123,6 @@ cudaError_t launch_widen_quant(const StepArgs &a, const void *k_codes, const voi
                             int64_t scratch_blocks, int32_t num_items, const int32_t *items, int32_t bits,
                             cudaStream_t stream);
 
-// Attention with modified scores, pool of `bits` (16: bf16) with its scales, every row of the step.
-cudaError_t launch_score_mod(const StepArgs &a, const void *k_scales, const void *v_scales, int32_t bits,
-                             cudaStream_t stream);
-
 cudaError_t launch_prefill(const StepArgs &a, const CUtensorMap &tmap_q, int32_t rows_per_tile,
                            int32_t num_items, const int32_t *items, cudaStream_t stream);
 // head_dim 128: items are tile pairs, run by clusters of two CTAs.

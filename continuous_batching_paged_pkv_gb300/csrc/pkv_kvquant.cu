@@ -146,10 +146,11 @@ __global__ void __launch_bounds__(256) cache_write_quant_kernel(
 
 // ---- prompt-chunk histories widened into a bf16 scratch pool ------------------
 
-// Item (segment, slot, first scratch block, blocks). CTA (item, y) widens the
-// item's logical blocks y, y + gridDim.y, ... : block j of the slot becomes
-// scratch block first + j, and the scratch table row of the slot points there.
-template <int D, int BITS>
+// Item (segment, slot, first scratch block, blocks); with modified scores (MOD)
+// word 1 is the first logical block that some row of the segment sees. CTA (item, y) widens the
+// item's blocks y, y + gridDim.y, ... : block j of the item becomes scratch
+// block first + j, and the scratch table row of the slot points there.
+template <int D, int BITS, bool MOD>
 __global__ void __launch_bounds__(256) widen_quant_kernel(const StepArgs a, const int32_t *__restrict__ items,
                                                        const int8_t *__restrict__ k_codes,
                                                        const __nv_bfloat16 *__restrict__ k_scales,
@@ -159,12 +160,16 @@ __global__ void __launch_bounds__(256) widen_quant_kernel(const StepArgs a, cons
                                                        __nv_bfloat16 *__restrict__ v_out,
                                                        int32_t *__restrict__ scratch_table, int64_t scratch_blocks) {
   const int4 it = __ldg(reinterpret_cast<const int4 *>(items) + blockIdx.x);
-  const int seg = it.x, slot = it.y, first = it.z, nblk = it.w;
-  bool ok = seg >= 0 && seg < a.num_seqs && slot >= 0 && slot < a.max_slots && first >= 0 && nblk >= 1 &&
-            static_cast<int64_t>(first) + nblk <= scratch_blocks && nblk <= a.max_blocks_per_slot;
+  const int seg = it.x, first = it.z, nblk = it.w, blk0 = MOD ? it.y : 0;
+  bool ok = seg >= 0 && seg < a.num_seqs && first >= 0 && nblk >= (MOD ? 0 : 1) && blk0 >= 0 &&
+            static_cast<int64_t>(first) + nblk <= scratch_blocks &&
+            static_cast<int64_t>(blk0) + nblk <= a.max_blocks_per_slot;
+  const int slot = !ok ? -1 : MOD ? __ldg(a.seq_slot + seg) : it.y;
+  ok = ok && slot >= 0 && slot < a.max_slots;
   if (ok) {
     const int L = __ldg(a.context_lens + slot);
-    ok = __ldg(a.seq_slot + seg) == slot && (L + a.block_size - 1) / a.block_size == nblk;
+    const int have = (L + a.block_size - 1) / a.block_size;
+    ok = MOD ? blk0 + nblk <= have : __ldg(a.seq_slot + seg) == slot && have == nblk;
   }
   grid_dependency_wait();  // the codes come from the cache write before this kernel
   launch_dependents();
@@ -176,10 +181,10 @@ __global__ void __launch_bounds__(256) widen_quant_kernel(const StepArgs a, cons
   const int64_t rows = static_cast<int64_t>(a.num_kv_heads) * a.block_size;  // rows of one block
   const int64_t vecs = rows * (D / 8);                                      // 8 values per vector
   for (int j = blockIdx.y; j < nblk; j += gridDim.y) {
-    const int bid = __ldg(a.block_tables + static_cast<int64_t>(slot) * a.max_blocks_per_slot + j);
+    const int bid = __ldg(a.block_tables + static_cast<int64_t>(slot) * a.max_blocks_per_slot + blk0 + j);
     const bool in_pool = bid >= 0 && bid < a.num_blocks;
     if (!in_pool && threadIdx.x == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_BLOCK);
-    if (threadIdx.x == 0) scratch_table[static_cast<int64_t>(slot) * a.max_blocks_per_slot + j] = first + j;
+    if (threadIdx.x == 0) scratch_table[static_cast<int64_t>(slot) * a.max_blocks_per_slot + blk0 + j] = first + j;
     const int64_t src_row0 = static_cast<int64_t>(in_pool ? bid : 0) * rows;
     const int64_t dst_row0 = static_cast<int64_t>(first + j) * rows;
     for (int64_t i = threadIdx.x; i < 2 * vecs; i += blockDim.x) {
@@ -390,7 +395,7 @@ __device__ __forceinline__ void key_offsets(float (&kinit)[D / 32][NT][4], const
     }
 }
 
-template <int D, int NT, bool MULTI, int NW, int BITS>
+template <int D, int NT, bool MULTI, bool MOD, int NW, int BITS>
 __global__ void __launch_bounds__(NW * 32, 1)
     decode_quant_kernel(const __grid_constant__ CUtensorMap tmap_kc, const __grid_constant__ CUtensorMap tmap_vc,
                      const StepArgs a, const __nv_bfloat16 *__restrict__ k_scales,
@@ -431,15 +436,15 @@ __global__ void __launch_bounds__(NW * 32, 1)
   uint32_t *const counter = a.task_counter;
   Task A, B;
   int4 rawC = make_int4(0, 0, 0, 0);
-  expand(A, t0, load_item(items, t0, hkv), a, lane);
+  expand<MOD>(A, t0, load_item(items, t0, hkv), a, lane);
   int tC;
   {
     const int t1 = t0 + stride;
-    expand(B, t1 < num_tasks ? t1 : -1, t1 < num_tasks ? load_item(items, t1, hkv) : rawC, a, lane);
+    expand<MOD>(B, t1 < num_tasks ? t1 : -1, t1 < num_tasks ? load_item(items, t1, hkv) : rawC, a, lane);
     tC = t1 + stride;
     if (tC < num_tasks) rawC = load_item(items, tC, hkv);
   }
-  finalize(A, a, lane, 8 * NT, kMaxRows);
+  finalize<MOD>(A, a, lane, 8 * NT, kMaxRows);
   uint32_t qA[NT][KT][2];
   float invA[NT];
   if (A.ok) load_q_quant<D, NT, MULTI, BITS>(qA, invA, A, a, lane);
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
     if (B.t >= 0) {
       if (!B.finalized) {
-        finalize(B, a, lane, 8 * NT, kMaxRows);
+        finalize<MOD>(B, a, lane, 8 * NT, kMaxRows);
         if (B.ok) prefetch_q<D, NT, MULTI>(B, a, lane);  // loaded when B becomes current
       }
       if (pb < B.units) {
@@ -507,6 +512,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
   // (rows r + 8 of a 4-bit m-tile hold odd nibbles, at 1152 + 16 c)
   constexpr uint32_t kNegOffLo = BITS == 8 ? 0xE480E480u : 0xE408E408u;
   const uint32_t kNegOff[4] = {kNegOffLo, 0xE480E480u, kNegOffLo, 0xE480E480u};
+  const Cap cap(MOD ? a.softcap : 0.f);
+  const bool bias = MOD && a.alibi_slopes;
   int cstage = 0;
   uint32_t cphase = 0;
 
@@ -536,7 +543,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     key_offsets<D, NT, BITS>(kinit, qA, lane);
     const int nrows = MULTI ? A.nrows : 1;
     uint32_t colrow = 0;
-    if (MULTI) {
+    if (MULTI && !MOD) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -553,6 +560,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
 #pragma unroll
       for (int c = 0; c < 2; ++c) sl2c[nt][c] = sl2 * __shfl_sync(kAll, invA[nt], (jq * 2 + c) * 4);
 
+    TaskMod<NT, MULTI> tm;
+    if constexpr (MOD) tm.set(A, a, lane);
+
     for (int u = 0; u < A.units; ++u) {
       const int stage = cstage;
       if (!mbar_wait(full + stage, cphase)) {
@@ -561,7 +571,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
       }
       const int row = __shfl_sync(kAll, A.row, u);
       const int kbase = A.key0 + u * kSubKeys;
-      const int v = row >= 0 ? min(kSubKeys, A.key1 - kbase) : 0;
+      int v = row >= 0 ? min(kSubKeys, A.key1 - kbase) : 0, v0 = 0;
+      if constexpr (MOD) {  // [v0, v): the keys that some row sees
+        v0 = max(0, tm.u_lo - kbase);
+        v = min(v, tm.u_hi - kbase);
+      }
       const int vis0 = A.L - nrows - kbase + 1;
       // this thread's K words of rows ka (and kb, 8 rows on) at chunk 0; a chunk index is XORed into
       // the swizzled chunk bits (the stage base is a multiple of 128)
@@ -583,8 +597,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
       }
 #pragma unroll
       for (int i = 0; i < NG2; ++i) {
-        vwa[i] = ka < v ? vwa[i] : 0u;
-        vwb[i] = kb < v ? vwb[i] : 0u;
+        vwa[i] = ka < v && (!MOD || ka >= v0) ? vwa[i] : 0u;
+        vwb[i] = kb < v && (!MOD || kb >= v0) ? vwb[i] : 0u;
       }
 
       // S^T = K Q^T per scale group over the offset codes, each group's
@@ -650,9 +664,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int vis = MULTI ? min(v, vis0 + static_cast<int>((colrow >> (8 * (nt * 2 + c))) & 0xFF)) : v;
-          x[nt][c][0] = ka < vis ? sacc[nt][c] * sl2c[nt][c] : -INFINITY;
-          x[nt][c][1] = kb < vis ? sacc[nt][c + 2] * sl2c[nt][c] : -INFINITY;
+          if constexpr (MOD) {
+            x[nt][c][0] = tm.logit(sacc[nt][c] * sl2c[nt][c], kbase + ka, nt, c, ka < v, cap, bias);
+            x[nt][c][1] = tm.logit(sacc[nt][c + 2] * sl2c[nt][c], kbase + kb, nt, c, kb < v, cap, bias);
+          } else {
+            const int vis = MULTI ? min(v, vis0 + static_cast<int>((colrow >> (8 * (nt * 2 + c))) & 0xFF)) : v;
+            x[nt][c][0] = ka < vis ? sacc[nt][c] * sl2c[nt][c] : -INFINITY;
+            x[nt][c][1] = kb < vis ? sacc[nt][c + 2] * sl2c[nt][c] : -INFINITY;
+          }
           need |= fmaxf(x[nt][c][0], x[nt][c][1]) > mr[nt][c];
         }
       if (__any_sync(kAll, need)) {
@@ -827,7 +846,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
             if (A.pbase < 0) {
               __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) +
                                    ((static_cast<size_t>(A.row0) + i) * a.num_q_heads + hbase + hh) * D + 4 * r;
-              const float inv = 1.f / l[nt][c];  // l also carries the 2^7
+              // l also carries the 2^7; it is 0 for a row that sees nothing, which gives zeros
+              const float inv = MOD && l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];
 #pragma unroll
               for (int g = 0; g < NG; ++g) {
                 uint2 pk;
@@ -838,7 +858,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             } else {
               // span partials in the merge's units: sums of p dv code and of p
               constexpr float kDown = 1.f / 128.f;
-              const size_t pi = (static_cast<size_t>(A.pbase + A.span * nrows + i) * a.num_q_heads + hbase + hh);
+              const size_t pi = (static_cast<size_t>(A.pbase + (MOD ? 0 : A.span * nrows) + i) * a.num_q_heads + hbase + hh);
               float *pacc = a.partial_acc + pi * D + 4 * r;
 #pragma unroll
               for (int g = 0; g < NG; ++g)
@@ -869,10 +889,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
     pa = pb;
     pb = 0;
     if (A.t >= 0) {
-      if (!A.finalized) finalize(A, a, lane, 8 * NT, kMaxRows);
+      if (!A.finalized) finalize<MOD>(A, a, lane, 8 * NT, kMaxRows);
       if (A.ok) load_q_quant<D, NT, MULTI, BITS>(qA, invA, A, a, lane);
     }
-    expand(B, next_t < num_tasks ? next_t : -1, rawC, a, lane);
+    expand<MOD>(B, next_t < num_tasks ? next_t : -1, rawC, a, lane);
     tC = after;
     if (tC < num_tasks) rawC = load_item(items, tC, hkv);
     while (P - C < NST && issue_next()) {
@@ -880,13 +900,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
   }
 }
 
-template <int D, int NT, bool MULTI, int NW, int BITS>
+template <int D, int NT, bool MULTI, bool MOD, int NW, int BITS>
 cudaError_t launch_decode_quant_w(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv,
                                const void *k_scales, const void *v_scales, int32_t num_items, const int32_t *items,
                                int grid, cudaStream_t stream) {
   constexpr int smem = QuantCfg<D, NW, BITS>::kSmem;
   static std::atomic<uint64_t> configured{0};  // one bit per device
-  if (const cudaError_t e = allow_smem_once(decode_quant_kernel<D, NT, MULTI, NW, BITS>, smem, configured);
+  if (const cudaError_t e = allow_smem_once(decode_quant_kernel<D, NT, MULTI, MOD, NW, BITS>, smem, configured);
       e != cudaSuccess)
     return e;
   const int64_t tasks = static_cast<int64_t>(num_items) * a.num_kv_heads;
@@ -897,7 +917,7 @@ cudaError_t launch_decode_quant_w(const StepArgs &a, const CUtensorMap &tk, cons
   } else {
     b.task_counter = nullptr;
   }
-  return launch_pdl(decode_quant_kernel<D, NT, MULTI, NW, BITS>, dim3(grid), dim3(NW * 32), smem, stream, tk, tv, b,
+  return launch_pdl(decode_quant_kernel<D, NT, MULTI, MOD, NW, BITS>, dim3(grid), dim3(NW * 32), smem, stream, tk, tv, b,
                     static_cast<const __nv_bfloat16 *>(k_scales), static_cast<const __nv_bfloat16 *>(v_scales),
                     items, num_items);
 }
@@ -907,7 +927,7 @@ cudaError_t launch_decode_quant_w(const StepArgs &a, const CUtensorMap &tk, cons
 // tasks run 12 warps instead: the code conversions make a warp's sub-tile a
 // long dependent chain, and more warps per scheduler hide it once every warp
 // has work (a small step's few busy warps stream faster through deeper rings).
-template <int D, int NT, bool MULTI, int BITS>
+template <int D, int NT, bool MULTI, bool MOD, int BITS>
 cudaError_t launch_decode_quant_t(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv,
                                const void *k_scales, const void *v_scales, int32_t num_items, const int32_t *items,
                                cudaStream_t stream) {
@@ -918,10 +938,10 @@ cudaError_t launch_decode_quant_t(const StepArgs &a, const CUtensorMap &tk, cons
   const int grid = static_cast<int>(tasks < sms ? tasks : sms);
   if constexpr (D == 128 && NT == 1 && !MULTI) {
     if (tasks > 3ll * grid * 12)
-      return launch_decode_quant_w<D, NT, MULTI, 12, BITS>(a, tk, tv, k_scales, v_scales, num_items, items, grid,
+      return launch_decode_quant_w<D, NT, MULTI, MOD, 12, BITS>(a, tk, tv, k_scales, v_scales, num_items, items, grid,
                                                          stream);
   }
-  return launch_decode_quant_w<D, NT, MULTI, kWarpsQuant, BITS>(a, tk, tv, k_scales, v_scales, num_items, items, grid,
+  return launch_decode_quant_w<D, NT, MULTI, MOD, kWarpsQuant, BITS>(a, tk, tv, k_scales, v_scales, num_items, items, grid,
                                                            stream);
 }
 
@@ -967,41 +987,45 @@ cudaError_t launch_widen_quant(const StepArgs &a, const void *k_codes, const voi
   auto *vsc = static_cast<const __nv_bfloat16 *>(v_scales);
   auto *ko = static_cast<__nv_bfloat16 *>(k_out);
   auto *vo = static_cast<__nv_bfloat16 *>(v_out);
-  if (bits == 4)
-    return launch_pdl(widen_quant_kernel<128, 4>, grid, dim3(256), 0, stream, a, items, kc, ksc, vc, vsc, ko, vo,
-                      scratch_table, scratch_blocks);
-  if (a.head_dim == 128)
-    return launch_pdl(widen_quant_kernel<128, 8>, grid, dim3(256), 0, stream, a, items, kc, ksc, vc, vsc, ko, vo,
-                      scratch_table, scratch_blocks);
-  return launch_pdl(widen_quant_kernel<64, 8>, grid, dim3(256), 0, stream, a, items, kc, ksc, vc, vsc, ko, vo,
-                    scratch_table, scratch_blocks);
+  auto *kernel = bits == 4            ? (a.modified ? widen_quant_kernel<128, 4, true> : widen_quant_kernel<128, 4, false>)
+                 : a.head_dim == 128 ? (a.modified ? widen_quant_kernel<128, 8, true> : widen_quant_kernel<128, 8, false>)
+                                     : (a.modified ? widen_quant_kernel<64, 8, true> : widen_quant_kernel<64, 8, false>);
+  return launch_pdl(kernel, grid, dim3(256), 0, stream, a, items, kc, ksc, vc, vsc, ko, vo, scratch_table, scratch_blocks);
+}
+
+template <bool MOD>
+static cudaError_t launch_decode_quant_m(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv,
+                                         const void *k_scales, const void *v_scales, int32_t num_items,
+                                         const int32_t *items, int32_t bits, cudaStream_t stream) {
+  const bool multi = a.decode_rows_max > 1;
+  const bool wide = a.group * (multi ? a.decode_rows_max : 1) > 8;
+  const int v = (wide ? 2 : 0) + (multi ? 1 : 0);
+  if (bits == 4) {  // head_dim 128 only
+    switch (v) {
+      case 0: return launch_decode_quant_t<128, 1, false, MOD, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+      case 1: return launch_decode_quant_t<128, 1, true, MOD, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+      case 2: return launch_decode_quant_t<128, 2, false, MOD, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+      default: return launch_decode_quant_t<128, 2, true, MOD, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    }
+  }
+  switch (v + (a.head_dim == 128 ? 4 : 0)) {
+    case 0: return launch_decode_quant_t<64, 1, false, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 1: return launch_decode_quant_t<64, 1, true, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 2: return launch_decode_quant_t<64, 2, false, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 3: return launch_decode_quant_t<64, 2, true, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 4: return launch_decode_quant_t<128, 1, false, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 5: return launch_decode_quant_t<128, 1, true, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 6: return launch_decode_quant_t<128, 2, false, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    default: return launch_decode_quant_t<128, 2, true, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+  }
 }
 
 cudaError_t launch_decode_quant(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, const void *k_scales,
                              const void *v_scales, int32_t num_items, const int32_t *items, int32_t bits,
                              cudaStream_t stream) {
   if (num_items <= 0) return cudaSuccess;
-  const bool multi = a.decode_rows_max > 1;
-  const bool wide = a.group * (multi ? a.decode_rows_max : 1) > 8;
-  const int v = (wide ? 2 : 0) + (multi ? 1 : 0);
-  if (bits == 4) {  // head_dim 128 only
-    switch (v) {
-      case 0: return launch_decode_quant_t<128, 1, false, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-      case 1: return launch_decode_quant_t<128, 1, true, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-      case 2: return launch_decode_quant_t<128, 2, false, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-      default: return launch_decode_quant_t<128, 2, true, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    }
-  }
-  switch (v + (a.head_dim == 128 ? 4 : 0)) {
-    case 0: return launch_decode_quant_t<64, 1, false, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 1: return launch_decode_quant_t<64, 1, true, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 2: return launch_decode_quant_t<64, 2, false, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 3: return launch_decode_quant_t<64, 2, true, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 4: return launch_decode_quant_t<128, 1, false, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 5: return launch_decode_quant_t<128, 1, true, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 6: return launch_decode_quant_t<128, 2, false, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    default: return launch_decode_quant_t<128, 2, true, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-  }
+  return a.modified ? launch_decode_quant_m<true>(a, tk, tv, k_scales, v_scales, num_items, items, bits, stream)
+                    : launch_decode_quant_m<false>(a, tk, tv, k_scales, v_scales, num_items, items, bits, stream);
 }
 
 }  // namespace pkv
