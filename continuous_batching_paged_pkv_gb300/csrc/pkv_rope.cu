@@ -19,64 +19,173 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxPairs = 64;  // head_dim / 2 at head_dim 128
 
-// One CTA per token: its angles once into shared memory, then one pair per
-// thread over the token's rows (q heads, then k heads, then v heads).
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
-  __shared__ float2 turn[kMaxPairs];  // (cos, sin) times the magnitude
-  grid_dependency_wait();             // every input may come from the previous kernel in the stream
+// The angles of token t: (cos, sin) times the magnitude of pair i into turn[i], one thread each.
+__device__ __forceinline__ void token_turns(const RopeArgs &a, int64_t t, float2 *turn) {
+  for (int i = threadIdx.x; i < a.rot_dim / 2; i += blockDim.x) {
+    const uint64_t angle =
+        static_cast<uint64_t>(static_cast<int64_t>(__ldg(a.positions + t))) * __ldg(a.phases + i);
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f, &s, &c);
+    turn[i] = make_float2(c * a.magnitude, s * a.magnitude);
+  }
+}
+
+// Where token t's key and value go: offset of its kv head 0 row in the pool, or
+// -1 where they are not kept. Head g's row is g * block_size rows further.
+__device__ __forceinline__ int64_t pool_offset(const RopeArgs &a, int64_t t, bool report) {
+  if (a.num_kv_heads == 0) return -1;
+  const int64_t slot = __ldg(a.slot_mapping + t);
+  if (slot < 0) return -1;
+  if (slot >= a.num_blocks * a.block_size) {
+    if (report && a.status) atomicOr(a.status, PKV_DEV_BAD_SLOT_MAPPING);
+    return -1;
+  }
+  const int64_t block = slot / a.block_size, row = slot % a.block_size;
+  return (block * a.num_kv_heads * a.block_size + row) * a.head_dim;
+}
+
+struct HeadRow {
+  const __nv_bfloat16 *src;
+  __nv_bfloat16 *dst;  // nullptr: nothing to do
+  bool turned;
+};
+
+// Head h of token t, in the order q heads, k heads, v heads.
+__device__ __forceinline__ HeadRow head_row(const RopeArgs &a, int64_t t, int h, int64_t pool) {
+  HeadRow r;
+  if (h < a.num_q_heads) {
+    r.src = a.q + t * a.q_stride + h * a.head_dim;
+    r.dst = a.q_out + t * a.q_out_stride + h * a.head_dim;
+    r.turned = true;
+    return r;
+  }
+  const bool is_v = h >= a.num_q_heads + a.num_kv_heads;
+  const int g = h - a.num_q_heads - (is_v ? a.num_kv_heads : 0);
+  r.src = (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + g * a.head_dim;
+  r.dst = pool < 0 ? nullptr
+                   : (is_v ? a.v_pool : a.k_pool) + pool + static_cast<int64_t>(g) * a.block_size * a.head_dim;
+  r.turned = !is_v;
+  return r;
+}
+
+// Any even rot_dim: one CTA per token, one pair of elements per thread.
+__global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const RopeArgs a) {
+  __shared__ float2 turn[kMaxPairs];
+  grid_dependency_wait();  // every input may come from the previous kernel in the stream
   const int rot_pairs = a.rot_dim / 2, row_pairs = a.head_dim / 2;
   const int heads = a.num_q_heads + 2 * a.num_kv_heads;
-  for (int64_t t = blockIdx.x; t < a.num_tokens; t += gridDim.x) {
-    if (threadIdx.x < rot_pairs) {
-      const uint64_t angle = static_cast<uint64_t>(static_cast<int64_t>(__ldg(a.positions + t))) *
-                             __ldg(a.phases + threadIdx.x);
-      float s, c;
-      sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f, &s, &c);
-      turn[threadIdx.x] = make_float2(c * a.magnitude, s * a.magnitude);
+  const int64_t t = blockIdx.x;
+  const int64_t pool = pool_offset(a, t, threadIdx.x == 0);
+  token_turns(a, t, turn);
+  __syncthreads();
+  for (int i = threadIdx.x; i < heads * row_pairs; i += kThreads) {
+    const int j = i % row_pairs;
+    const HeadRow r = head_row(a, t, i / row_pairs, pool);
+    if (!r.dst) continue;
+    const int i0 = a.interleaved || j >= rot_pairs ? 2 * j : j;
+    const int i1 = a.interleaved || j >= rot_pairs ? 2 * j + 1 : j + rot_pairs;
+    const __nv_bfloat16 x0 = r.src[i0], x1 = r.src[i1];
+    if (r.turned && j < rot_pairs) {
+      const float2 w = turn[j];
+      const float f0 = __bfloat162float(x0), f1 = __bfloat162float(x1);
+      r.dst[i0] = __float2bfloat16_rn(f0 * w.x - f1 * w.y);
+      r.dst[i1] = __float2bfloat16_rn(f0 * w.y + f1 * w.x);
+    } else {
+      r.dst[i0] = x0;
+      r.dst[i1] = x1;
     }
-    __syncthreads();
-    int64_t block = 0, row = 0;
-    bool keep = false;
-    if (a.num_kv_heads > 0) {
-      const int64_t slot = __ldg(a.slot_mapping + t);
-      keep = slot >= 0 && slot < a.num_blocks * a.block_size;
-      if (slot >= 0 && !keep && threadIdx.x == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_SLOT_MAPPING);
-      block = keep ? slot / a.block_size : 0;
-      row = keep ? slot % a.block_size : 0;
+  }
+  __threadfence();  // as in rope_vectors_kernel
+}
+
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Half layout: vector x holds the first elements of eight pairs, y the second ones.
+__device__ __forceinline__ void turn_halves(uint4 &x, uint4 &y, const float2 *w) {
+  uint32_t *px = &x.x, *py = &y.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 w0 = w[2 * i], w1 = w[2 * i + 1];
+    const float a0 = low(px[i]), a1 = high(px[i]), b0 = low(py[i]), b1 = high(py[i]);
+    px[i] = pack_bf16x2(a0 * w0.x - b0 * w0.y, a1 * w1.x - b1 * w1.y);
+    py[i] = pack_bf16x2(a0 * w0.y + b0 * w0.x, a1 * w1.y + b1 * w1.x);
+  }
+}
+
+// Interleaved: a vector holds four pairs.
+__device__ __forceinline__ void turn_pairs(uint4 &x, const float2 *w) {
+  uint32_t *p = &x.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float f0 = low(p[i]), f1 = high(p[i]);
+    p[i] = pack_bf16x2(f0 * w[i].x - f1 * w[i].y, f0 * w[i].y + f1 * w[i].x);
+  }
+}
+
+// rot_dim in whole 16-byte vectors (half layout: a multiple of 16, interleaved:
+// of 8). A unit is two vectors of a head: the two halves of eight pairs, or two
+// neighbours. A thread keeps its place within the head (D / 16 units divide the
+// CTA's threads), so it reads its eight angles from shared memory once and walks
+// the token's heads with them, one unit at a time; the first is requested before
+// the angles are computed. gridDim.y CTAs share a token's units where tokens are few.
+//
+// Bound by HBM: T (2 Hq + 4 Hkv) D 2 bytes move and the angles are shared by a
+// token's heads. What counts is CTAs in flight (12 of 128 threads per SM at 42
+// registers, or 24 of 64), since a CTA waits in turn for position, vectors and
+// stores: 24500 tokens of 64 + 8 heads of 128 take 155 us (6480 GB/s, 96% of the
+// measured copy rate); with three units in flight per thread and 80 registers
+// they took 223 us, and one pair of elements per thread 379 us.
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, 12) rope_vectors_kernel(const RopeArgs a) {
+  constexpr int U = D / 16;  // units per head
+  __shared__ float2 turn[kMaxPairs];
+  grid_dependency_wait();  // every input may come from the previous kernel in the stream
+  const int64_t t = blockIdx.x;
+  const int64_t pool = pool_offset(a, t, threadIdx.x == 0 && blockIdx.y == 0);
+  const int heads = a.num_q_heads + 2 * a.num_kv_heads;
+  const int c = threadIdx.x % U;
+  const int turned_vecs = a.rot_dim / 8;
+  // this thread's two vectors of a head
+  const bool halves = !INTERLEAVED && c < turned_vecs / 2;
+  const int v0 = halves ? c : 2 * c, v1 = halves ? c + turned_vecs / 2 : 2 * c + 1;
+  const int step = blockDim.x / U * gridDim.y;
+  int h = blockIdx.y * (blockDim.x / U) + threadIdx.x / U;
+
+  HeadRow r;
+  uint4 x, y;
+  auto load = [&]() {
+    r.dst = nullptr;
+    if (h < heads) r = head_row(a, t, h, pool);
+    if (r.dst) {
+      x = reinterpret_cast<const uint4 *>(r.src)[v0];
+      y = reinterpret_cast<const uint4 *>(r.src)[v1];
     }
-    for (int i = threadIdx.x; i < heads * row_pairs; i += kThreads) {
-      const int h = i / row_pairs, j = i % row_pairs;
-      const __nv_bfloat16 *src;
-      __nv_bfloat16 *dst;
-      const bool is_q = h < a.num_q_heads, is_v = h >= a.num_q_heads + a.num_kv_heads;
-      if (is_q) {
-        src = a.q + t * a.q_stride + h * a.head_dim;
-        dst = a.q_out + t * a.q_out_stride + h * a.head_dim;
-      } else {
-        if (!keep) continue;
-        const int g = h - a.num_q_heads - (is_v ? a.num_kv_heads : 0);
-        src = is_v ? a.v + t * a.v_stride + g * a.head_dim : a.k + t * a.k_stride + g * a.head_dim;
-        dst = (is_v ? a.v_pool : a.k_pool) +
-              ((block * a.num_kv_heads + g) * a.block_size + row) * static_cast<int64_t>(a.head_dim);
+  };
+  load();
+  token_turns(a, t, turn);
+  __syncthreads();
+  float2 w[8];
+  if (INTERLEAVED || halves) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = turn[c * 8 + i];  // past the rotated part: not used
+  }
+  for (; h < heads; h += step, load()) {
+    if (!r.dst) continue;
+    if (r.turned) {
+      if constexpr (INTERLEAVED) {
+        if (v0 < turned_vecs) turn_pairs(x, w);
+        if (v1 < turned_vecs) turn_pairs(y, w + 4);
+      } else if (halves) {
+        turn_halves(x, y, w);
       }
-      const bool turned = j < rot_pairs && !is_v;
-      const int i0 = a.interleaved || j >= rot_pairs ? 2 * j : j;
-      const int i1 = a.interleaved || j >= rot_pairs ? 2 * j + 1 : j + rot_pairs;
-      const __nv_bfloat16 x0 = src[i0], x1 = src[i1];
-      if (turned) {
-        const float2 w = turn[j];
-        const float f0 = __bfloat162float(x0), f1 = __bfloat162float(x1);
-        dst[i0] = __float2bfloat16_rn(f0 * w.x - f1 * w.y);
-        dst[i1] = __float2bfloat16_rn(f0 * w.y + f1 * w.x);
-      } else {
-        dst[i0] = x0;
-        dst[i1] = x1;
-      }
     }
-    __syncthreads();  // the angles are overwritten for the next token
+    uint4 *dst = reinterpret_cast<uint4 *>(r.dst);
+    dst[v0] = x;
+    dst[v1] = y;
   }
   // pkv_attention reads q before it waits for this grid: every store is
   // performed before its thread ends, and this kernel never signals early.
@@ -86,8 +195,24 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream) {
-  const int64_t grid = a.num_tokens < (int64_t(1) << 30) ? a.num_tokens : int64_t(1) << 30;
-  return launch_pdl(rope_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, a);
+  const unsigned tokens = static_cast<unsigned>(a.num_tokens);
+  if (a.rot_dim % (a.interleaved ? 8 : 16) != 0)
+    return launch_pdl(rope_pairs_kernel, dim3(tokens), dim3(kThreads), 0, stream, a);
+  const int units = (a.num_q_heads + 2 * a.num_kv_heads) * (a.head_dim / 16);
+  // Fewer tokens than SMs: one unit per thread, a token over several CTAs. Else one
+  // CTA per token, with more units per thread (fewer, smaller CTAs reuse the angles
+  // longer) the more tokens there are to fill the SMs. Measured with 3 / 5 / 10
+  // units: 256 tokens of 64 + 8 heads 4.3 / 4.9 / 6.8 us, 2048 of 32 + 8 13.7 /
+  // 10.9 / 11.9 us, 24500 of 64 + 8 175 / 162 / 152 us.
+  const bool few = a.num_tokens < 152;
+  const int per_thread = few ? 1 : a.num_tokens < 1024 ? 3 : a.num_tokens < 8192 ? 5 : 10;
+  const int want = (units + per_thread - 1) / per_thread;
+  const int passes = (want + kThreads - 1) / kThreads;
+  const int threads = ((want + passes - 1) / passes + 31) / 32 * 32;
+  const dim3 grid(tokens, few ? passes : 1);
+  auto *kernel = a.head_dim == 128 ? (a.interleaved ? rope_vectors_kernel<128, true> : rope_vectors_kernel<128, false>)
+                                   : (a.interleaved ? rope_vectors_kernel<64, true> : rope_vectors_kernel<64, false>);
+  return launch_pdl(kernel, grid, dim3(threads), 0, stream, a);
 }
 
 }  // namespace pkv
