@@ -474,12 +474,20 @@ class _BoundCall:
     The buffers must stay in place while the object is used; it holds references to them. With
     ``stream=None`` every call runs on the stream that is current then."""
 
-    def _bind(self, name, args, keep, stream):
-        self._fn, self._name, self._args = getattr(_lib(), name), name, args
-        self._keep, self._on = keep, None if stream is None else _stream(stream)
+    def _bind(self, name, args, keep, device, stream):
+        import torch
+
+        # every argument already is a ctypes object, so a call converts nothing but the stream
+        self._fn = _lib()[name]
+        self._fn.restype = ctypes.c_int
+        kinds = getattr(_lib(), name).argtypes
+        self._args = tuple(t(a) if isinstance(a, (int, float)) else a for a, t in zip(args, kinds))
+        self._name, self._keep, self._device = name, keep, device.index
+        self._current = torch._C._cuda_getCurrentRawStream
+        self._on = None if stream is None else _stream(stream)
 
     def __call__(self) -> None:
-        rc = self._fn(*self._args, _stream(None) if self._on is None else self._on)
+        rc = self._fn(*self._args, ctypes.c_void_p(self._current(self._device)) if self._on is None else self._on)
         if rc != PKV_OK:
             raise PkvError(rc, self._name)
 
@@ -499,7 +507,7 @@ class RopeCall(_BoundCall):
         table = _rope_table(phases, rot_dim, interleaved, magnitude)
         _need_on(x.device, positions, phases, out)
         self._bind("pkv_rope", (_t_ptr(x), xs, _t_ptr(positions), ctypes.byref(table), t, h, d, _t_ptr(out),
-                                _need_rows(out, t, "out")[2]), (x, positions, phases, out, table), stream)
+                                _need_rows(out, t, "out")[2]), (x, positions, phases, out, table), x.device, stream)
 
 
 class RopeCacheWriteCall(_BoundCall):
@@ -530,7 +538,7 @@ class RopeCacheWriteCall(_BoundCall):
                     ctypes.byref(table), t, hq, hkv, d, _t_ptr(q_out), os_, _t_ptr(k_pool), _t_ptr(v_pool), nb, bs,
                     _t_ptr(device_status)),
                    (q, k_new, v_new, positions, phases, slot_mapping, q_out, k_pool, v_pool, device_status, table),
-                   stream)
+                   q.device, stream)
 
 
 def pkv_rope(x, positions, phases, out, *, rot_dim: int, interleaved: bool = False, magnitude: float = 1.0,
@@ -612,7 +620,7 @@ class AttentionModCall(_BoundCall):
                     float(scale), ctypes.byref(args), _t_ptr(work), ctypes.byref(info), _t_ptr(out), _t_ptr(workspace),
                     ws_bytes, _t_ptr(device_status)),
                    (q, cu_seqlens_q, seq_slot, context_lens, block_tables, tuple(pool), work, info, out, workspace, mod,
-                    args, (mod.alibi_slopes, mod.key_begin, mod.key_end), device_status), stream)
+                    args, (mod.alibi_slopes, mod.key_begin, mod.key_end), device_status), q.device, stream)
 
 
 def pkv_attention_mod(q, cu_seqlens_q, seq_slot, context_lens, block_tables, k_pool, v_pool, work, info: WorkInfo, out,
