@@ -312,14 +312,21 @@ __global__ void __launch_bounds__(NW * 32, 1)
       // does the warp reduce the column maxima.
       float x[NT][2][2];
       bool need = false;
+      if constexpr (MOD) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            x[nt][c][0] = (s0[nt][c] + s1[nt][c]) * sl2;
+            x[nt][c][1] = (s0[nt][c + 2] + s1[nt][c + 2]) * sl2;
+          }
+        tm.logits(x, kbase, ka, v, cap, bias);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if constexpr (MOD) {
-            x[nt][c][0] = tm.logit((s0[nt][c] + s1[nt][c]) * sl2, kbase + ka, nt, c, ka < v, cap, bias);
-            x[nt][c][1] = tm.logit((s0[nt][c + 2] + s1[nt][c + 2]) * sl2, kbase + kb, nt, c, kb < v, cap, bias);
-          } else {
+          if constexpr (!MOD) {
             // causal limit of this column's row (a single row sees the whole span)
             const int vis = MULTI ? min(v, vis0 + static_cast<int>((colrow >> (8 * (nt * 2 + c))) & 0xFF)) : v;
             x[nt][c][0] = ka < vis ? (s0[nt][c] + s1[nt][c]) * sl2 : -INFINITY;

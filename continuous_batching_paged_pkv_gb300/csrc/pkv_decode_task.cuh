@@ -108,19 +108,24 @@ template <int NT, bool MULTI>
 struct TaskMod {
   static constexpr int N = MULTI ? NT : 1, C = MULTI ? 2 : 1;
   int lo[N][C], hi[N][C];  // visible keys [lo, hi) of the column
-  int pos[N][C];           // position of the column's row
+  float row[N][C];         // index of the column's row within the segment
   float slope[NT][2];      // distance bias per key, log2 units
   int u_lo, u_hi;          // keys that some row of the segment sees
+  int a_lo, a_hi;          // keys that every row of the segment sees
+  int pos0;                // position of the segment's first row
 
   __device__ __forceinline__ void set(const Task &T, const StepArgs &a, int lane) {
     const int n = T.ok ? T.nrows : 0;
+    pos0 = T.L - n;
     int lo_l = INT32_MAX, hi_l = 0;
     if (lane < n) {
-      visible_keys(a, T.begin, T.end, T.L - n + lane, T.L, lo_l, hi_l);
+      visible_keys(a, T.begin, T.end, pos0 + lane, T.L, lo_l, hi_l);
       if (lo_l >= hi_l) lo_l = INT32_MAX, hi_l = 0;
     }
     u_lo = __reduce_min_sync(0xffffffffu, lo_l);
     u_hi = __reduce_max_sync(0xffffffffu, hi_l);
+    a_lo = __reduce_max_sync(0xffffffffu, lane < n ? lo_l : 0);
+    a_hi = __reduce_min_sync(0xffffffffu, lane < n ? hi_l : INT32_MAX);
     // The rows' keys inside the span (all of them, if it is the only one) must be those the item names.
     const int s0 = T.span * PKV_SPLIT_KEYS;
     const int need0 = T.pbase < 0 ? u_lo : max(u_lo, s0), need1 = T.pbase < 0 ? u_hi : min(u_hi - s0, PKV_SPLIT_KEYS) + s0;
@@ -136,19 +141,49 @@ struct TaskMod {
           const int i = MULTI && valid ? col / a.group : 0;
           lo[nt][c] = __shfl_sync(0xffffffffu, lo_l, i);
           hi[nt][c] = __shfl_sync(0xffffffffu, hi_l, i);
-          pos[nt][c] = T.L - n + i;
+          row[nt][c] = static_cast<float>(i);
         }
         slope[nt][c] = valid && a.alibi_slopes
                            ? __ldg(a.alibi_slopes + T.g * a.group + (MULTI ? col % a.group : col)) * 1.4426950408889634f
                            : 0.f;
       }
   }
-  // The logit (log2 units) of the scaled score `x` (log2 units) at key j.
-  __device__ __forceinline__ float logit(float x, int j, int nt, int c, bool loaded, const Cap &cap, bool bias) const {
-    const int i = MULTI ? nt : 0, k = MULTI ? c : 0;
-    if (cap.on) x = cap(x);
-    if (bias) x = fmaf(-slope[nt][c], fabsf(static_cast<float>(pos[i][k] - j)), x);
-    return loaded && j >= lo[i][k] && j < hi[i][k] ? x : -INFINITY;
+
+  // A sub-tile's scores (log2 units) of keys kbase + ka and kbase + ka + 8
+  // become logits; keys past the loaded ones (`v` of them) or outside the
+  // column's interval become -inf. Most sub-tiles lie inside every row's interval.
+  __device__ __forceinline__ void logits(float (&x)[NT][2][2], int kbase, int ka, int v, const Cap &cap, bool bias) const {
+    if (cap.on) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) x[nt][c][i] = cap(x[nt][c][i]);
+    }
+    if (bias) {
+      const float away = static_cast<float>(pos0 - kbase) - static_cast<float>(ka);  // row 0 from key kbase + ka
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float d = MULTI ? away + row[MULTI ? nt : 0][MULTI ? c : 0] : away;
+          x[nt][c][0] = fmaf(-slope[nt][c], fabsf(d), x[nt][c][0]);
+          x[nt][c][1] = fmaf(-slope[nt][c], fabsf(d - 8.f), x[nt][c][1]);
+        }
+    }
+    if (v < kSubKeys || kbase < a_lo || kbase + kSubKeys > a_hi) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int k = ka + 8 * i, j = kbase + k;
+            if (!(k < v && j >= lo[MULTI ? nt : 0][MULTI ? c : 0] && j < hi[MULTI ? nt : 0][MULTI ? c : 0]))
+              x[nt][c][i] = -INFINITY;
+          }
+    }
   }
 };
 

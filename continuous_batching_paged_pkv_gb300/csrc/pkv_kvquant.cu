@@ -660,14 +660,21 @@ __global__ void __launch_bounds__(NW * 32, 1)
       // by the lazy margin
       float x[NT][2][2];
       bool need = false;
+      if constexpr (MOD) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            x[nt][c][0] = sacc[nt][c] * sl2c[nt][c];
+            x[nt][c][1] = sacc[nt][c + 2] * sl2c[nt][c];
+          }
+        tm.logits(x, kbase, ka, v, cap, bias);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if constexpr (MOD) {
-            x[nt][c][0] = tm.logit(sacc[nt][c] * sl2c[nt][c], kbase + ka, nt, c, ka < v, cap, bias);
-            x[nt][c][1] = tm.logit(sacc[nt][c + 2] * sl2c[nt][c], kbase + kb, nt, c, kb < v, cap, bias);
-          } else {
+          if constexpr (!MOD) {
             const int vis = MULTI ? min(v, vis0 + static_cast<int>((colrow >> (8 * (nt * 2 + c))) & 0xFF)) : v;
             x[nt][c][0] = ka < vis ? sacc[nt][c] * sl2c[nt][c] : -INFINITY;
             x[nt][c][1] = kb < vis ? sacc[nt][c + 2] * sl2c[nt][c] : -INFINITY;
