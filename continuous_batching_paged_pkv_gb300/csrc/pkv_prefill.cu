@@ -41,6 +41,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
 #include "pkv_score_mod.cuh"
@@ -323,13 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const bool row_valid = mrow < G * P && pos < rows;
     const int p_row = L - n + pos0 + pos;  // last visible key of this row (inclusive)
     const float sl2 = a.scale_log2;
-    int lo = 0, hi = 0;  // visible keys of this row (modified scores)
-    float slope = 0.f;   // its bias per key, log2 units
-    const Cap cap((MODE & kModCap) ? a.softcap : 0.f);
-    if constexpr (MODE != kModNone) {
-      if (row_valid) row_sees(a, static_cast<int64_t>(row0) + pos0 + pos, p_row, L, lo, hi);
-      if constexpr ((MODE & kModBias) != 0) slope = __ldg(a.alibi_slopes + g * G + hh) * 1.4426950408889634f;
-    }
+    int lo = 0, hi = INT32_MAX;  // visible keys of this row (modified scores); rows that are not stored mask nothing
+    if (MODE != kModNone && row_valid) row_sees(a, static_cast<int64_t>(row0) + pos0 + pos, p_row, L, lo, hi);
+    TileScores<MODE> ts(a, g * G + hh);
     float m_used = -INFINITY;  // log2 units
     bool ok = true;
     for (int j = 0; j < ntiles; ++j) {
@@ -341,13 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_base + s * 128 + c * 32, sv[c]);
       tmem_wait_ld();
       const int kt0 = base + j * kKeysPerTile;
-      if constexpr ((MODE & (kModCap | kModBias)) != 0)
-        tile_logits<MODE>(sv, sl2, cap, slope, p_row - kt0,
-                          a.key_end != nullptr && __any_sync(kFull, min(hi, kt0 + kKeysPerTile) > p_row + 1));
       // Edges: only tiles that reach past some row's keys need a mask (causal and ragged; both ends with modified scores).
+      float mx;
       if constexpr (MODE != kModNone) {
-        const int first = lo - kt0, lim = hi - 1 - kt0;
-        if (!__all_sync(kFull, first <= 0 && lim >= kKeysPerTile - 1)) mask_tile(sv, first, lim);
+        mx = ts.top(sv, p_row - kt0, lo - kt0, hi - 1 - kt0);
       } else {
         const int lim = min(p_row, kv_end - 1) - kt0;
         if (!__all_sync(kFull, lim >= kKeysPerTile - 1)) {
@@ -357,15 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             for (int i = 0; i < 32; ++i)
               if (c * 32 + i > lim) sv[c][i] = kNegInfBits;
         }
+        mx = tile_max(sv) * sl2;
       }
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(sv[c][i]));
-      // sv holds raw products, or logits where the scores were capped or biased
-      const float unit = (MODE & (kModCap | kModBias)) ? 1.f : sl2;
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * unit;
       const float m_new = fmaxf(m_used, mx);
       // before a row's first visible key there is nothing to rescale
       const bool fresh = MODE != kModNone ? m_used == -INFINITY : j == 0;
@@ -394,15 +382,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         tmem_st16(tmem + lane_base + kLCol, lv);
       }
       const float nm = MODE != kModNone && m_used == -INFINITY ? 0.f : -m_used;
+      auto weigh = [&](auto is_raw) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          pk[i] = pack_bf16x2(ex2_approx(fmaf(__uint_as_float(sv[c][2 * i]), unit, nm)),
-                              ex2_approx(fmaf(__uint_as_float(sv[c][2 * i + 1]), unit, nm)));
-        tmem_st16(tmem + lane_base + s * 128 + c * 16, pk);
-      }
+          for (int i = 0; i < 16; ++i) {
+            float x0, x1;
+            ts.template exponents<decltype(is_raw)::value>(x0, x1, sv, c * 32 + 2 * i, nm);
+            pk[i] = pack_bf16x2(ex2_approx(x0), ex2_approx(x1));
+          }
+          tmem_st16(tmem + lane_base + s * 128 + c * 16, pk);
+        }
+      };
+      if ((MODE & (kModCap | kModBias)) == 0 || ts.raw)
+        weigh(std::true_type{});
+      else
+        weigh(std::false_type{});
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(bar + kPReady + s);

@@ -53,6 +53,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
 #include "pkv_score_mod.cuh"
@@ -206,6 +208,12 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
   }
   const int base = kv_begin & ~(kSubKeys - 1);
   const int ntiles = (kv_end - base + kKeysPerTile - 1) / kKeysPerTile;  // 0: no row of the pair sees a key
+  // Tile taken at step j. A distance bias makes the nearest keys' logits the
+  // largest, so those variants go from the last tile to the first: going up, the
+  // running max would grow by slope * 128 with every tile and O be rescaled at
+  // each (a capped-free 2048-row chunk at context 8192: 323 us going up).
+  constexpr bool kDown = (MODE & kModBias) != 0;
+  auto tile_at = [&](int j) { return kDown ? ntiles - 1 - j : j; };
   const int32_t *bt_row = a.block_tables + static_cast<int64_t>(slot) * a.max_blocks_per_slot;
 
   if (threadIdx.x == 0) {
@@ -243,12 +251,12 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
     // pool: 0 when outside it, the status word reports it) only when that
     // group comes into use, so no block-table latency is ever waited on.
     auto group_ids = [&](int t0) -> int {
-      const int key = base + (t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
-      return key < kv_end ? __ldg(bt_row + key / a.block_size) : 0;
+      const int key = base + tile_at(t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
+      return key >= base && key < kv_end ? __ldg(bt_row + key / a.block_size) : 0;
     };
     auto group_rows = [&](int t0, int blk) -> int {
-      const int key = base + (t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
-      if (key >= kv_end) return 0;
+      const int key = base + tile_at(t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
+      if (key < base || key >= kv_end) return 0;
       if (blk < 0 || blk >= a.num_blocks) {
         if (a.status) atomicOr(a.status, PKV_DEV_BAD_BLOCK);
         return 0;
@@ -279,7 +287,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
         rows_cur = group_rows(j, ids_next);
         ids_next = group_ids(j + 4);
       }
-      const int kt0 = base + j * kKeysPerTile;
+      const int kt0 = base + tile_at(j) * kKeysPerTile;
       const int vs = min(kSubPerTile, (kv_end - kt0 + kSubKeys - 1) / kSubKeys);  // sub-tiles with a visible key
       const uint32_t kv_full = cluster_addr(bar + kKVFull + s, 0);
       // The pair loads 4 boxes per visible sub-tile: two K halves (one CTA) and two V halves (one each).
@@ -333,7 +341,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
         // P_j written by all eight softmax warps of the pair; V_j has landed (S_j used K_j of the same stage).
         if (!wait_or_abort<true>(bar + kPReady + sp, (j / kSBufs) & 1, abort_flag)) break;
         tc_fence_after();
-        const int valid = min(kKeysPerTile, kv_end - base - j * kKeysPerTile);
+        const int valid = min(kKeysPerTile, kv_end - base - tile_at(j) * kKeysPerTile);
         const int ksteps = (valid + kSubKeys - 1) / kSubKeys;
         const uint32_t v_base = smem_addr(sKV + (j % kStages) * Lay::kStageBytes + Lay::kKBytes);
         for (int ks = 0; ks < ksteps; ++ks) {
@@ -357,13 +365,10 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
     const int pos = mrow / G;
     const int p_row = L - n + pos0 + pos;  // last visible key of this row (inclusive)
     const float sl2 = a.scale_log2;
-    int lo = 0, hi = 0;  // visible keys of this row (modified scores)
-    float slope = 0.f;   // its bias per key, log2 units
-    const Cap cap((MODE & kModCap) ? a.softcap : 0.f);
-    if constexpr (MODE != kModNone) {
-      if (mrow < G * P && pos < rows) row_sees(a, static_cast<int64_t>(row0) + pos0 + pos, p_row, L, lo, hi);
-      if constexpr ((MODE & kModBias) != 0) slope = __ldg(a.alibi_slopes + g * G + mrow % G) * 1.4426950408889634f;
-    }
+    int lo = 0, hi = INT32_MAX;  // visible keys of this row (modified scores); rows that are not stored mask nothing
+    const bool stored = mrow < G * P && pos < rows;
+    if (MODE != kModNone && stored) row_sees(a, static_cast<int64_t>(row0) + pos0 + pos, p_row, L, lo, hi);
+    TileScores<MODE> ts(a, g * G + mrow % G);
     const uint32_t p_ready0 = cluster_addr(bar + kPReady, 0);
     float m_used = -INFINITY;  // log2 units
     bool ok = true;
@@ -376,14 +381,11 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_base + s * 128 + c * 32, sv[c]);
       tmem_wait_ld();
-      const int kt0 = base + j * kKeysPerTile;
-      if constexpr ((MODE & (kModCap | kModBias)) != 0)
-        tile_logits<MODE>(sv, sl2, cap, slope, p_row - kt0,
-                          a.key_end != nullptr && __any_sync(kFull, min(hi, kt0 + kKeysPerTile) > p_row + 1));
+      const int tile_j = tile_at(j), kt0 = base + tile_j * kKeysPerTile;
       // Edges: only tiles that reach past some row's keys need a mask (causal and ragged; both ends with modified scores).
+      float mx;
       if constexpr (MODE != kModNone) {
-        const int first = lo - kt0, lim = hi - 1 - kt0;
-        if (!__all_sync(kFull, first <= 0 && lim >= kKeysPerTile - 1)) mask_tile(sv, first, lim);
+        mx = ts.top(sv, p_row - kt0, lo - kt0, hi - 1 - kt0);
       } else {
         const int lim = min(p_row, kv_end - 1) - kt0;
         if (!__all_sync(kFull, lim >= kKeysPerTile - 1)) {
@@ -393,17 +395,8 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
             for (int i = 0; i < 32; ++i)
               if (c * 32 + i > lim) sv[c][i] = kNegInfBits;
         }
+        mx = tile_max(sv) * sl2;
       }
-      // Row max: three-input max, four independent chains.
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 32; i += 2)
-          mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(sv[c][i]), __uint_as_float(sv[c][i + 1]));
-      // sv holds raw products, or logits where the scores were capped or biased
-      const float unit = (MODE & (kModCap | kModBias)) ? 1.f : sl2;
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * unit;
       const float m_new = fmaxf(m_used, mx);
       // before a row's first visible key there is nothing to rescale
       const bool fresh = MODE != kModNone ? m_used == -INFINITY : j == 0;
@@ -428,25 +421,31 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
         }
       }
       const float nm = MODE != kModNone && m_used == -INFINITY ? 0.f : -m_used;
+      auto weigh = [&](auto is_raw) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float x0, x1;
-          fma2(x0, x1, __uint_as_float(sv[c][2 * i]), __uint_as_float(sv[c][2 * i + 1]), unit, unit, nm, nm);
-          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-          add2(l_sum, l_odd, p0, p1);
-          pk[i] = pack_bf16x2(p0, p1);
+          for (int i = 0; i < 16; ++i) {
+            float x0, x1;
+            ts.template exponents<decltype(is_raw)::value>(x0, x1, sv, c * 32 + 2 * i, nm);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            add2(l_sum, l_odd, p0, p1);
+            pk[i] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(tmem + lane_base + s * 128 + c * 16, pk);
         }
-        tmem_st16(tmem + lane_base + s * 128 + c * 16, pk);
-      }
+      };
+      if ((MODE & (kModCap | kModBias)) == 0 || ts.raw)
+        weigh(std::true_type{});
+      else
+        weigh(std::false_type{});
       // Zero this CTA's V rows past the last visible key inside the final 16-key
       // step, and before the first visible one inside the first: a block may
       // hold stale or NaN rows there, and 0 * NaN would reach O. The tile's data
       // has landed (S_j exists).
-      bool wrote_v = j == ntiles - 1;
-      if (j == ntiles - 1) {
+      bool wrote_v = tile_j == ntiles - 1;
+      if (tile_j == ntiles - 1) {
         const int valid = kv_end - kt0;
         const int tail = (kSubKeys - valid % kSubKeys) % kSubKeys;
         if (tail) {
@@ -456,8 +455,8 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
           fence_proxy_async_smem();
         }
       }
-      if (MODE != kModNone && j == 0 && kv_begin > base) {
-        uint8_t *sV = sKV + Lay::kKBytes;
+      if (MODE != kModNone && tile_j == 0 && kv_begin > base) {
+        uint8_t *sV = sKV + (j % kStages) * Lay::kStageBytes + Lay::kKBytes;
         for (int i = threadIdx.x; i < (kv_begin - base) * 8; i += 128)
           *reinterpret_cast<uint4 *>(sV + i * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
@@ -483,7 +482,6 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
       constexpr int kRowBytes = D * 2, kChunks = kRowBytes / 16;
       if (!a.out_on_host) {
         // each thread stores its own row, 64 bytes per TMEM load (the loads are warp-wide)
-        const bool row_valid = mrow < G * P && pos < rows;
         uint4 *orow = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) +
                                                 (static_cast<size_t>(row0 + pos0 + pos) * a.num_q_heads + g * G +
                                                  mrow % G) * D);
@@ -492,7 +490,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
           uint32_t ov[32];
           tmem_ld32(tmem + lane_base + kOCol + c * 32, ov);
           tmem_wait_ld();
-          if (row_valid) {
+          if (stored) {
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)

@@ -68,44 +68,6 @@ __device__ __forceinline__ void rows_see(const StepArgs &a, int64_t row0, int po
   __syncthreads();
 }
 
-// One tile's scores of a row (raw products) become logits in log2 units.
-// `away`: position of the row minus the tile's first key; `ahead`: the row may
-// see keys past its own position, so the distance needs its absolute value.
-template <int MODE>
-__device__ __forceinline__ void tile_logits(uint32_t (&sv)[4][32], float sl2, const Cap &cap, float slope, int away,
-                                            bool ahead) {
-  const float kk = sl2 * cap.k;
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      float x = __uint_as_float(sv[c][i]);
-      if constexpr ((MODE & kModCap) != 0)
-        x = fmaf(cap.c2, rcp_approx(1.f + ex2_approx(x * kk)), cap.c);
-      else
-        x *= sl2;
-      sv[c][i] = __float_as_uint(x);
-    }
-  if constexpr ((MODE & kModBias) != 0) {
-    const float from = static_cast<float>(away);
-    if (ahead) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          sv[c][i] = __float_as_uint(
-              fmaf(-slope, fabsf(from - static_cast<float>(c * 32 + i)), __uint_as_float(sv[c][i])));
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          sv[c][i] =
-              __float_as_uint(fmaf(-slope, from - static_cast<float>(c * 32 + i), __uint_as_float(sv[c][i])));
-    }
-  }
-}
-
 // Scores outside [first, last] of the tile's 128 keys become -inf.
 __device__ __forceinline__ void mask_tile(uint32_t (&sv)[4][32], int first, int last) {
 #pragma unroll
@@ -114,6 +76,132 @@ __device__ __forceinline__ void mask_tile(uint32_t (&sv)[4][32], int first, int 
     for (int i = 0; i < 32; ++i)
       if (c * 32 + i < first || c * 32 + i > last) sv[c][i] = 0xff800000u;
 }
+
+__device__ __forceinline__ float score(const uint32_t (&sv)[4][32], int i) { return __uint_as_float(sv[i >> 5][i & 31]); }
+
+// Largest of a row's 128 scores, or the smallest: three-input maxima, four independent chains.
+template <bool MIN = false>
+__device__ __forceinline__ float tile_max(const uint32_t (&sv)[4][32]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 128; i += 2)
+    m[(i >> 1) & 3] = MIN ? max3(m[(i >> 1) & 3], -score(sv, i), -score(sv, i + 1))
+                          : max3(m[(i >> 1) & 3], score(sv, i), score(sv, i + 1));
+  const float r = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  return MIN ? -r : r;
+}
+
+// Modified scores in a chunk kernel's softmax thread: one row, tile by tile.
+// The scores of a tile arrive as raw products; top() gives a reference for the
+// tile's running max (log2 units) and exponents() the pairs 2^x is taken of.
+//
+// A tile that every row of the warp sees whole (most are) stays raw: the cap is
+// y P(y^2) with y = raw r, |y| <= 0.55 and P of degree 3, fitted here to the
+// least largest error of y P(y^2) (2^-21.5 in fp32 arithmetic), its coefficients
+// scaled so that a score costs 5 operations, the last of which also subtracts the
+// reference (2^x and 1/x would be two SFU operations of each score beside the
+// softmax's own 2^x); the bias is one more. The reference is then the largest raw
+// score's logit plus the tile's largest bias: an upper bound at most kSpread above
+// the row's largest logit. Weights then start at 2^-80 instead of 1, which fp32
+// and bf16 hold as exactly; only weights under 2^-46 of the row's largest are lost.
+// Every other tile has its logits written out, masked, and their maximum taken.
+template <int MODE>
+struct TileScores {
+  static constexpr bool kCap = (MODE & kModCap) != 0, kBias = (MODE & kModBias) != 0;
+  static constexpr float kSpread = 80.f;  // log2 units
+  Cap cap;
+  float sl2, slope;  // scale and bias per key in log2 units
+  float r, p0, p1, p2, p3;
+  bool poly, flat;   // warp-uniform: the cap's r leaves the coefficients in range; a tile's biases stay within kSpread
+  // of the current tile
+  bool raw;    // warp-uniform
+  float near;  // bias of its first key
+
+  __device__ __forceinline__ TileScores(const StepArgs &a, int head)
+      : cap(kCap ? a.softcap : 0.f), sl2(a.scale_log2), slope(0.f), r(0.f), raw(true), near(0.f) {
+    if constexpr (kBias) slope = __ldg(a.alibi_slopes + head) * 1.4426950408889634f;
+    flat = !kBias || __all_sync(0xffffffffu, fabsf(slope) * 127.f <= kSpread);
+    if constexpr (kCap) {
+      r = sl2 / cap.c;
+      poly = r > 0x1p-17f && r < 0x1p17f;
+      const float u = r * r, c = cap.c * r;
+      p0 = 0.9999952912330627f * c;
+      p1 = -0.3331194519996643f * c * u;
+      p2 = 0.13069017231464386f * c * u * u;
+      p3 = -0.04152349755167961f * c * u * u * u;
+    }
+  }
+
+  // `away`: position of the row minus the tile's first key; keys [first, last] of the tile are the row's.
+  __device__ __forceinline__ float top(uint32_t (&sv)[4][32], int away, int first, int last) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    const bool inside = __all_sync(kAll, first <= 0 && last >= 127);
+    if constexpr (!kCap && !kBias) {
+      if (!inside) mask_tile(sv, first, last);
+      return tile_max(sv) * sl2;
+    } else {
+      // rows that see keys past their own position take the distance's absolute value
+      const bool ahead = kBias && __any_sync(kAll, min(last, 127) > away);
+      float mx = 0.f;
+      raw = inside && flat && !ahead && (!kCap || poly);
+      if (kBias) near = -slope * static_cast<float>(away);
+      if (raw) {
+        mx = tile_max(sv);
+        if constexpr (kCap) raw = __all_sync(kAll, fmaxf(mx, -tile_max<true>(sv)) * r <= 0.55f);
+      }
+      if (raw) {
+        const float t = kCap ? cap(mx * sl2) : mx * sl2;
+        return kBias ? t + fmaxf(near, fmaf(slope, 127.f, near)) : t;
+      }
+      const float from = static_cast<float>(away);
+#pragma unroll
+      for (int i = 0; i < 128; i += 2) {
+        float x0 = score(sv, i), x1 = score(sv, i + 1);
+        if constexpr (kCap) {
+          x0 = cap(x0 * sl2);
+          x1 = cap(x1 * sl2);
+        }
+        if constexpr (kBias) {
+          const float unit = kCap ? 1.f : sl2;
+          float b0, b1;
+          if (ahead) {
+            b0 = -slope * fabsf(from - static_cast<float>(i));
+            b1 = -slope * fabsf(from - static_cast<float>(i + 1));
+          } else {
+            fma2(b0, b1, slope, slope, static_cast<float>(i), static_cast<float>(i + 1), near, near);
+          }
+          fma2(x0, x1, x0, x1, unit, unit, b0, b1);
+        }
+        sv[i >> 5][i & 31] = __float_as_uint(x0);
+        sv[(i + 1) >> 5][(i + 1) & 31] = __float_as_uint(x1);
+      }
+      if (!inside) mask_tile(sv, first, last);
+      return tile_max(sv);
+    }
+  }
+
+  // x0, x1: exponents of keys i and i + 1 less the reference (nm = -reference).
+  template <bool RAW>
+  __device__ __forceinline__ void exponents(float &x0, float &x1, const uint32_t (&sv)[4][32], int i, float nm) const {
+    const float s0 = score(sv, i), s1 = score(sv, i + 1);
+    float b0 = nm, b1 = nm;
+    if constexpr (RAW && kBias) {
+      const float n = near + nm;
+      fma2(b0, b1, slope, slope, static_cast<float>(i), static_cast<float>(i + 1), n, n);
+    }
+    if constexpr (RAW && kCap) {
+      float u0, u1, f0 = p3, f1 = p3;
+      mul2(u0, u1, s0, s1, s0, s1);
+      fma2(f0, f1, f0, f1, u0, u1, p2, p2);
+      fma2(f0, f1, f0, f1, u0, u1, p1, p1);
+      fma2(f0, f1, f0, f1, u0, u1, p0, p0);
+      fma2(x0, x1, s0, s1, f0, f1, b0, b1);
+    } else {
+      const float unit = RAW ? sl2 : 1.f;
+      fma2(x0, x1, s0, s1, unit, unit, b0, b1);
+    }
+  }
+};
 
 }  // namespace
 }  // namespace pkv
