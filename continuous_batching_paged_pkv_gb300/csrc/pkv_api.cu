@@ -278,6 +278,7 @@ pkv_status pkv::attention(const void *q, const int32_t *cu_seqlens_q, int32_t nu
   cudaError_t e = side ? cudaEventRecord(side->fork, st) : cudaSuccess;
   if (e == cudaSuccess)
     e = head_dim == 128 ? pkv::launch_prefill_pair(a, tq, tks, tv, rpt, info->num_prefill_items, pre, beside, st)
+        : mod           ? pkv::launch_prefill_mod(a, tq, tk, tv, rpt, info->num_prefill_items, pre, st)
                         : pkv::launch_prefill(a, tq, rpt, info->num_prefill_items, pre, st);
   cudaStream_t dst = side ? side->stream : st;
   if (e == cudaSuccess && side) e = cudaStreamWaitEvent(side->stream, side->fork, 0);
@@ -468,6 +469,7 @@ static pkv_status attention_quant(int32_t bits, const void *q, const int32_t *cu
                              static_cast<int64_t>(sb), info->num_scratch_items, scr, bits, st);
     if (e == cudaSuccess)
       e = head_dim == 128 ? pkv::launch_prefill_pair(c, tq, tk, tv, rpt, info->num_prefill_items, pre, false, st)
+          : mod           ? pkv::launch_prefill_mod(c, tq, tk, tv, rpt, info->num_prefill_items, pre, st)
                           : pkv::launch_prefill(c, tq, rpt, info->num_prefill_items, pre, st);
   }
   cudaStream_t dst = side ? side->stream : st;

@@ -125,6 +125,10 @@ cudaError_t launch_widen_quant(const StepArgs &a, const void *k_codes, const voi
 
 cudaError_t launch_prefill(const StepArgs &a, const CUtensorMap &tmap_q, int32_t rows_per_tile,
                            int32_t num_items, const int32_t *items, cudaStream_t stream);
+// head_dim 64 with modified scores.
+cudaError_t launch_prefill_mod(const StepArgs &a, const CUtensorMap &tmap_q, const CUtensorMap &tmap_k,
+                               const CUtensorMap &tmap_v, int32_t rows_per_tile, int32_t num_items,
+                               const int32_t *items, cudaStream_t stream);
 // head_dim 128: items are tile pairs, run by clusters of two CTAs.
 // `beside_decode`: the step also has decode rows, whose kernel runs at the
 // same time; the chunk kernel then keeps fewer K/V stages so that a decode CTA

@@ -41,11 +41,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
-#include <type_traits>
-
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
-#include "pkv_score_mod.cuh"
 
 namespace pkv {
 namespace {
@@ -112,7 +109,7 @@ __device__ __forceinline__ bool warp_wait_or_abort(uint64_t *bar, uint32_t parit
   return __all_sync(kFull, wait_or_abort(bar, parity, abort));
 }
 
-template <int D, int MODE>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                                               const StepArgs a,
                                                               const int32_t *__restrict__ items,
@@ -153,16 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
   const int pos0 = tile * P;                 // first query row of the tile within the segment
   const int rows = min(P, n - pos0);         // query positions present in this tile
-  // keys [kv_begin, kv_end) are visible to some row; tiles start at their first 16-key sub-tile
-  int kv_begin = 0, kv_end = L - n + pos0 + rows;
-  if constexpr (MODE != kModNone) {
-    int *u = const_cast<int *>(abort_flag) + 1;
-    rows_see(a, static_cast<int64_t>(row0) + pos0, L - n + pos0, rows, L, u);
-    kv_begin = min(u[0], u[1]);
-    kv_end = u[1];
-  }
-  const int base = kv_begin & ~(kSubKeys - 1);
-  const int ntiles = (kv_end - base + kKeysPerTile - 1) / kKeysPerTile;  // 0: no row of the tile sees a key
+  const int kv_end = L - n + pos0 + rows;    // keys [0, kv_end) are visible to some row
+  const int ntiles = (kv_end + kKeysPerTile - 1) / kKeysPerTile;
   const int32_t *bt_row = a.block_tables + static_cast<int64_t>(slot) * a.max_blocks_per_slot;
 
   if (threadIdx.x == 0) {
@@ -212,11 +201,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // pool: -1 when outside it, the status word reports it) only when that
     // group comes into use, so no block-table latency is ever waited on.
     auto group_ids = [&](int t0) -> int {
-      const int key = base + (t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
+      const int key = (t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
       return key < kv_end ? __ldg(bt_row + key / a.block_size) : 0;
     };
     auto group_rows = [&](int t0, int blk) -> int {
-      const int key = base + (t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
+      const int key = (t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
       if (key >= kv_end) return 0;
       if (blk < 0 || blk >= a.num_blocks) {
         if (a.status && warp == 0) atomicOr(a.status, PKV_DEV_BAD_BLOCK);
@@ -241,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         rows_cur = group_rows(j, ids_next);
         ids_next = group_ids(j + 4);
       }
-      const int kt0 = base + j * kKeysPerTile;
+      const int kt0 = j * kKeysPerTile;
       const uint32_t sK = smem_addr(sKV + s * Lay::kStageBytes);
       const uint32_t sV = sK + Lay::kKVBytes;
 #pragma unroll 4
@@ -250,8 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const int r = ((k & 1) << 3) + (p >> 3);
         const int urow = __shfl_sync(kFull, rows_cur, (j & 3) * 8 + u);
         if (h < H) {
-          const int key = kt0 + u * kSubKeys + r;
-          const bool valid = key < kv_end && (MODE == kModNone || key >= kv_begin) && urow >= 0;
+          const bool valid = kt0 + u * kSubKeys + r < kv_end && urow >= 0;
           const int64_t off = (static_cast<int64_t>(valid ? urow : 0) + (valid ? r : 0)) * row_bytes + h * 128 + c * 16;
           const uint32_t dst = (t ? sV : sK) + h * Lay::kKVHalf + (u * kSubKeys + r) * 128 + ((c ^ (r & 7)) << 4);
           cp_async_16_zfill(dst, (t ? vp : kp) + off, valid);
@@ -266,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
     }
     cp_async_wait<0>();  // also on abort: no copy may still target shared memory at exit
-    if (ok && ntiles > 0) {
+    if (ok) {
       fence_proxy_async_smem();
       mbar_arrive(bar + kKVFull + (ntiles - 1) % kStages);
     }
@@ -282,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const int sp = jj & 1;
         if (!wait_or_abort(bar + kPReady + sp, (jj >> 1) & 1, abort_flag)) return false;
         tc_fence_after();
-        const int valid = min(kKeysPerTile, kv_end - base - jj * kKeysPerTile);
+        const int valid = min(kKeysPerTile, kv_end - jj * kKeysPerTile);
         const int ksteps = (valid + kSubKeys - 1) / kSubKeys;
         const uint32_t v_base = smem_addr(sKV + (jj % kStages) * Lay::kStageBytes + Lay::kKVBytes);
         for (int ks = 0; ks < ksteps; ++ks) {
@@ -312,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         tc_commit(bar + kSFull + s);
         if (j >= 1 && !(ok = issue_pv(j - 1))) break;
       }
-      if (ok && ntiles > 0) issue_pv(ntiles - 1);
+      if (ok) issue_pv(ntiles - 1);
       tc_commit(bar + kDrain);
       if (!wait_or_abort(bar + kDrain, 0, abort_flag) && a.status) atomicOr(a.status, PKV_DEV_TIMEOUT);
     }
@@ -325,9 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const bool row_valid = mrow < G * P && pos < rows;
     const int p_row = L - n + pos0 + pos;  // last visible key of this row (inclusive)
     const float sl2 = a.scale_log2;
-    int lo = 0, hi = INT32_MAX;  // visible keys of this row (modified scores); rows that are not stored mask nothing
-    if (MODE != kModNone && row_valid) row_sees(a, static_cast<int64_t>(row0) + pos0 + pos, p_row, L, lo, hi);
-    TileScores<MODE> ts(a, g * G + hh);
     float m_used = -INFINITY;  // log2 units
     bool ok = true;
     for (int j = 0; j < ntiles; ++j) {
@@ -338,27 +323,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_base + s * 128 + c * 32, sv[c]);
       tmem_wait_ld();
-      const int kt0 = base + j * kKeysPerTile;
-      // Edges: only tiles that reach past some row's keys need a mask (causal and ragged; both ends with modified scores).
-      float mx;
-      if constexpr (MODE != kModNone) {
-        mx = ts.top(sv, p_row - kt0, lo - kt0, hi - 1 - kt0);
-      } else {
-        const int lim = min(p_row, kv_end - 1) - kt0;
-        if (!__all_sync(kFull, lim >= kKeysPerTile - 1)) {
+      // Causal / ragged edge: only tiles that reach past some row's last key need a mask.
+      const int lim = min(p_row, kv_end - 1) - j * kKeysPerTile;
+      if (!__all_sync(kFull, lim >= kKeysPerTile - 1)) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c * 32 + i > lim) sv[c][i] = kNegInfBits;
-        }
-        mx = tile_max(sv) * sl2;
+          for (int i = 0; i < 32; ++i)
+            if (c * 32 + i > lim) sv[c][i] = kNegInfBits;
       }
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(sv[c][i]));
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
       const float m_new = fmaxf(m_used, mx);
-      // before a row's first visible key there is nothing to rescale
-      const bool fresh = MODE != kModNone ? m_used == -INFINITY : j == 0;
-      const bool need = !fresh && m_new > m_used + kRescaleThreshold;
-      if (fresh) m_used = m_new;
+      const bool need = j > 0 && m_new > m_used + kRescaleThreshold;
+      if (j == 0) m_used = m_new;
       if (__any_sync(kFull, need)) {
         // O and l must hold tile j-1's products before they are rescaled.
         if (!(ok = warp_wait_or_abort(bar + kPVDone + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort_flag))) break;
@@ -381,37 +363,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         for (int i = 0; i < 16; ++i) lv[i] = __float_as_uint(__uint_as_float(lv[i]) * corr);
         tmem_st16(tmem + lane_base + kLCol, lv);
       }
-      const float nm = MODE != kModNone && m_used == -INFINITY ? 0.f : -m_used;
-      auto weigh = [&](auto is_raw) {
+      const float nm = -m_used;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x0, x1;
-            ts.template exponents<decltype(is_raw)::value>(x0, x1, sv, c * 32 + 2 * i, nm);
-            pk[i] = pack_bf16x2(ex2_approx(x0), ex2_approx(x1));
-          }
-          tmem_st16(tmem + lane_base + s * 128 + c * 16, pk);
-        }
-      };
-      if ((MODE & (kModCap | kModBias)) == 0 || ts.raw)
-        weigh(std::true_type{});
-      else
-        weigh(std::false_type{});
+        for (int i = 0; i < 16; ++i)
+          pk[i] = pack_bf16x2(ex2_approx(fmaf(__uint_as_float(sv[c][2 * i]), sl2, nm)),
+                              ex2_approx(fmaf(__uint_as_float(sv[c][2 * i + 1]), sl2, nm)));
+        tmem_st16(tmem + lane_base + s * 128 + c * 16, pk);
+      }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(bar + kPReady + s);
     }
-    if (ok && (ntiles == 0 ||
-               warp_wait_or_abort(bar + kPVDone + ((ntiles - 1) & 1), ((ntiles - 1) >> 1) & 1, abort_flag))) {
+    if (ok && warp_wait_or_abort(bar + kPVDone + ((ntiles - 1) & 1), ((ntiles - 1) >> 1) & 1, abort_flag)) {
       tc_fence_after();
       uint32_t lv[16];
       tmem_ld16(tmem + lane_base + kLCol, lv);
       tmem_wait_ld();
       const float inv = 1.f / __uint_as_float(lv[0]);
-      // a row that sees nothing gives zeros, whatever O and l hold (an empty tile's were never written)
-      const bool none = MODE != kModNone && lo >= hi;
       __nv_bfloat16 *orow = reinterpret_cast<__nv_bfloat16 *>(a.out) +
                             (static_cast<size_t>(row0 + pos0 + pos) * a.num_q_heads + g * G + hh) * D;
 #pragma unroll
@@ -423,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            pk[i] = none ? 0u : pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
+            pk[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
           uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 32);
 #pragma unroll
           for (int v = 0; v < 4; ++v) dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
@@ -441,14 +412,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
 }
 
-template <int D, int MODE>
+template <int D>
 cudaError_t launch_prefill_t(const StepArgs &a, const CUtensorMap &tq, int32_t rows_per_tile, int32_t num_items,
                              const int32_t *items, cudaStream_t stream) {
   constexpr int smem = PrefillLayout<D>::kSmem;
   static std::atomic<uint64_t> configured{0};  // one bit per device
-  if (const cudaError_t e = allow_smem_once(prefill_kernel<D, MODE>, smem, configured); e != cudaSuccess) return e;
+  if (const cudaError_t e = allow_smem_once(prefill_kernel<D>, smem, configured); e != cudaSuccess) return e;
   dim3 grid(static_cast<unsigned>(num_items), static_cast<unsigned>(a.num_kv_heads));
-  return launch_pdl(prefill_kernel<D, MODE>, grid, dim3(kThreads), smem, stream, tq, a, items, rows_per_tile);
+  return launch_pdl(prefill_kernel<D>, grid, dim3(kThreads), smem, stream, tq, a, items, rows_per_tile);
 }
 
 }  // namespace
@@ -457,15 +428,7 @@ cudaError_t launch_prefill(const StepArgs &a, const CUtensorMap &tq, int32_t row
                            const int32_t *items, cudaStream_t stream) {
   if (num_items <= 0) return cudaSuccess;
   if (a.head_dim != 64) return cudaErrorInvalidValue;  // head_dim 128 runs on SM pairs
-  switch (mode_of(a)) {
-    case kModNone: return launch_prefill_t<64, kModNone>(a, tq, rows_per_tile, num_items, items, stream);
-    case kModMask: return launch_prefill_t<64, kModMask>(a, tq, rows_per_tile, num_items, items, stream);
-    case kModMask | kModCap: return launch_prefill_t<64, kModMask | kModCap>(a, tq, rows_per_tile, num_items, items, stream);
-    case kModMask | kModBias:
-      return launch_prefill_t<64, kModMask | kModBias>(a, tq, rows_per_tile, num_items, items, stream);
-    default:
-      return launch_prefill_t<64, kModMask | kModCap | kModBias>(a, tq, rows_per_tile, num_items, items, stream);
-  }
+  return launch_prefill_t<64>(a, tq, rows_per_tile, num_items, items, stream);
 }
 
 }  // namespace pkv

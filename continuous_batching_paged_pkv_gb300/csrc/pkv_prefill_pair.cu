@@ -377,11 +377,11 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
       const int s = j % kSBufs;
       if (!(ok = warp_wait_or_abort(bar + kSFull + s, (j / kSBufs) & 1, abort_flag))) break;
       tc_fence_after();
+      const int tile_j = tile_at(j), kt0 = base + tile_j * kKeysPerTile;
       uint32_t sv[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_base + s * 128 + c * 32, sv[c]);
       tmem_wait_ld();
-      const int tile_j = tile_at(j), kt0 = base + tile_j * kKeysPerTile;
       // Edges: only tiles that reach past some row's keys need a mask (causal and ragged; both ends with modified scores).
       float mx;
       if constexpr (MODE != kModNone) {
@@ -422,13 +422,14 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
       }
       const float nm = MODE != kModNone && m_used == -INFINITY ? 0.f : -m_used;
       auto weigh = [&](auto is_raw) {
+        float b0, b1;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float x0, x1;
-            ts.template exponents<decltype(is_raw)::value>(x0, x1, sv, c * 32 + 2 * i, nm);
+            ts.template exponents<decltype(is_raw)::value>(x0, x1, b0, b1, sv, c * 32 + 2 * i, nm);
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             add2(l_sum, l_odd, p0, p1);
             pk[i] = pack_bf16x2(p0, p1);

@@ -95,13 +95,14 @@ __device__ __forceinline__ float tile_max(const uint32_t (&sv)[4][32]) {
 // The scores of a tile arrive as raw products; top() gives a reference for the
 // tile's running max (log2 units) and exponents() the pairs 2^x is taken of.
 //
-// A tile that every row of the warp sees whole (most are) stays raw: the cap is
+// A tile stays raw where it can: without a cap its unseen scores become -inf as
+// they are; with one, where every row of the warp sees it whole (most tiles). The cap is
 // y P(y^2) with y = raw r, |y| <= 0.55 and P of degree 3, fitted here to the
 // least largest error of y P(y^2) (2^-21.5 in fp32 arithmetic), its coefficients
 // scaled so that a score costs 5 operations, the last of which also subtracts the
 // reference (2^x and 1/x would be two SFU operations of each score beside the
 // softmax's own 2^x); the bias is one more. The reference is then the largest raw
-// score's logit plus the tile's largest bias: an upper bound at most kSpread above
+// score's logit plus the largest bias of a key the row sees: an upper bound at most kSpread above
 // the row's largest logit. Weights then start at 2^-80 instead of 1, which fp32
 // and bf16 hold as exactly; only weights under 2^-46 of the row's largest are lost.
 // Every other tile has its logits written out, masked, and their maximum taken.
@@ -143,17 +144,21 @@ struct TileScores {
       // rows that see keys past their own position take the distance's absolute value
       const bool ahead = kBias && __any_sync(kAll, min(last, 127) > away);
       float mx = 0.f;
-      raw = inside && flat && !ahead && (!kCap || poly);
+      raw = (!kCap || (inside && poly)) && flat && !ahead;
       if (kBias) near = -slope * static_cast<float>(away);
       if (raw) {
+        if (!kCap && !inside) mask_tile(sv, first, last);
         mx = tile_max(sv);
         if constexpr (kCap) raw = __all_sync(kAll, fmaxf(mx, -tile_max<true>(sv)) * r <= 0.55f);
       }
       if (raw) {
         const float t = kCap ? cap(mx * sl2) : mx * sl2;
-        return kBias ? t + fmaxf(near, fmaf(slope, 127.f, near)) : t;
+        const float b0 = fmaf(slope, static_cast<float>(max(first, 0)), near);
+        const float b1 = fmaf(slope, static_cast<float>(min(last, 127)), near);
+        return kBias ? t + fmaxf(b0, b1) : t;
       }
       const float from = static_cast<float>(away);
+      float b0 = 0.f, b1 = 0.f;
 #pragma unroll
       for (int i = 0; i < 128; i += 2) {
         float x0 = score(sv, i), x1 = score(sv, i + 1);
@@ -163,12 +168,11 @@ struct TileScores {
         }
         if constexpr (kBias) {
           const float unit = kCap ? 1.f : sl2;
-          float b0, b1;
           if (ahead) {
             b0 = -slope * fabsf(from - static_cast<float>(i));
             b1 = -slope * fabsf(from - static_cast<float>(i + 1));
           } else {
-            fma2(b0, b1, slope, slope, static_cast<float>(i), static_cast<float>(i + 1), near, near);
+            bias(b0, b1, i, near);
           }
           fma2(x0, x1, x0, x1, unit, unit, b0, b1);
         }
@@ -180,15 +184,27 @@ struct TileScores {
     }
   }
 
-  // x0, x1: exponents of keys i and i + 1 less the reference (nm = -reference).
-  template <bool RAW>
-  __device__ __forceinline__ void exponents(float &x0, float &x1, const uint32_t (&sv)[4][32], int i, float nm) const {
-    const float s0 = score(sv, i), s1 = score(sv, i + 1);
-    float b0 = nm, b1 = nm;
-    if constexpr (RAW && kBias) {
-      const float n = near + nm;
-      fma2(b0, b1, slope, slope, static_cast<float>(i), static_cast<float>(i + 1), n, n);
+  // Biases (plus `first`) of keys i and i + 1, called for i = 0, 2, 4, ...: two
+  // products every eight keys, packed additions in between (three roundings).
+  __device__ __forceinline__ void bias(float &b0, float &b1, int i, float first) const {
+    if (i % 8 == 0) {
+      b0 = fmaf(slope, static_cast<float>(i), first);
+      b1 = fmaf(slope, static_cast<float>(i + 1), first);
+    } else {
+      add2(b0, b1, 2.f * slope, 2.f * slope);
     }
+  }
+
+  // x0, x1: exponents of keys i and i + 1 (i = 0, 2, 4, ...) less the reference
+  // (nm = -reference); b0, b1 carry the biases from one call to the next.
+  template <bool RAW>
+  __device__ __forceinline__ void exponents(float &x0, float &x1, float &b0, float &b1, const uint32_t (&sv)[4][32],
+                                            int i, float nm) const {
+    const float s0 = score(sv, i), s1 = score(sv, i + 1);
+    if constexpr (RAW && kBias)
+      bias(b0, b1, i, near + nm);
+    else
+      b0 = b1 = nm;
     if constexpr (RAW && kCap) {
       float u0, u1, f0 = p3, f1 = p3;
       mul2(u0, u1, s0, s1, s0, s1);
