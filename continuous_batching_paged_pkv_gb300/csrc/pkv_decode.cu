@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            x[nt][c][0] = (s0[nt][c] + s1[nt][c]) * sl2;
-            x[nt][c][1] = (s0[nt][c + 2] + s1[nt][c + 2]) * sl2;
+            x[nt][c][0] = __fmul_rn(s0[nt][c] + s1[nt][c], sl2);
+            x[nt][c][1] = __fmul_rn(s0[nt][c + 2] + s1[nt][c + 2], sl2);
           }
         tm.logits(x, kbase, ka, v, cap, bias);
       }

@@ -665,8 +665,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            x[nt][c][0] = sacc[nt][c] * sl2c[nt][c];
-            x[nt][c][1] = sacc[nt][c + 2] * sl2c[nt][c];
+            x[nt][c][0] = __fmul_rn(sacc[nt][c], sl2c[nt][c]);
+            x[nt][c][1] = __fmul_rn(sacc[nt][c + 2], sl2c[nt][c]);
           }
         tm.logits(x, kbase, ka, v, cap, bias);
       }

@@ -327,7 +327,8 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + kSFree);
-      const float m_new = fmaxf(m_used, ts.top(sv, p_row - kt0, lo - kt0, hi - 1 - kt0));
+      typename TileScores<MODE>::Tile found;
+      const float m_new = fmaxf(m_used, ts.top(sv, p_row - kt0, lo - kt0, hi - 1 - kt0, found));
       // before a row's first visible key there is nothing to rescale
       const bool fresh = m_used == -INFINITY;
       const bool need = !fresh && m_new > m_used + kRescaleThreshold;
@@ -352,22 +353,14 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
       }
       const float nm = m_used == -INFINITY ? 0.f : -m_used;
       auto weigh = [&](auto is_raw) {
-        float b0, b1;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x0, x1;
-            ts.template exponents<decltype(is_raw)::value>(x0, x1, b0, b1, sv, c * 32 + 2 * i, nm);
-            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            add2(l_sum, l_odd, p0, p1);
-            pk[i] = pack_bf16x2(p0, p1);
-          }
+          ts.template weigh<decltype(is_raw)::value>(pk, sv, c, nm, found.near, l_sum, l_odd);
           tmem_st16(tmem + lane_base + kPCol + c * 16, pk);
         }
       };
-      if ((MODE & (kModCap | kModBias)) == 0 || ts.raw)
+      if ((MODE & (kModCap | kModBias)) == 0 || found.raw)
         weigh(std::true_type{});
       else
         weigh(std::false_type{});

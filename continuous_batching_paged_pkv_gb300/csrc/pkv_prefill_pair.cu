@@ -75,10 +75,23 @@ constexpr int kOCol = 384;
 // warpgroup lowers its own to kOtherRegs (the sum is unchanged), so each SM
 // sub-partition holds one softmax warp and one other warp in 9,728 registers
 // and keeps room for a decode warp of the same step beside them.
-constexpr int kThreads = 256;
-constexpr int kWarpProducer = 4, kWarpQK = 5, kWarpPV = 6;
+//
+// With a cap or a bias the softmax's arithmetic, not its chain of waits, sets the
+// pace of a tile. Those variants run two softmax warpgroups (SG = 2) where no
+// decode CTA shares their SMs: each takes 64 of a tile's 128 keys for the same
+// rows, the two warps of a row meet once a tile for the row's maximum (shared
+// memory and an mbarrier, which also orders the first half's scores, in registers
+// by then, before the second half's weights, which overlay them), and each
+// rescales and stores half of O. 384 threads of 168 registers, five K/V stages.
+// Capped 2048-row chunk at context 8192: SG1 us with one warpgroup, SG2 us with two.
+template <int SG>
+struct Roles {
+  static constexpr int kThreads = 128 * (SG + 1);
+  static constexpr int kWarpProducer = 4 * SG, kWarpQK = 4 * SG + 1, kWarpPV = 4 * SG + 2;
+  static constexpr int kRegs = SG == 1 ? 152 : 168;
+};
 constexpr int kLaunchRegs = 152, kSoftmaxRegs = 216, kOtherRegs = 88;
-static_assert(kSoftmaxRegs + kOtherRegs == 2 * kLaunchRegs, "register shares must add up to the launch's");
+static_assert(Roles<1>::kRegs == kLaunchRegs && kSoftmaxRegs + kOtherRegs == 2 * kLaunchRegs, "register shares must add up to the launch's");
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale when the max grows by > 256x
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kNegInfBits = 0xff800000u;
@@ -95,9 +108,12 @@ struct Layout {
   static constexpr int kVBytes = kKeysPerTile * 128;       // 128 keys x this CTA's 64 columns
   static constexpr int kStageBytes = kKBytes + kVBytes;    // 32 KiB: 4 K boxes of 4 KiB, 8 V boxes of 2 KiB
   static constexpr int kBarOffset = kQBytes + kStages * kStageBytes;
-  static constexpr int kSmem = kBarOffset + 256 + 1024;    // barriers/flags + alignment slack
+  static constexpr int kMaxOffset = kBarOffset + 256;      // two warpgroups: [2 parities][2 halves][128 rows] floats
+  template <int SG>
+  static constexpr int kSmem = kMaxOffset + (SG == 2 ? 2048 : 0) + 1024;  // + alignment slack
 };
-static_assert(Layout<6>::kSmem <= 232448, "dynamic shared memory per CTA");
+constexpr int kPairStages = 6, kPairStagesTwoGroups = 5;
+static_assert(Layout<kPairStages>::kSmem<1> <= 232448 && Layout<kPairStagesTwoGroups>::kSmem<2> <= 232448, "dynamic shared memory per CTA");
 
 // Barrier indices for NST stages.
 template <int NST>
@@ -110,7 +126,8 @@ struct Bars {
   static constexpr int kPVDone = kPReady + kSBufs;     // +buffer (3); both CTAs
   static constexpr int kDrain = kPVDone + kSBufs;      // QK issuer's MMAs complete
   static constexpr int kDrainPV = kDrain + 1;          // PV issuer's MMAs complete
-  static constexpr int kNumBars = kDrainPV + 1;
+  static constexpr int kMaxReady = kDrainPV + 1;       // +lane quarter (4): both halves' row maxima (two softmax warpgroups)
+  static constexpr int kNumBars = kMaxReady + 4;
   static_assert(kNumBars * 8 + 16 <= 256, "barriers, TMEM address, abort flag and key range fit their 256 bytes");
 };
 
@@ -143,18 +160,20 @@ __device__ __forceinline__ bool warp_wait_or_abort(uint64_t *bar, uint32_t parit
   return __all_sync(kFull, wait_or_abort(bar, parity, abort));
 }
 
-template <int NST, int MODE>
-__global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
+template <int NST, int MODE, int SG>
+__global__ void __maxnreg__(Roles<SG>::kRegs) prefill_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                                                    const __grid_constant__ CUtensorMap tmap_k,
                                                                    const __grid_constant__ CUtensorMap tmap_v,
                                                                    const StepArgs a,
                                                                    const int32_t *__restrict__ items,
                                                                    int rows_per_tile) {
   using Lay = Layout<NST>;
+  constexpr int kWarpProducer = Roles<SG>::kWarpProducer, kWarpQK = Roles<SG>::kWarpQK, kWarpPV = Roles<SG>::kWarpPV;
   constexpr int kStages = NST;
   constexpr int kQFull = Bars<NST>::kQFull, kKVFull = Bars<NST>::kKVFull, kKVEmpty = Bars<NST>::kKVEmpty;
   constexpr int kSFull = Bars<NST>::kSFull, kPReady = Bars<NST>::kPReady, kPVDone = Bars<NST>::kPVDone;
   constexpr int kDrain = Bars<NST>::kDrain, kDrainPV = Bars<NST>::kDrainPV, kNumBars = Bars<NST>::kNumBars;
+  constexpr int kMaxReady = Bars<NST>::kMaxReady;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align1024(smem_raw);
   uint8_t *sQ = smem;
@@ -211,13 +230,13 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
   // Tile taken at step j. A distance bias makes the nearest keys' logits the
   // largest, so those variants go from the last tile to the first: going up, the
   // running max would grow by slope * 128 with every tile and O be rescaled at
-  // each (a capped-free 2048-row chunk at context 8192: 323 us going up).
+  // each (2048 biased rows at context 8192 took 323 us going up).
   constexpr bool kDown = (MODE & kModBias) != 0;
   auto tile_at = [&](int j) { return kDown ? ntiles - 1 - j : j; };
   const int32_t *bt_row = a.block_tables + static_cast<int64_t>(slot) * a.max_blocks_per_slot;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(bar + i, (i >= kPReady && i < kPReady + kSBufs) ? 8 : 1);
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bar + i, i >= kMaxReady ? 2 : i >= kPReady && i < kPReady + kSBufs ? 8 * SG : 1);
     fence_barrier_init();
     *abort_flag = 0;
   }
@@ -241,8 +260,8 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= 4) {
-   setmaxnreg_dec<kOtherRegs>();
+  if (warp >= 4 * SG) {
+   if constexpr (SG == 1) setmaxnreg_dec<kOtherRegs>();
    if (warp == kWarpProducer) {
     // ------------------------------------------------------------ producer
     // Pool rows of the 16-key sub-tiles, four tiles per warp-wide load: lane l
@@ -358,9 +377,15 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
    }
   } else {
     // ------------------------------------------------------------ softmax
-    setmaxnreg_inc<kSoftmaxRegs>();
-    const int qw = warp;
+    if constexpr (SG == 1) setmaxnreg_inc<kSoftmaxRegs>();
+    // A tile goes whole, or, with a cap or a bias, as two halves of 64 keys: one per
+    // warpgroup, or one after the other in one warpgroup with the same arithmetic
+    // (a row's result must not depend on whether decode rows share the step).
+    constexpr int Q = (MODE & (kModCap | kModBias)) ? 2 : 4, H = 4 / Q / SG;  // quarters per part, parts per thread
+    static_assert(H >= 1, "masks alone run one warpgroup");
+    const int qw = warp & 3, half = SG == 1 ? 0 : warp >> 2;
     const int mrow = qw * 32 + lane;
+    float *row_max = reinterpret_cast<float *>(smem + Lay::kMaxOffset);
     const uint32_t lane_base = static_cast<uint32_t>(qw * 32) << 16;
     const int pos = mrow / G;
     const int p_row = L - n + pos0 + pos;  // last visible key of this row (inclusive)
@@ -368,34 +393,52 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
     int lo = 0, hi = INT32_MAX;  // visible keys of this row (modified scores); rows that are not stored mask nothing
     const bool stored = mrow < G * P && pos < rows;
     if (MODE != kModNone && stored) row_sees(a, static_cast<int64_t>(row0) + pos0 + pos, p_row, L, lo, hi);
-    TileScores<MODE> ts(a, g * G + mrow % G);
+    TileScores<MODE, Q> ts(a, g * G + mrow % G);
     const uint32_t p_ready0 = cluster_addr(bar + kPReady, 0);
     float m_used = -INFINITY;  // log2 units
     bool ok = true;
-    float l_sum = 0.f, l_odd = 0.f;  // row sum, as even and odd columns (packed adds)
+    float l_sum[H] = {}, l_odd[H] = {};  // row sum per part, as even and odd columns (packed adds)
     for (int j = 0; j < ntiles; ++j) {
       const int s = j % kSBufs;
       if (!(ok = warp_wait_or_abort(bar + kSFull + s, (j / kSBufs) & 1, abort_flag))) break;
       tc_fence_after();
       const int tile_j = tile_at(j), kt0 = base + tile_j * kKeysPerTile;
-      uint32_t sv[4][32];
+      uint32_t sv[H][Q][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_base + s * 128 + c * 32, sv[c]);
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int c = 0; c < Q; ++c) tmem_ld32(tmem + lane_base + s * 128 + ((half + h) * Q + c) * 32, sv[h][c]);
       tmem_wait_ld();
       // Edges: only tiles that reach past some row's keys need a mask (causal and ragged; both ends with modified scores).
+      typename TileScores<MODE, Q>::Tile found[H];
       float mx;
       if constexpr (MODE != kModNone) {
-        mx = ts.top(sv, p_row - kt0, lo - kt0, hi - 1 - kt0);
+        mx = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const int k0 = kt0 + (half + h) * Q * 32;
+          mx = fmaxf(mx, ts.top(sv[h], p_row - k0, lo - k0, hi - 1 - k0, found[h]));
+        }
+        if constexpr (SG == 2) {
+          float *mine = row_max + (j & 1) * 256 + mrow;
+          mine[half * 128] = mx;
+          tc_fence_before();  // this half's scores are in registers
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar + kMaxReady + qw);
+          if (!(ok = warp_wait_or_abort(bar + kMaxReady + qw, j & 1, abort_flag))) break;
+          tc_fence_after();
+          mx = fmaxf(mx, mine[(half ^ 1) * 128]);
+        }
       } else {
         const int lim = min(p_row, kv_end - 1) - kt0;
         if (!__all_sync(kFull, lim >= kKeysPerTile - 1)) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < Q; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (c * 32 + i > lim) sv[c][i] = kNegInfBits;
+              if (c * 32 + i > lim) sv[0][c][i] = kNegInfBits;
         }
-        mx = tile_max(sv) * sl2;
+        mx = tile_max(sv[0]) * sl2;
       }
       const float m_new = fmaxf(m_used, mx);
       // before a row's first visible key there is nothing to rescale
@@ -408,39 +451,37 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
         tc_fence_after();
         const float corr = need ? ex2_approx(m_used - m_new) : 1.f;
         if (need) m_used = m_new;
-        l_sum *= corr;
-        l_odd *= corr;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int h = 0; h < H; ++h) {
+          l_sum[h] *= corr;
+          l_odd[h] *= corr;
+        }
+#pragma unroll
+        for (int c = 0; c < 4 / SG; ++c) {
           uint32_t ov[32];
-          tmem_ld32(tmem + lane_base + kOCol + c * 32, ov);
+          tmem_ld32(tmem + lane_base + kOCol + (half * 2 + c) * 32, ov);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * corr);
-          tmem_st32(tmem + lane_base + kOCol + c * 32, ov);
+          tmem_st32(tmem + lane_base + kOCol + (half * 2 + c) * 32, ov);
         }
       }
       const float nm = MODE != kModNone && m_used == -INFINITY ? 0.f : -m_used;
-      auto weigh = [&](auto is_raw) {
-        float b0, b1;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
+      for (int h = 0; h < H; ++h) {
+        auto weigh = [&](auto is_raw) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x0, x1;
-            ts.template exponents<decltype(is_raw)::value>(x0, x1, b0, b1, sv, c * 32 + 2 * i, nm);
-            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            add2(l_sum, l_odd, p0, p1);
-            pk[i] = pack_bf16x2(p0, p1);
+          for (int c = 0; c < Q; ++c) {
+            uint32_t pk[16];
+            ts.template weigh<decltype(is_raw)::value>(pk, sv[h], c, nm, found[h].near, l_sum[h], l_odd[h]);
+            tmem_st16(tmem + lane_base + s * 128 + ((half + h) * Q + c) * 16, pk);
           }
-          tmem_st16(tmem + lane_base + s * 128 + c * 16, pk);
-        }
-      };
-      if ((MODE & (kModCap | kModBias)) == 0 || ts.raw)
-        weigh(std::true_type{});
-      else
-        weigh(std::false_type{});
+        };
+        if ((MODE & (kModCap | kModBias)) == 0 || found[h].raw)
+          weigh(std::true_type{});
+        else
+          weigh(std::false_type{});
+      }
       // Zero this CTA's V rows past the last visible key inside the final 16-key
       // step, and before the first visible one inside the first: a block may
       // hold stale or NaN rows there, and 0 * NaN would reach O. The tile's data
@@ -451,14 +492,14 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
         const int tail = (kSubKeys - valid % kSubKeys) % kSubKeys;
         if (tail) {
           uint8_t *sV = sKV + (j % kStages) * Lay::kStageBytes + Lay::kKBytes;
-          for (int i = threadIdx.x; i < tail * 8; i += 128)
+          for (int i = threadIdx.x; i < tail * 8; i += 128 * SG)
             *reinterpret_cast<uint4 *>(sV + (valid + i / 8) * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
       }
       if (MODE != kModNone && tile_j == 0 && kv_begin > base) {
         uint8_t *sV = sKV + (j % kStages) * Lay::kStageBytes + Lay::kKBytes;
-        for (int i = threadIdx.x; i < (kv_begin - base) * 8; i += 128)
+        for (int i = threadIdx.x; i < (kv_begin - base) * 8; i += 128 * SG)
           *reinterpret_cast<uint4 *>(sV + i * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         wrote_v = true;
@@ -477,7 +518,17 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
     if (ok && (ntiles == 0 ||
                warp_wait_or_abort(bar + kPVDone + (ntiles - 1) % kSBufs, ((ntiles - 1) / kSBufs) & 1, abort_flag))) {
       tc_fence_after();
-      const float inv = 1.f / (l_sum + l_odd);
+      float l_row = l_sum[0] + l_odd[0];
+      if constexpr (H == 2) l_row += l_sum[1] + l_odd[1];
+      if constexpr (SG == 2) {  // the other half's share of the row sum
+        float *mine = row_max + (ntiles & 1) * 256 + mrow;
+        mine[half * 128] = l_row;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + kMaxReady + qw);
+        ok = warp_wait_or_abort(bar + kMaxReady + qw, ntiles & 1, abort_flag);  // (false: the status word says so)
+        l_row = mine[0] + mine[128];
+      }
+      const float inv = 1.f / l_row;
       // a row that sees nothing gives zeros, whatever O holds (an empty pair's O was never written)
       const bool none = MODE != kModNone && lo >= hi;
       constexpr int kRowBytes = D * 2, kChunks = kRowBytes / 16;
@@ -487,7 +538,8 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
                                                 (static_cast<size_t>(row0 + pos0 + pos) * a.num_q_heads + g * G +
                                                  mrow % G) * D);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int k = 0; k < 4 / SG; ++k) {
+          const int c = half * 2 + k;
           uint32_t ov[32];
           tmem_ld32(tmem + lane_base + kOCol + c * 32, ov);
           tmem_wait_ld();
@@ -501,7 +553,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
               orow[c * 4 + v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
           }
         }
-      } else {
+      } else if constexpr (SG == 1) {
         // Output in host memory: the rows leave through shared memory, the Q
         // tile (no longer read once the last P.V is done, its S consumed
         // above). Each warp stages its 32 rows (16-byte chunk k of row r at
@@ -549,15 +601,15 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_pair_kernel(const __grid_consta
   }
 }
 
-template <int NST, int MODE>
+template <int NST, int MODE, int SG>
 cudaError_t launch_pair_t(const StepArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           int32_t rows_per_tile, int32_t num_items, const int32_t *items, cudaStream_t stream) {
-  constexpr int smem = Layout<NST>::kSmem;
+  constexpr int smem = Layout<NST>::template kSmem<SG>;
   static std::atomic<uint64_t> configured{0};  // one bit per device
-  if (const cudaError_t e = allow_smem_once(prefill_pair_kernel<NST, MODE>, smem, configured); e != cudaSuccess) return e;
+  if (const cudaError_t e = allow_smem_once(prefill_pair_kernel<NST, MODE, SG>, smem, configured); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * num_items), static_cast<unsigned>(a.num_kv_heads));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Roles<SG>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -569,21 +621,25 @@ cudaError_t launch_pair_t(const StepArgs &a, const CUtensorMap &tq, const CUtens
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<NST, MODE>, tq, tk, tv, a, items, rows_per_tile);
+  return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<NST, MODE, SG>, tq, tk, tv, a, items, rows_per_tile);
 }
 
-template <int NST>
+// One softmax warpgroup beside decode CTAs and wherever scores are only masked; two for caps and biases.
+template <bool BESIDE>
 cudaError_t launch_pair_m(const StepArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           int32_t rows_per_tile, int32_t num_items, const int32_t *items, cudaStream_t stream) {
+  constexpr int N1 = BESIDE ? kPairStagesBesideDecode : kPairStages;
+  constexpr int N2 = BESIDE ? kPairStagesBesideDecode : kPairStagesTwoGroups, SG = BESIDE ? 1 : 2;
   switch (mode_of(a)) {
-    case kModNone: return launch_pair_t<NST, kModNone>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
-    case kModMask: return launch_pair_t<NST, kModMask>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+    case kModNone: return launch_pair_t<N1, kModNone, 1>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+    case kModMask: return launch_pair_t<N1, kModMask, 1>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
     case kModMask | kModCap:
-      return launch_pair_t<NST, kModMask | kModCap>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+      return launch_pair_t<N2, kModMask | kModCap, SG>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
     case kModMask | kModBias:
-      return launch_pair_t<NST, kModMask | kModBias>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+      return launch_pair_t<N2, kModMask | kModBias, SG>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
     default:
-      return launch_pair_t<NST, kModMask | kModCap | kModBias>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+      return launch_pair_t<N2, kModMask | kModCap | kModBias, SG>(a, tq, tk, tv, rows_per_tile, num_items, items,
+                                                                  stream);
   }
 }
 
@@ -593,8 +649,8 @@ cudaError_t launch_prefill_pair(const StepArgs &a, const CUtensorMap &tq, const 
                                 const CUtensorMap &tv, int32_t rows_per_tile, int32_t num_items,
                                 const int32_t *items, bool beside_decode, cudaStream_t stream) {
   if (num_items <= 0) return cudaSuccess;
-  return beside_decode ? launch_pair_m<kPairStagesBesideDecode>(a, tq, tk, tv, rows_per_tile, num_items, items, stream)
-                       : launch_pair_m<6>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+  return beside_decode ? launch_pair_m<true>(a, tq, tk, tv, rows_per_tile, num_items, items, stream)
+                       : launch_pair_m<false>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
 }
 
 }  // namespace pkv

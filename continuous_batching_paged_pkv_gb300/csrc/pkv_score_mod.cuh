@@ -33,7 +33,7 @@ struct Cap {
   float k, c, c2;
   __device__ __forceinline__ explicit Cap(float softcap)
       : on(softcap > 0.f), k(2.f / softcap), c(softcap * 1.4426950408889634f), c2(-2.f * c) {}
-  __device__ __forceinline__ float operator()(float x) const { return fmaf(c2, rcp_approx(1.f + ex2_approx(x * k)), c); }
+  __device__ __forceinline__ float operator()(float x) const { return fmaf(c2, rcp_approx(1.f + ex2_approx(__fmul_rn(x, k))), c); }
 };
 
 // Variants of the chunk kernels: plain, or modified scores with or without the
@@ -68,30 +68,35 @@ __device__ __forceinline__ void rows_see(const StepArgs &a, int64_t row0, int po
   __syncthreads();
 }
 
-// Scores outside [first, last] of the tile's 128 keys become -inf.
-__device__ __forceinline__ void mask_tile(uint32_t (&sv)[4][32], int first, int last) {
+// Scores outside [first, last] of the thread's Q x 32 keys become -inf.
+template <int Q>
+__device__ __forceinline__ void mask_tile(uint32_t (&sv)[Q][32], int first, int last) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
+  for (int c = 0; c < Q; ++c)
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       if (c * 32 + i < first || c * 32 + i > last) sv[c][i] = 0xff800000u;
 }
 
-__device__ __forceinline__ float score(const uint32_t (&sv)[4][32], int i) { return __uint_as_float(sv[i >> 5][i & 31]); }
+template <int Q>
+__device__ __forceinline__ float score(const uint32_t (&sv)[Q][32], int i) {
+  return __uint_as_float(sv[i >> 5][i & 31]);
+}
 
-// Largest of a row's 128 scores, or the smallest: three-input maxima, four independent chains.
-template <bool MIN = false>
-__device__ __forceinline__ float tile_max(const uint32_t (&sv)[4][32]) {
+// Largest of a thread's scores, or the smallest: three-input maxima, four independent chains.
+template <bool MIN = false, int Q>
+__device__ __forceinline__ float tile_max(const uint32_t (&sv)[Q][32]) {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < 128; i += 2)
+  for (int i = 0; i < Q * 32; i += 2)
     m[(i >> 1) & 3] = MIN ? max3(m[(i >> 1) & 3], -score(sv, i), -score(sv, i + 1))
                           : max3(m[(i >> 1) & 3], score(sv, i), score(sv, i + 1));
   const float r = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
   return MIN ? -r : r;
 }
 
-// Modified scores in a chunk kernel's softmax thread: one row, tile by tile.
+// Modified scores in a chunk kernel's softmax thread: Q x 32 keys of one row, tile
+// by tile (the whole tile of 128, or one half where two warpgroups share it).
 // The scores of a tile arrive as raw products; top() gives a reference for the
 // tile's running max (log2 units) and exponents() the pairs 2^x is taken of.
 //
@@ -106,22 +111,27 @@ __device__ __forceinline__ float tile_max(const uint32_t (&sv)[4][32]) {
 // the row's largest logit. Weights then start at 2^-80 instead of 1, which fp32
 // and bf16 hold as exactly; only weights under 2^-46 of the row's largest are lost.
 // Every other tile has its logits written out, masked, and their maximum taken.
-template <int MODE>
+// Products that a sum follows are rounded explicitly: the compiler must not fuse
+// them in one variant and not in another, or a row's last bits would depend on
+// whether decode rows share the step.
+template <int MODE, int Q = 4>
 struct TileScores {
+  static constexpr int kKeys = Q * 32;
   static constexpr bool kCap = (MODE & kModCap) != 0, kBias = (MODE & kModBias) != 0;
   static constexpr float kSpread = 80.f;  // log2 units
   Cap cap;
   float sl2, slope;  // scale and bias per key in log2 units
   float r, p0, p1, p2, p3;
   bool poly, flat;   // warp-uniform: the cap's r leaves the coefficients in range; a tile's biases stay within kSpread
-  // of the current tile
-  bool raw;    // warp-uniform
-  float near;  // bias of its first key
+  struct Tile {  // what top() found of a tile
+    bool raw;    // warp-uniform
+    float near;  // bias of its first key
+  };
 
   __device__ __forceinline__ TileScores(const StepArgs &a, int head)
-      : cap(kCap ? a.softcap : 0.f), sl2(a.scale_log2), slope(0.f), r(0.f), raw(true), near(0.f) {
+      : cap(kCap ? a.softcap : 0.f), sl2(a.scale_log2), slope(0.f), r(0.f) {
     if constexpr (kBias) slope = __ldg(a.alibi_slopes + head) * 1.4426950408889634f;
-    flat = !kBias || __all_sync(0xffffffffu, fabsf(slope) * 127.f <= kSpread);
+    flat = !kBias || __all_sync(0xffffffffu, fabsf(slope) * (kKeys - 1) <= kSpread);
     if constexpr (kCap) {
       r = sl2 / cap.c;
       poly = r > 0x1p-17f && r < 0x1p17f;
@@ -133,34 +143,38 @@ struct TileScores {
     }
   }
 
-  // `away`: position of the row minus the tile's first key; keys [first, last] of the tile are the row's.
-  __device__ __forceinline__ float top(uint32_t (&sv)[4][32], int away, int first, int last) {
+  // `away`: position of the row minus the thread's first key; of its keys [first, last] are the row's.
+  __device__ __forceinline__ float top(uint32_t (&sv)[Q][32], int away, int first, int last, Tile &tile) const {
     constexpr uint32_t kAll = 0xffffffffu;
-    const bool inside = __all_sync(kAll, first <= 0 && last >= 127);
+    tile.raw = true;
+    tile.near = 0.f;
+    const bool inside = __all_sync(kAll, first <= 0 && last >= kKeys - 1);
     if constexpr (!kCap && !kBias) {
       if (!inside) mask_tile(sv, first, last);
       return tile_max(sv) * sl2;
     } else {
       // rows that see keys past their own position take the distance's absolute value
-      const bool ahead = kBias && __any_sync(kAll, min(last, 127) > away);
+      const bool ahead = kBias && __any_sync(kAll, min(last, kKeys - 1) > away);
       float mx = 0.f;
-      raw = (!kCap || (inside && poly)) && flat && !ahead;
-      if (kBias) near = -slope * static_cast<float>(away);
+      bool raw = (!kCap || (inside && poly)) && flat && !ahead;
+      const float near = kBias ? __fmul_rn(-slope, static_cast<float>(away)) : 0.f;
+      tile.near = near;
       if (raw) {
         if (!kCap && !inside) mask_tile(sv, first, last);
         mx = tile_max(sv);
         if constexpr (kCap) raw = __all_sync(kAll, fmaxf(mx, -tile_max<true>(sv)) * r <= 0.55f);
       }
+      tile.raw = raw;
       if (raw) {
-        const float t = kCap ? cap(mx * sl2) : mx * sl2;
+        const float t = kCap ? cap(__fmul_rn(mx, sl2)) : __fmul_rn(mx, sl2);
         const float b0 = fmaf(slope, static_cast<float>(max(first, 0)), near);
-        const float b1 = fmaf(slope, static_cast<float>(min(last, 127)), near);
+        const float b1 = fmaf(slope, static_cast<float>(min(last, kKeys - 1)), near);
         return kBias ? t + fmaxf(b0, b1) : t;
       }
       const float from = static_cast<float>(away);
       float b0 = 0.f, b1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < 128; i += 2) {
+      for (int i = 0; i < kKeys; i += 2) {
         float x0 = score(sv, i), x1 = score(sv, i + 1);
         if constexpr (kCap) {
           x0 = cap(x0 * sl2);
@@ -198,8 +212,8 @@ struct TileScores {
   // x0, x1: exponents of keys i and i + 1 (i = 0, 2, 4, ...) less the reference
   // (nm = -reference); b0, b1 carry the biases from one call to the next.
   template <bool RAW>
-  __device__ __forceinline__ void exponents(float &x0, float &x1, float &b0, float &b1, const uint32_t (&sv)[4][32],
-                                            int i, float nm) const {
+  __device__ __forceinline__ void exponents(float &x0, float &x1, float &b0, float &b1, const uint32_t (&sv)[Q][32],
+                                            int i, float nm, float near) const {
     const float s0 = score(sv, i), s1 = score(sv, i + 1);
     if constexpr (RAW && kBias)
       bias(b0, b1, i, near + nm);
@@ -215,6 +229,21 @@ struct TileScores {
     } else {
       const float unit = RAW ? sl2 : 1.f;
       fma2(x0, x1, s0, s1, unit, unit, b0, b1);
+    }
+  }
+
+  // Weights of keys c * 32 .. c * 32 + 31 as bf16 pairs, added to the row sum's even and odd parts.
+  template <bool RAW>
+  __device__ __forceinline__ void weigh(uint32_t (&pk)[16], const uint32_t (&sv)[Q][32], int c, float nm, float near,
+                                        float &even, float &odd) const {
+    float b0, b1;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float x0, x1;
+      exponents<RAW>(x0, x1, b0, b1, sv, c * 32 + 2 * i, nm, near);
+      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+      add2(even, odd, p0, p1);
+      pk[i] = pack_bf16x2(p0, p1);
     }
   }
 };
