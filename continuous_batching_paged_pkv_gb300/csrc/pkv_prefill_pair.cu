@@ -76,22 +76,23 @@ constexpr int kOCol = 384;
 // sub-partition holds one softmax warp and one other warp in 9,728 registers
 // and keeps room for a decode warp of the same step beside them.
 //
-// With a cap or a bias the softmax's arithmetic, not its chain of waits, sets the
-// pace of a tile. Those variants run two softmax warpgroups (SG = 2) where no
-// decode CTA shares their SMs: each takes 64 of a tile's 128 keys for the same
-// rows, the two warps of a row meet once a tile for the row's maximum (shared
-// memory and an mbarrier, which also orders the first half's scores, in registers
-// by then, before the second half's weights, which overlay them), and each
-// rescales and stores half of O. 384 threads of 168 registers, five K/V stages.
-// Capped 2048-row chunk at context 8192: SG1 us with one warpgroup, SG2 us with two.
+// With a cap or a bias, where no decode CTA shares their SMs, two softmax
+// warpgroups (SG = 2) take the tiles in turn: while one weighs its tile, the other
+// loads the next one's scores and finds their maximum. A row's running max passes
+// from step to step through shared memory and an mbarrier; each group keeps the
+// row sum of its own tiles, brought to the current max when it takes over. The one
+// warpgroup of the other launches keeps the same two sums, so a row's bits do not
+// depend on which of the two ran. 384 threads launched with 168 registers, shares
+// of 208, 208 and 88, five K/V stages. 2048 rows at context 8192: capped 292 us
+// with one group, 273 us with two; biased 263 and 238 us; only masked 187 and 186 us
+// (the tensor core's chain S, P, O through three buffers sets the pace there).
 template <int SG>
 struct Roles {
   static constexpr int kThreads = 128 * (SG + 1);
   static constexpr int kWarpProducer = 4 * SG, kWarpQK = 4 * SG + 1, kWarpPV = 4 * SG + 2;
-  static constexpr int kRegs = SG == 1 ? 152 : 168;
+  static constexpr int kLaunchRegs = SG == 1 ? 152 : 168, kSoftmaxRegs = SG == 1 ? 216 : 208, kOtherRegs = 88;
+  static_assert(SG * kSoftmaxRegs + kOtherRegs == (SG + 1) * kLaunchRegs, "register shares must add up to the launch's");
 };
-constexpr int kLaunchRegs = 152, kSoftmaxRegs = 216, kOtherRegs = 88;
-static_assert(Roles<1>::kRegs == kLaunchRegs && kSoftmaxRegs + kOtherRegs == 2 * kLaunchRegs, "register shares must add up to the launch's");
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale when the max grows by > 256x
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kNegInfBits = 0xff800000u;
@@ -108,12 +109,13 @@ struct Layout {
   static constexpr int kVBytes = kKeysPerTile * 128;       // 128 keys x this CTA's 64 columns
   static constexpr int kStageBytes = kKBytes + kVBytes;    // 32 KiB: 4 K boxes of 4 KiB, 8 V boxes of 2 KiB
   static constexpr int kBarOffset = kQBytes + kStages * kStageBytes;
-  static constexpr int kMaxOffset = kBarOffset + 256;      // two warpgroups: [2 parities][2 halves][128 rows] floats
+  static constexpr int kMaxOffset = kBarOffset + 320;      // two warpgroups: maxima, then sums, [2][128 rows] floats each
   template <int SG>
   static constexpr int kSmem = kMaxOffset + (SG == 2 ? 2048 : 0) + 1024;  // + alignment slack
 };
 constexpr int kPairStages = 6, kPairStagesTwoGroups = 5;
-static_assert(Layout<kPairStages>::kSmem<1> <= 232448 && Layout<kPairStagesTwoGroups>::kSmem<2> <= 232448, "dynamic shared memory per CTA");
+static_assert(Layout<kPairStages>::kSmem<1> <= 232448 && Layout<kPairStagesTwoGroups>::kSmem<2> <= 232448,
+              "dynamic shared memory per CTA");
 
 // Barrier indices for NST stages.
 template <int NST>
@@ -126,9 +128,10 @@ struct Bars {
   static constexpr int kPVDone = kPReady + kSBufs;     // +buffer (3); both CTAs
   static constexpr int kDrain = kPVDone + kSBufs;      // QK issuer's MMAs complete
   static constexpr int kDrainPV = kDrain + 1;          // PV issuer's MMAs complete
-  static constexpr int kMaxReady = kDrainPV + 1;       // +lane quarter (4): both halves' row maxima (two softmax warpgroups)
-  static constexpr int kNumBars = kMaxReady + 4;
-  static_assert(kNumBars * 8 + 16 <= 256, "barriers, TMEM address, abort flag and key range fit their 256 bytes");
+  static constexpr int kMaxReady = kDrainPV + 1;       // +lane quarter (4): a step's running maxima (two softmax warpgroups)
+  static constexpr int kSumReady = kMaxReady + 4;      // +lane quarter (4): both groups' row sums
+  static constexpr int kNumBars = kSumReady + 4;
+  static_assert(kNumBars * 8 + 16 <= 320, "barriers, TMEM address, abort flag and key range fit their 320 bytes");
 };
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
@@ -161,7 +164,7 @@ __device__ __forceinline__ bool warp_wait_or_abort(uint64_t *bar, uint32_t parit
 }
 
 template <int NST, int MODE, int SG>
-__global__ void __maxnreg__(Roles<SG>::kRegs) prefill_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
+__global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                                                    const __grid_constant__ CUtensorMap tmap_k,
                                                                    const __grid_constant__ CUtensorMap tmap_v,
                                                                    const StepArgs a,
@@ -173,7 +176,7 @@ __global__ void __maxnreg__(Roles<SG>::kRegs) prefill_pair_kernel(const __grid_c
   constexpr int kQFull = Bars<NST>::kQFull, kKVFull = Bars<NST>::kKVFull, kKVEmpty = Bars<NST>::kKVEmpty;
   constexpr int kSFull = Bars<NST>::kSFull, kPReady = Bars<NST>::kPReady, kPVDone = Bars<NST>::kPVDone;
   constexpr int kDrain = Bars<NST>::kDrain, kDrainPV = Bars<NST>::kDrainPV, kNumBars = Bars<NST>::kNumBars;
-  constexpr int kMaxReady = Bars<NST>::kMaxReady;
+  constexpr int kMaxReady = Bars<NST>::kMaxReady, kSumReady = Bars<NST>::kSumReady;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align1024(smem_raw);
   uint8_t *sQ = smem;
@@ -236,7 +239,7 @@ __global__ void __maxnreg__(Roles<SG>::kRegs) prefill_pair_kernel(const __grid_c
   const int32_t *bt_row = a.block_tables + static_cast<int64_t>(slot) * a.max_blocks_per_slot;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(bar + i, i >= kMaxReady ? 2 : i >= kPReady && i < kPReady + kSBufs ? 8 * SG : 1);
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bar + i, i >= kSumReady ? 2 : i >= kPReady && i < kPReady + kSBufs ? 8 : 1);
     fence_barrier_init();
     *abort_flag = 0;
   }
@@ -261,7 +264,7 @@ __global__ void __maxnreg__(Roles<SG>::kRegs) prefill_pair_kernel(const __grid_c
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= 4 * SG) {
-   if constexpr (SG == 1) setmaxnreg_dec<kOtherRegs>();
+   setmaxnreg_dec<Roles<SG>::kOtherRegs>();
    if (warp == kWarpProducer) {
     // ------------------------------------------------------------ producer
     // Pool rows of the 16-key sub-tiles, four tiles per warp-wide load: lane l
@@ -377,15 +380,10 @@ __global__ void __maxnreg__(Roles<SG>::kRegs) prefill_pair_kernel(const __grid_c
    }
   } else {
     // ------------------------------------------------------------ softmax
-    if constexpr (SG == 1) setmaxnreg_inc<kSoftmaxRegs>();
-    // A tile goes whole, or, with a cap or a bias, as two halves of 64 keys: one per
-    // warpgroup, or one after the other in one warpgroup with the same arithmetic
-    // (a row's result must not depend on whether decode rows share the step).
-    constexpr int Q = (MODE & (kModCap | kModBias)) ? 2 : 4, H = 4 / Q / SG;  // quarters per part, parts per thread
-    static_assert(H >= 1, "masks alone run one warpgroup");
-    const int qw = warp & 3, half = SG == 1 ? 0 : warp >> 2;
+    setmaxnreg_inc<Roles<SG>::kSoftmaxRegs>();
+    const int qw = warp & 3, group = SG == 1 ? 0 : warp >> 2, tid = threadIdx.x & 127;
     const int mrow = qw * 32 + lane;
-    float *row_max = reinterpret_cast<float *>(smem + Lay::kMaxOffset);
+    float *step_max = reinterpret_cast<float *>(smem + Lay::kMaxOffset) + mrow, *group_sum = step_max + 256;
     const uint32_t lane_base = static_cast<uint32_t>(qw * 32) << 16;
     const int pos = mrow / G;
     const int p_row = L - n + pos0 + pos;  // last visible key of this row (inclusive)
@@ -393,57 +391,60 @@ __global__ void __maxnreg__(Roles<SG>::kRegs) prefill_pair_kernel(const __grid_c
     int lo = 0, hi = INT32_MAX;  // visible keys of this row (modified scores); rows that are not stored mask nothing
     const bool stored = mrow < G * P && pos < rows;
     if (MODE != kModNone && stored) row_sees(a, static_cast<int64_t>(row0) + pos0 + pos, p_row, L, lo, hi);
-    TileScores<MODE, Q> ts(a, g * G + mrow % G);
+    TileScores<MODE> ts(a, g * G + mrow % G);
     const uint32_t p_ready0 = cluster_addr(bar + kPReady, 0);
     float m_used = -INFINITY;  // log2 units
     bool ok = true;
-    float l_sum[H] = {}, l_odd[H] = {};  // row sum per part, as even and odd columns (packed adds)
-    for (int j = 0; j < ntiles; ++j) {
+    float l_sum = 0.f, l_odd = 0.f;  // row sum, as even and odd columns (packed adds)
+    // With modified scores a row sum for the tiles of even steps and one for those of odd steps: one per
+    // warpgroup, or both here, this step's parity in l and the other in k.
+    float k_sum = 0.f, k_odd = 0.f;
+    for (int j = group; j < ntiles; j += SG) {
       const int s = j % kSBufs;
       if (!(ok = warp_wait_or_abort(bar + kSFull + s, (j / kSBufs) & 1, abort_flag))) break;
       tc_fence_after();
       const int tile_j = tile_at(j), kt0 = base + tile_j * kKeysPerTile;
-      uint32_t sv[H][Q][32];
+      uint32_t sv[4][32];
 #pragma unroll
-      for (int h = 0; h < H; ++h)
-#pragma unroll
-        for (int c = 0; c < Q; ++c) tmem_ld32(tmem + lane_base + s * 128 + ((half + h) * Q + c) * 32, sv[h][c]);
+      for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_base + s * 128 + c * 32, sv[c]);
       tmem_wait_ld();
       // Edges: only tiles that reach past some row's keys need a mask (causal and ragged; both ends with modified scores).
-      typename TileScores<MODE, Q>::Tile found[H];
+      typename TileScores<MODE>::Tile found;
       float mx;
       if constexpr (MODE != kModNone) {
-        mx = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          const int k0 = kt0 + (half + h) * Q * 32;
-          mx = fmaxf(mx, ts.top(sv[h], p_row - k0, lo - k0, hi - 1 - k0, found[h]));
-        }
-        if constexpr (SG == 2) {
-          float *mine = row_max + (j & 1) * 256 + mrow;
-          mine[half * 128] = mx;
-          tc_fence_before();  // this half's scores are in registers
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar + kMaxReady + qw);
-          if (!(ok = warp_wait_or_abort(bar + kMaxReady + qw, j & 1, abort_flag))) break;
-          tc_fence_after();
-          mx = fmaxf(mx, mine[(half ^ 1) * 128]);
-        }
+        mx = ts.top(sv, p_row - kt0, lo - kt0, hi - 1 - kt0, found);
       } else {
         const int lim = min(p_row, kv_end - 1) - kt0;
         if (!__all_sync(kFull, lim >= kKeysPerTile - 1)) {
 #pragma unroll
-          for (int c = 0; c < Q; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (c * 32 + i > lim) sv[0][c][i] = kNegInfBits;
+              if (c * 32 + i > lim) sv[c][i] = kNegInfBits;
         }
-        mx = tile_max(sv[0]) * sl2;
+        mx = tile_max(sv) * sl2;
+      }
+      if constexpr (SG == 2) {  // the other group's step may have moved the reference
+        if (j > 0) {
+          if (!(ok = warp_wait_or_abort(bar + kMaxReady + qw, (j - 1) & 1, abort_flag))) break;
+          const float m = step_max[((j - 1) & 1) * 128];
+          if (m != m_used && m_used != -INFINITY) {
+            const float corr = ex2_approx(m_used - m);
+            l_sum *= corr;
+            l_odd *= corr;
+          }
+          m_used = m;
+        }
       }
       const float m_new = fmaxf(m_used, mx);
       // before a row's first visible key there is nothing to rescale
       const bool fresh = MODE != kModNone ? m_used == -INFINITY : j == 0;
       const bool need = !fresh && m_new > m_used + kRescaleThreshold;
+      if constexpr (SG == 2) {
+        step_max[(j & 1) * 128] = fresh || need ? m_new : m_used;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + kMaxReady + qw);
+      }
       if (fresh) m_used = m_new;
       if (__any_sync(kFull, need)) {
         // O must hold tile j-1's products before it is rescaled.
@@ -451,37 +452,35 @@ __global__ void __maxnreg__(Roles<SG>::kRegs) prefill_pair_kernel(const __grid_c
         tc_fence_after();
         const float corr = need ? ex2_approx(m_used - m_new) : 1.f;
         if (need) m_used = m_new;
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          l_sum[h] *= corr;
-          l_odd[h] *= corr;
+        l_sum *= corr;
+        l_odd *= corr;
+        if constexpr (MODE != kModNone && SG == 1) {
+          k_sum *= corr;
+          k_odd *= corr;
         }
 #pragma unroll
-        for (int c = 0; c < 4 / SG; ++c) {
+        for (int c = 0; c < D / 32; ++c) {
           uint32_t ov[32];
-          tmem_ld32(tmem + lane_base + kOCol + (half * 2 + c) * 32, ov);
+          tmem_ld32(tmem + lane_base + kOCol + c * 32, ov);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * corr);
-          tmem_st32(tmem + lane_base + kOCol + (half * 2 + c) * 32, ov);
+          tmem_st32(tmem + lane_base + kOCol + c * 32, ov);
         }
       }
       const float nm = MODE != kModNone && m_used == -INFINITY ? 0.f : -m_used;
+      auto weigh = [&](auto is_raw) {
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        auto weigh = [&](auto is_raw) {
-#pragma unroll
-          for (int c = 0; c < Q; ++c) {
-            uint32_t pk[16];
-            ts.template weigh<decltype(is_raw)::value>(pk, sv[h], c, nm, found[h].near, l_sum[h], l_odd[h]);
-            tmem_st16(tmem + lane_base + s * 128 + ((half + h) * Q + c) * 16, pk);
-          }
-        };
-        if ((MODE & (kModCap | kModBias)) == 0 || found[h].raw)
-          weigh(std::true_type{});
-        else
-          weigh(std::false_type{});
-      }
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+          ts.template weigh<decltype(is_raw)::value>(pk, sv, c, nm, found.near, l_sum, l_odd);
+          tmem_st16(tmem + lane_base + s * 128 + c * 16, pk);
+        }
+      };
+      if ((MODE & (kModCap | kModBias)) == 0 || found.raw)
+        weigh(std::true_type{});
+      else
+        weigh(std::false_type{});
       // Zero this CTA's V rows past the last visible key inside the final 16-key
       // step, and before the first visible one inside the first: a block may
       // hold stale or NaN rows there, and 0 * NaN would reach O. The tile's data
@@ -492,14 +491,14 @@ __global__ void __maxnreg__(Roles<SG>::kRegs) prefill_pair_kernel(const __grid_c
         const int tail = (kSubKeys - valid % kSubKeys) % kSubKeys;
         if (tail) {
           uint8_t *sV = sKV + (j % kStages) * Lay::kStageBytes + Lay::kKBytes;
-          for (int i = threadIdx.x; i < tail * 8; i += 128 * SG)
+          for (int i = tid; i < tail * 8; i += 128)
             *reinterpret_cast<uint4 *>(sV + (valid + i / 8) * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
       }
       if (MODE != kModNone && tile_j == 0 && kv_begin > base) {
         uint8_t *sV = sKV + (j % kStages) * Lay::kStageBytes + Lay::kKBytes;
-        for (int i = threadIdx.x; i < (kv_begin - base) * 8; i += 128 * SG)
+        for (int i = tid; i < (kv_begin - base) * 8; i += 128)
           *reinterpret_cast<uint4 *>(sV + i * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         wrote_v = true;
@@ -514,19 +513,31 @@ __global__ void __maxnreg__(Roles<SG>::kRegs) prefill_pair_kernel(const __grid_c
         else
           mbar_arrive_remote_cta_release(p_ready0 + s * 8);
       }
+      if constexpr (MODE != kModNone && SG == 1) {  // the next step's parity
+        const float t0 = l_sum, t1 = l_odd;
+        l_sum = k_sum, l_odd = k_odd;
+        k_sum = t0, k_odd = t1;
+      }
     }
     if (ok && (ntiles == 0 ||
                warp_wait_or_abort(bar + kPVDone + (ntiles - 1) % kSBufs, ((ntiles - 1) / kSBufs) & 1, abort_flag))) {
       tc_fence_after();
-      float l_row = l_sum[0] + l_odd[0];
-      if constexpr (H == 2) l_row += l_sum[1] + l_odd[1];
-      if constexpr (SG == 2) {  // the other half's share of the row sum
-        float *mine = row_max + (ntiles & 1) * 256 + mrow;
-        mine[half * 128] = l_row;
+      float l_row = l_sum + l_odd;
+      if constexpr (MODE != kModNone && SG == 1) l_row = __fadd_rn(l_row, k_sum + k_odd);
+      if constexpr (SG == 2) {
+        if (ntiles > 0 && ((ntiles - 1) & 1) != group) {  // the last step was the other group's
+          ok = warp_wait_or_abort(bar + kMaxReady + qw, (ntiles - 1) & 1, abort_flag);
+          const float m = step_max[((ntiles - 1) & 1) * 128];
+          if (m != m_used && m_used != -INFINITY) {
+            const float corr = ex2_approx(m_used - m);
+            l_row = __fmul_rn(l_sum, corr) + __fmul_rn(l_odd, corr);
+          }
+        }
+        group_sum[group * 128] = l_row;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar + kMaxReady + qw);
-        ok = warp_wait_or_abort(bar + kMaxReady + qw, ntiles & 1, abort_flag);  // (false: the status word says so)
-        l_row = mine[0] + mine[128];
+        if (lane == 0) mbar_arrive(bar + kSumReady + qw);
+        ok = ok && warp_wait_or_abort(bar + kSumReady + qw, 0, abort_flag);  // (if not, the status word says so)
+        l_row = __fadd_rn(group_sum[0], group_sum[128]);
       }
       const float inv = 1.f / l_row;
       // a row that sees nothing gives zeros, whatever O holds (an empty pair's O was never written)
@@ -539,7 +550,7 @@ __global__ void __maxnreg__(Roles<SG>::kRegs) prefill_pair_kernel(const __grid_c
                                                  mrow % G) * D);
 #pragma unroll
         for (int k = 0; k < 4 / SG; ++k) {
-          const int c = half * 2 + k;
+          const int c = group * 2 + k;
           uint32_t ov[32];
           tmem_ld32(tmem + lane_base + kOCol + c * 32, ov);
           tmem_wait_ld();
@@ -624,7 +635,7 @@ cudaError_t launch_pair_t(const StepArgs &a, const CUtensorMap &tq, const CUtens
   return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<NST, MODE, SG>, tq, tk, tv, a, items, rows_per_tile);
 }
 
-// One softmax warpgroup beside decode CTAs and wherever scores are only masked; two for caps and biases.
+// Caps and biases: two softmax warpgroups, but one beside decode CTAs.
 template <bool BESIDE>
 cudaError_t launch_pair_m(const StepArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           int32_t rows_per_tile, int32_t num_items, const int32_t *items, cudaStream_t stream) {
