@@ -241,6 +241,7 @@ pkv_status pkv::attention(const void *q, const int32_t *cu_seqlens_q, int32_t nu
   a.head_dim = head_dim;
   a.decode_rows_max = info->decode_rows_max;
   set_mod(a, mod);
+  a.num_partials = info->num_partials;
   const float s = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
   a.scale_log2 = s * 1.4426950408889634f;
   a.work = work;
@@ -415,6 +416,7 @@ static pkv_status attention_quant(int32_t bits, const void *q, const int32_t *cu
   a.head_dim = head_dim;
   a.decode_rows_max = info->decode_rows_max;
   set_mod(a, mod);
+  a.num_partials = info->num_partials;
   const float s = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
   a.scale_log2 = s * 1.4426950408889634f;
   a.work = work;

@@ -107,14 +107,20 @@ __device__ __forceinline__ void load_q(uint32_t (&qf)[NT][D / 16][2], const Task
   }
 }
 
+// The footprint that runs beside chunk CTAs stays within 208 registers, the most
+// that leaves room for it there (the modified variants would take up to 219: a
+// 509-row chunk with a prefix beside four decode rows then took 38.7 us, not 30.2).
+template <int NW, int NS>
+constexpr int kDecodeRegs = NW == kDecodeWarpsBesideChunk && NS == kDecodeStagesBesideChunk ? 208 : 255;
+
 // NT: 8-column MMA tiles of (row, q head) columns; MULTI: segments may hold
 // more than one row (otherwise every segment is a single decode row).
 // NW, NS: warps per CTA and stages per warp ring. A warp's stream of
 // sub-tiles is latency-bound (its ring's bytes per HBM round trip), so steps
 // with fewer tasks than warps run fewer warps with deeper rings; the math of
-// a task does not depend on them.
+// a task does not depend on them. MOD: modified scores (see above).
 template <int D, int NT, bool MULTI, bool MOD, int NW, int NS>
-__global__ void __launch_bounds__(NW * 32, 1)
+__global__ void __maxnreg__((kDecodeRegs<NW, NS>))
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const StepArgs a, const int32_t *__restrict__ items, int num_items) {
   using Cfg = DecodeCfg<D, NW, NS>;
@@ -535,7 +541,8 @@ __device__ __forceinline__ MergeRow merge_row(const StepArgs &a, const int32_t *
     const int L = __ldg(a.context_lens + slot);
     r.row = row0 + ri;
     r.bad = __ldg(a.seq_slot + seg) != slot || __ldg(a.cu_seqlens_q + seg + 1) - row0 != r.nrows ||
-            (a.modified ? (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS < r.spans
+            (a.modified ? (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS < r.spans ||
+                              static_cast<int64_t>(r.pbase) + static_cast<int64_t>(r.spans - 1) * r.nrows >= a.num_partials
                         : (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS != r.spans) ||
             row0 < 0 || row0 + r.nrows > a.total_q ||
             r.nrows > L;

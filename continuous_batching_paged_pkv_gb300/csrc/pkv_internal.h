@@ -53,6 +53,7 @@ struct StepArgs {
   int32_t window;
   const float *alibi_slopes;
   const int32_t *key_begin, *key_end;
+  int32_t num_partials;  // span partials in the workspace: a modified list's items must stay among them
 };
 
 // pkv_attention with the output's location: out_on_host marks `out` as host

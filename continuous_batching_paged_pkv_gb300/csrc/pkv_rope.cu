@@ -237,7 +237,7 @@ bool rows_meet(const void *x, int64_t x_stride, int64_t x_width, const void *y, 
 
 // Rows of `width` elements need 16-byte vectors and rows that do not overlap.
 bool bad_rows(const void *p, int64_t stride, int64_t width, int64_t rows) {
-  return !p || !aligned16(p) || stride % 8 != 0 || (rows > 1 && stride < width) || stride > (int64_t(1) << 40);
+  return !p || !aligned16(p) || stride % 8 != 0 || (rows > 1 && stride < width) || stride > (int64_t(1) << 60) / rows;
 }
 
 pkv_status check_rope(const pkv_rope_table *rope, int32_t head_dim) {

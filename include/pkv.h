@@ -640,9 +640,10 @@ pkv_status pkv_plan_work_mod(const int32_t *cu_seqlens_q, int32_t num_seqs, cons
 /*
  * pkv_attention with modified scores: same arguments, results, workspace and
  * ordering rules, but for `mod` (its pointers are device memory, with the
- * values that pkv_plan_work_mod saw) and a work list and info from
- * pkv_plan_work_mod. A row whose bounds reach past the keys that the list
- * covers sets PKV_DEV_BAD_SEGMENT (decode path).
+ * values that pkv_plan_work_mod saw; like q, they are read before the wait for
+ * the previous kernel) and a work list and info from pkv_plan_work_mod. Items
+ * that do not fit the step are skipped and set PKV_DEV_BAD_SEGMENT, and so do, on
+ * the decode path, bounds that reach past the keys of a row's own spans.
  */
 pkv_status pkv_attention_mod(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
                              const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,

@@ -295,6 +295,69 @@ def test_bad_blocks_are_reported():
     assert B.pkv_check_device_status(ds.status) & 2
 
 
+def test_a_list_of_another_step_is_reported_not_followed():
+    """Items that name partials past the workspace, or spans past the context, are skipped and set the status."""
+    heads = dict(num_q_heads=8, num_kv_heads=2, head_dim=128)
+    w = W.random_step(4, [(1, 900), (2, 600)], **heads)
+    _, ds = run(w, "bf16", make_mod("cap", w, 0))
+    good = ds.work.clone()
+    nd, nc = ds.info.num_decode_items, ds.info.num_combine_items
+    for at, word in ((3, ds.info.num_partials), (3, 2 ** 31 - 1), (2, 0x7FFFFF | 16 << 27), (2, 17 << 27), (2, 31 << 27),
+                     (0, 2), (1, 5), (nd * 4 + 3, ds.info.num_partials - 2), (nd * 4 + 2, 65535), (nd * 4 + 2, 0)):
+        assert nc > 0
+        bad = good.clone()
+        bad[at] = word if word < 2 ** 31 else word - 2 ** 32
+        ds.work.copy_(bad)
+        R.run_attention(ds)
+        assert B.pkv_check_device_status(ds.status) & 4, (at, word)
+    ds.work.copy_(good)
+    ds.out.zero_()
+    R.run_attention(ds)
+    assert B.pkv_check_device_status(ds.status) == 0
+    check(R.out_f32(ds), w, "bf16", make_mod("cap", w, 0), "after the bad lists")
+
+
+def test_bounds_wider_than_the_plan_are_reported():
+    w = W.random_step(4, [(1, 900), (1, 300)], num_q_heads=8, num_kv_heads=2, head_dim=128)
+    mod = B.ScoreMod(key_begin=np.array([700, 280]))
+    _, ds = run(w, "bf16", mod)
+    ds.mod.key_begin.copy_(torch.tensor([700, 100], dtype=torch.int32))
+    R.run_attention(ds)
+    assert B.pkv_check_device_status(ds.status) & 4
+
+
+def test_pools_past_2_31_elements():
+    """Rotation, append and windowed attention in the last blocks of pools of 2.2e9 elements each."""
+    hq, hkv, d, bs, nb, n = 16, 8, 128, 16, 134300, 300
+    kp = torch.empty(nb, hkv, bs, d, dtype=torch.bfloat16, device="cuda")
+    vp = torch.empty_like(kp)
+    g = torch.Generator("cuda").manual_seed(1)
+    q, k, v = torch.randn(n, hq + 2 * hkv, d, generator=g, device="cuda", dtype=torch.bfloat16).split([hq, hkv, hkv], 1)
+    pool = B.Pool(nb, bs, 2, 32, free_order=np.arange(nb - 40, nb, dtype=np.int32))
+    assert pool.admit(1, n) == B.PKV_OK
+    low = pool.lower([(1, n)])
+    assert low.slot_mapping.max() * hkv * d > 2 ** 31
+    plan = B.pkv_rope_plan(d)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    qr, out = torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda"), torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda")
+    pos = R._i32(np.arange(n), "cuda")
+    B.pkv_rope_cache_write(q, k, v, pos, plan.phase_tensor("cuda"), R._i64(low.slot_mapping, "cuda"), qr, kp, vp, rot_dim=d,
+                           device_status=status)
+    work, info = B.pkv_plan_work_mod(low.cu_seqlens_q, low.seq_slot, low.context_lens, max_slots=2, max_blocks_per_slot=32,
+                                     block_size=bs, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, window=77)
+    room = torch.empty(max(1, info.workspace_bytes), dtype=torch.uint8, device="cuda")
+    B.pkv_attention_mod(qr, R._i32(low.cu_seqlens_q, "cuda"), R._i32(low.seq_slot, "cuda"), R._i32(low.context_lens, "cuda"),
+                        R._i32(pool.block_tables(), "cuda"), kp, vp, R._i32(work, "cuda"), info, out, room,
+                        mod=B.ScoreMod(window=77), device_status=status)
+    assert B.pkv_check_device_status(status) == 0
+    kr = torch.empty(n, hkv, d, dtype=torch.bfloat16, device="cuda")
+    B.pkv_rope(k, pos, plan.phase_tensor("cuda"), kr, rot_dim=d)
+    f = lambda t: t.float().cpu().numpy()  # noqa: E731
+    p = np.arange(n)
+    want, tol = SM.attention(f(qr), f(kr), f(v), p, *SM.bounds(p, n, window=77), d ** -0.5)
+    assert (np.abs(f(out) - want) <= tol).all()
+
+
 def test_arguments_are_checked():
     w = W.random_step(4, [(1, 300), (20, 90)], num_q_heads=8, num_kv_heads=2, head_dim=64)
     _, ds = run(w, "bf16", make_mod("documents", w, 0))

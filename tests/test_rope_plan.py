@@ -102,7 +102,7 @@ def _write(table=None, **kw):
                                          a["nb"], a["bs"], None, None)
 
 
-@pytest.mark.parametrize("kw", [dict(q=None), dict(k=AT + 8), dict(qs=510), dict(qs=504), dict(ks=128), dict(t=-1),
+@pytest.mark.parametrize("kw", [dict(q=None), dict(k=AT + 8), dict(qs=1 << 60), dict(qs=510), dict(qs=504), dict(ks=128), dict(t=-1),
                                 dict(hq=0), dict(hkv=0), dict(nb=0), dict(bs=0), dict(pos=None), dict(pos=AT + 2),
                                 dict(sm=AT + 4), dict(kp=None), dict(vp=AT + 4), dict(out=None),
                                 dict(out=AT + 16),               # shifted onto the input rows
