@@ -81,7 +81,8 @@ bool encode_pool(CUtensorMap *m, const void *pool, int64_t rows, int32_t head_di
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Key pool at head_dim 128 for the chunk kernel, seen as five dimensions
+// Key pool at head_dim 128 for the chunk kernel (and both pools for the modified
+// decode kernel), seen as five dimensions
 // (column within a 64-column half, key within 8, half, group of 8 keys within
 // the block, block x kv head): one box is a whole 16-key sub-tile, 4 KiB,
 // landing as [key group][half][8 keys][128 B] in shared memory, so each
@@ -253,13 +254,17 @@ pkv_status pkv::attention(const void *q, const int32_t *cu_seqlens_q, int32_t nu
   a.task_counter =
       need ? reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + acc_bytes + ml_bytes) : nullptr;
 
-  CUtensorMap tk, tv, tq, tks;
+  CUtensorMap tk, tv, tq, tks, tvs;
   if (!encode_pool(&tk, k_pool, rows, head_dim) || !encode_pool(&tv, v_pool, rows, head_dim))
     return PKV_ERR_CUDA;
+  const bool whole_boxes = mod && head_dim == 128 && info->num_decode_items > 0;  // the modified decode kernel's boxes
   const int32_t rpt = pkv::prefill_rows_per_tile(a.group);
   if (info->num_prefill_items > 0 &&
       (!encode_q(&tq, q, total_q, num_q_heads, head_dim, a.group, rpt) ||
        (head_dim == 128 && !encode_pool_subtiles(&tks, k_pool, num_blocks * num_kv_heads, block_size))))
+    return PKV_ERR_CUDA;
+  if (whole_boxes && (!encode_pool_subtiles(&tks, k_pool, num_blocks * num_kv_heads, block_size) ||
+                      !encode_pool_subtiles(&tvs, v_pool, num_blocks * num_kv_heads, block_size)))
     return PKV_ERR_CUDA;
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -283,7 +288,8 @@ pkv_status pkv::attention(const void *q, const int32_t *cu_seqlens_q, int32_t nu
                         : pkv::launch_prefill(a, tq, rpt, info->num_prefill_items, pre, st);
   cudaStream_t dst = side ? side->stream : st;
   if (e == cudaSuccess && side) e = cudaStreamWaitEvent(side->stream, side->fork, 0);
-  if (e == cudaSuccess) e = pkv::launch_decode(a, tk, tv, info->num_decode_items, dec, beside, dst);
+  if (e == cudaSuccess)
+    e = pkv::launch_decode(a, whole_boxes ? tks : tk, whole_boxes ? tvs : tv, info->num_decode_items, dec, beside, dst);
   if (e == cudaSuccess) e = pkv::launch_merge(a, info->num_combine_items, info->num_long_combine_items, comb, dst);
   if (side) {
     // join even after a failed launch, so the caller's stream never runs ahead of queued work

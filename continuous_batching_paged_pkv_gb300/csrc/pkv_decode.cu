@@ -127,6 +127,12 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
   constexpr int KT = D / 16;  // k-steps of QK^T, m-tiles of PV
   constexpr int NST = Cfg::kStages;
   constexpr int kMaxRows = MULTI ? 16 : 1;
+  // Modified scores at head_dim 128: a sub-tile of K or V is one 4 KiB box (as the
+  // chunk kernel loads K), [8-key group][half][8 keys][128 B], two TMA instructions
+  // a stage instead of four.
+  constexpr bool kWholeBoxes = MOD && D == 128;
+  constexpr int kHalfStep = kWholeBoxes ? 1024 : Cfg::kHalfBytes;  // from one 64-column half to the other
+  const int block_shift = 31 - __clz(a.block_size);                // block sizes are powers of two
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align1024(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -189,10 +195,16 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
       uint8_t *dst = ring + pstage * Cfg::kStageBytes;
       if (row >= 0) {
         mbar_arrive_expect_tx(bar, Cfg::kStageBytes);
+        if constexpr (kWholeBoxes) {
+          const int key8 = (row & (a.block_size - 1)) >> 3, block = row >> block_shift;
+          tma_load_5d_hint(dst, &tmap_k, 0, 0, 0, key8, block, bar, policy);
+          tma_load_5d_hint(dst + Cfg::kTileBytes, &tmap_v, 0, 0, 0, key8, block, bar, policy);
+        } else {
 #pragma unroll
-        for (int h = 0; h < Cfg::kHalves; ++h) {
-          tma_load_2d_hint(dst + h * Cfg::kHalfBytes, &tmap_k, h * 64, row, bar, policy);
-          tma_load_2d_hint(dst + Cfg::kTileBytes + h * Cfg::kHalfBytes, &tmap_v, h * 64, row, bar, policy);
+          for (int h = 0; h < Cfg::kHalves; ++h) {
+            tma_load_2d_hint(dst + h * Cfg::kHalfBytes, &tmap_k, h * 64, row, bar, policy);
+            tma_load_2d_hint(dst + Cfg::kTileBytes + h * Cfg::kHalfBytes, &tmap_v, h * 64, row, bar, policy);
+          }
         }
       } else {
         mbar_arrive(bar);  // nothing loaded; the consumer masks this sub-tile out
@@ -228,13 +240,14 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
   // half, for K (A operand, rows = keys) and V (transposed A operand).
   // Row r's 16-byte chunk c sits at chunk c ^ (r % 8) (128-byte swizzle).
   uint32_t koff[4], voff[4];
+  auto row_offset = [](int r) { return kWholeBoxes ? (r >> 3) * 2048 + (r & 7) * 128 : r * 128; };
   {
     const int j = lane >> 3;
     const int rk = (lane & 7) + ((j & 1) << 3), rv = (lane & 7) + ((j >> 1) << 3);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      koff[q] = rk * 128 + ((((q << 1) + (j >> 1)) ^ (rk & 7)) << 4);
-      voff[q] = rv * 128 + ((((q << 1) + (j & 1)) ^ (rv & 7)) << 4);
+      koff[q] = row_offset(rk) + ((((q << 1) + (j >> 1)) ^ (rk & 7)) << 4);
+      voff[q] = row_offset(rv) + ((((q << 1) + (j & 1)) ^ (rv & 7)) << 4);
     }
   }
   const uint32_t ring_addr = smem_addr(ring);
@@ -307,7 +320,7 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
 #pragma unroll
       for (int kk = 0; kk < KT; ++kk) {
         uint32_t af[4];
-        ldmatrix_x4(af, kaddr + (kk >> 2) * Cfg::kHalfBytes + koff[kk & 3]);
+        ldmatrix_x4(af, kaddr + (kk >> 2) * kHalfStep + koff[kk & 3]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_bf16_16816((kk & 1) ? s1[nt] : s0[nt], af, qA[nt][kk][0], qA[nt][kk][1]);
       }
@@ -385,7 +398,7 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
 #pragma unroll
       for (int mt = 0; mt < KT; ++mt) {
         uint32_t af[4];
-        ldmatrix_x4_trans(af, kaddr + Cfg::kTileBytes + (mt >> 2) * Cfg::kHalfBytes + voff[mt & 3]);
+        ldmatrix_x4_trans(af, kaddr + Cfg::kTileBytes + (mt >> 2) * kHalfStep + voff[mt & 3]);
         if (part) {
           af[0] &= mlo;
           af[1] &= mlo;
