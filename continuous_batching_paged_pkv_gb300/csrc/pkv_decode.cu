@@ -554,7 +554,7 @@ __device__ __forceinline__ MergeRow merge_row(const StepArgs &a, const int32_t *
     const int L = __ldg(a.context_lens + slot);
     r.row = row0 + ri;
     r.bad = __ldg(a.seq_slot + seg) != slot || __ldg(a.cu_seqlens_q + seg + 1) - row0 != r.nrows ||
-            (a.modified ? (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS < r.spans ||
+            (a.modified ? L / 64 + 2 < r.spans ||  // spans of 64 keys or more
                               static_cast<int64_t>(r.pbase) + static_cast<int64_t>(r.spans - 1) * r.nrows >= a.num_partials
                         : (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS != r.spans) ||
             row0 < 0 || row0 + r.nrows > a.total_q ||

@@ -127,10 +127,8 @@ struct TaskMod {
     u_hi = __reduce_max_sync(0xffffffffu, hi_l);
     a_lo = __reduce_max_sync(0xffffffffu, lane < n ? lo_l : 0);
     a_hi = __reduce_min_sync(0xffffffffu, lane < n ? hi_l : INT32_MAX);
-    // The rows' keys inside the span (all of them, if it is the only one) must be those the item names.
-    const int s0 = T.span * PKV_SPLIT_KEYS;
-    const int need0 = T.pbase < 0 ? u_lo : max(u_lo, s0), need1 = T.pbase < 0 ? u_hi : min(u_hi - s0, PKV_SPLIT_KEYS) + s0;
-    if (T.ok && need0 < need1 && (need0 < T.key0 || need1 > T.key1) && lane == 0 && a.status)
+    // Of a single span the item must name all the keys that the rows see.
+    if (T.ok && T.pbase < 0 && u_lo < u_hi && (u_lo < T.key0 || u_hi > T.key1) && lane == 0 && a.status)
       atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)

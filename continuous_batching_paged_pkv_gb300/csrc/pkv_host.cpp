@@ -343,6 +343,8 @@ pkv_status pkv_plan_lower(pkv_pool *p, const pkv_segment *plan, int32_t num_segm
 
 namespace {
 
+constexpr int64_t kSubsPerSpan = PKV_SPLIT_KEYS / pkv::kSubKeys;
+
 struct KeyRange {
   int64_t lo, hi;  // keys [lo, hi); lo >= hi: none
 };
@@ -362,6 +364,23 @@ KeyRange rows_see(const pkv_score_mod *mod, int64_t row0, int64_t first, int64_t
   }
   if (u.lo >= u.hi) u = {0, 0};
   return u;
+}
+
+// Keys per span of a segment whose rows see `keys` keys, with modified scores: 64
+// or 128 instead of PKV_SPLIT_KEYS while a step with all slots so long would still
+// have a warp of its own for each of its tasks (eight on each of 152 SMs), since a
+// warp takes its sub-tiles one after the other; but no more than 64 spans, whose
+// merge then costs more than they save. It depends on the segment and the tables'
+// shape, not on the rest of the step. Measured with spans of 64 / 128 / 256 keys:
+// five slots of 1024 keys, 8 kv heads: 10.0 / 11.1 / 15.4 us; one of 1000: 8.3 /
+// 10.4 / 14.7; one of 8000 (126 spans of 64): 16.8 / 13.8 / 15.5; sixteen of 2000
+// stay at 256: 25.7 (26.6 with 64).
+int32_t span_keys(int64_t keys, int32_t max_slots, int32_t num_kv_heads) {
+  for (int32_t s = 64; s < PKV_SPLIT_KEYS; s *= 2) {
+    const int64_t spans = ceil_div(keys, s);
+    if (spans <= pkv::kLongMergeSpans && spans * max_slots * num_kv_heads <= 8 * 152) return s;
+  }
+  return PKV_SPLIT_KEYS;
 }
 
 // The work list of a step: of pkv_plan_work without `mod`, of pkv_plan_work_mod with it.
@@ -424,18 +443,22 @@ pkv_status plan_work(const int32_t *cu, int32_t num_seqs, const int32_t *seq_slo
       if (u.hi == 0) {
         dec_short.push_back({{s, slot, 0, -1}, 0});
       } else {
-        const int64_t sp0 = u.lo / PKV_SPLIT_KEYS, sp1 = (u.hi - 1) / PKV_SPLIT_KEYS;
+        // Eight sub-tiles or fewer (sixteen with long spans) are one span wherever they
+        // lie: two spans would need a merge (100 keys: 4.5 us against 7.6).
+        const int32_t sk = span_keys(u.hi - u.lo, max_slots, num_kv_heads);
+        const int64_t subs = ceil_div(u.hi, pkv::kSubKeys) - u.lo / pkv::kSubKeys;
+        const bool whole = subs <= (sk == PKV_SPLIT_KEYS ? kSubsPerSpan : kSubsPerSpan / 2);
+        const int64_t sp0 = whole ? 0 : u.lo / sk, sp1 = whole ? 0 : (u.hi - 1) / sk;
         const int32_t spans = static_cast<int32_t>(sp1 - sp0 + 1);
-        if (sp1 >= (1 << 23) || spans >= (1 << 16)) return PKV_ERR_UNSUPPORTED;
+        if (u.hi > (int64_t(1) << 23) * PKV_SPLIT_KEYS || sp1 - sp0 + 1 >= (1 << 16)) return PKV_ERR_UNSUPPORTED;
         if (static_cast<int64_t>(partials) + static_cast<int64_t>(spans) * n > INT32_MAX) return PKV_ERR_UNSUPPORTED;
         for (int64_t sp = sp0; sp <= sp1; ++sp) {
-          const int64_t k0 = std::max(u.lo, sp * PKV_SPLIT_KEYS) / pkv::kSubKeys;
-          const int64_t k1 = ceil_div(std::min(u.hi, (sp + 1) * PKV_SPLIT_KEYS), pkv::kSubKeys);
-          const uint32_t sub = PKV_SPLIT_KEYS / pkv::kSubKeys;
-          const uint32_t w = static_cast<uint32_t>(sp) | (static_cast<uint32_t>(k0) % sub) << 23 |
+          const int64_t k0 = (whole ? u.lo : std::max(u.lo, sp * sk)) / pkv::kSubKeys;
+          const int64_t k1 = ceil_div(whole ? u.hi : std::min(u.hi, (sp + 1) * sk), pkv::kSubKeys);
+          const uint32_t w = static_cast<uint32_t>(k0 / kSubsPerSpan) | static_cast<uint32_t>(k0 % kSubsPerSpan) << 23 |
                              static_cast<uint32_t>(k1 - k0) << 27;
           const int32_t first = spans > 1 ? partials + static_cast<int32_t>(sp - sp0) * n : -1;
-          (k1 - k0 == sub ? dec : dec_short).push_back({{s, slot, static_cast<int32_t>(w), first}, k1 - k0});
+          (k1 - k0 == kSubsPerSpan ? dec : dec_short).push_back({{s, slot, static_cast<int32_t>(w), first}, k1 - k0});
         }
         if (spans > 1) {
           for (int32_t i = 0; i < n; ++i)

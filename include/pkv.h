@@ -623,7 +623,10 @@ typedef struct pkv_score_mod {
  * (key_begin and key_end are HOST copies here; softcap and alibi_slopes are
  * not looked at). The key spans of the decode path and the tiles of the chunk
  * path cover the keys that some row of the segment (of the tile pair) sees,
- * and nothing else; spans stay cut at multiples of PKV_SPLIT_KEYS. Same
+ * and nothing else. Spans are cut at multiples of PKV_SPLIT_KEYS, or of 64 or
+ * 128 keys where the slots are so few that every span of a full step has a warp
+ * of its own; the cut depends on the keys that the segment sees, max_slots and
+ * num_kv_heads, not on the other segments of the step. Same
  * validation, sizes and errors as pkv_plan_work, and PKV_ERR_INVALID_ARG for a
  * negative window. info->modified is 1.
  *
@@ -642,8 +645,8 @@ pkv_status pkv_plan_work_mod(const int32_t *cu_seqlens_q, int32_t num_seqs, cons
  * ordering rules, but for `mod` (its pointers are device memory, with the
  * values that pkv_plan_work_mod saw; like q, they are read before the wait for
  * the previous kernel) and a work list and info from pkv_plan_work_mod. Items
- * that do not fit the step are skipped and set PKV_DEV_BAD_SEGMENT, and so do, on
- * the decode path, bounds that reach past the keys of a row's own spans.
+ * that do not fit the step are skipped and set PKV_DEV_BAD_SEGMENT; bounds that
+ * reach past the keys the list covers set it where a segment has a single span.
  */
 pkv_status pkv_attention_mod(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
                              const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,

@@ -73,11 +73,16 @@ def test_work_list_covers_what_the_rows_see(seed):
                 continue
             k0 = span * 256 + first * 16
             order = np.argsort(k0)
-            # back to back from the first sub-tile with a visible key to the last, cut at multiples of 256 keys
+            # back to back from the first sub-tile with a visible key to the last, cut at multiples of the span: the
+            # shortest that leaves at most 64 spans and 8 x 152 tasks with all nine slots as long, 256 keys at most
+            cut = next((k for k in (64, 128) if -(-(u[1] - u[0]) // k) <= min(64, 8 * 152 / (9 * heads[1]))), 256)
+            subs = -(-u[1] // 16) - u[0] // 16
+            assert (len(mine) == 1) == (subs <= (16 if cut == 256 else 8) or u[0] // cut == (u[1] - 1) // cut)
             assert k0[order][0] == u[0] // 16 * 16
             assert (k0 + count * 16)[order][-1] == -(-u[1] // 16) * 16
             assert ((k0 + count * 16)[order][:-1] == k0[order][1:]).all()
-            assert (k0[order][1:] % 256 == 0).all() and (count >= 1).all() and (first + count <= 16).all()
+            assert (k0[order][1:] % cut == 0).all() and (count >= 1).all() and (count <= 16).all()
+            assert len(mine) == 1 or ((first * 16) % cut + count * 16 <= cut).all()
             merges = comb[comb[:, 0] == s]
             if len(mine) == 1:
                 assert mine[0, 3] == -1 and not len(merges)
@@ -102,9 +107,9 @@ def test_work_list_covers_what_the_rows_see(seed):
 
 
 def test_causal_list_matches_the_plain_one():
-    """Without any bound the decode spans, tiles and merges are pkv_plan_work's."""
-    cu, slots, ctx = [0, 1, 4, 204, 205], [0, 1, 2, 3], [700, 5, 900, 256]
-    shape = dict(max_slots=4, max_blocks_per_slot=64, block_size=16, num_q_heads=32, num_kv_heads=8, head_dim=128)
+    """Without any bound, in a table too wide for shorter spans, the spans, tiles and merges are pkv_plan_work's."""
+    cu, slots, ctx = [0, 1, 4, 204, 205], [0, 1, 2, 3], [700, 5, 900, 256] + [0] * 124
+    shape = dict(max_slots=128, max_blocks_per_slot=64, block_size=16, num_q_heads=32, num_kv_heads=8, head_dim=128)
     w0, i0 = B.pkv_plan_work(cu, slots, ctx, **shape)
     w1, i1 = B.pkv_plan_work_mod(cu, slots, ctx, **shape)
     for f in ("num_decode_items", "num_prefill_items", "num_combine_items", "num_partials", "work_words",
