@@ -554,11 +554,14 @@ __device__ __forceinline__ MergeRow merge_row(const StepArgs &a, const int32_t *
     const int L = __ldg(a.context_lens + slot);
     r.row = row0 + ri;
     r.bad = __ldg(a.seq_slot + seg) != slot || __ldg(a.cu_seqlens_q + seg + 1) - row0 != r.nrows ||
-            (a.modified ? L / 64 + 2 < r.spans ||  // spans of 64 keys or more
-                              static_cast<int64_t>(r.pbase) + static_cast<int64_t>(r.spans - 1) * r.nrows >= a.num_partials
-                        : (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS != r.spans) ||
             row0 < 0 || row0 + r.nrows > a.total_q ||
             r.nrows > L;
+    // modified scores: spans of 64 keys or more over part of the history, partials inside the workspace
+    if (a.modified)
+      r.bad |= L / 64 + 2 < r.spans ||
+               r.pbase + static_cast<int64_t>(r.spans - 1) * r.nrows >= static_cast<int64_t>(a.num_partials);
+    else
+      r.bad |= (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS != r.spans;
   }
   return r;
 }

@@ -81,9 +81,10 @@ __device__ __forceinline__ void finalize(Task &T, const StepArgs &a, int lane, i
   T.ok = T.raw_ok && T.sslot == T.slot && T.nrows >= 1 && T.nrows <= max_rows && T.nrows * a.group <= max_cols && T.nrows <= T.L &&
          T.L >= 1 &&
          static_cast<int64_t>(T.L) <= static_cast<int64_t>(a.max_blocks_per_slot) * a.block_size &&
-         (T.key0 < T.L || (MOD && T.subs == 0)) && (!MOD || (T.subs <= PKV_SPLIT_KEYS / kSubKeys && (T.pbase < 0 || T.pbase <= a.num_partials - T.nrows))) &&
-         T.row0 >= 0 &&
+         (T.key0 < T.L || (MOD && T.subs == 0)) && T.row0 >= 0 &&
          static_cast<int64_t>(T.row0) + T.nrows <= a.total_q;
+  if constexpr (MOD)  // at most a span's sub-tiles, and the partials inside the workspace
+    T.ok = T.ok && T.subs <= PKV_SPLIT_KEYS / kSubKeys && (T.pbase < 0 || T.pbase <= a.num_partials - T.nrows);
   if (!T.ok) {
     if (lane == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
     return;
