@@ -135,8 +135,10 @@ uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 bool bad_mod(const pkv_score_mod *mod, const pkv_work_info *info) {
   if (info->modified != (mod ? 1 : 0)) return true;
   if (!mod) return false;
-  return !(mod->softcap >= 0.f) || std::isinf(mod->softcap) || mod->window < 0 || !aligned(mod->alibi_slopes, 4) ||
-         !aligned(mod->key_begin, 4) || !aligned(mod->key_end, 4);
+  // The kernels' cap is off by its own 2^-21: a larger one would shift logits by more than the weights' bf16
+  // rounding, and at the ends of the type 2 / cap or cap * log2(e) would overflow.
+  if (mod->softcap != 0.f && !(mod->softcap >= 0x1p-20f && mod->softcap <= 0x1p12f)) return true;
+  return mod->window < 0 || !aligned(mod->alibi_slopes, 4) || !aligned(mod->key_begin, 4) || !aligned(mod->key_end, 4);
 }
 
 void set_mod(pkv::StepArgs &a, const pkv_score_mod *mod) {

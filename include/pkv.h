@@ -611,7 +611,7 @@ pkv_status pkv_attention_q4(const void *q, const int32_t *cu_seqlens_q, int32_t 
  * the segment's tile sees reaches none.
  * ---------------------------------------------------------------------- */
 typedef struct pkv_score_mod {
-    float softcap;             /* 0: none; else finite and > 0 */
+    float softcap;             /* 0: none; else 2^-20 .. 2^12 (the capped score is within softcap * 2^-21) */
     int32_t window;            /* 0: none; else >= 1 */
     const float *alibi_slopes; /* float [num_q_heads], or NULL; finite */
     const int32_t *key_begin;  /* int32 [total_q], or NULL */

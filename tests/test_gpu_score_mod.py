@@ -176,6 +176,15 @@ def test_scores_all_far_below_zero(sign):
         check(got, w, "bf16", mod, str(mod))
 
 
+@pytest.mark.parametrize("cap", [2.0 ** -20, 0.01, 700.0, 4096.0])
+def test_caps_from_the_least_to_the_largest(cap):
+    for d in (64, 128):
+        w = W.random_step(12, SHAPES["mixed"], num_q_heads=8, num_kv_heads=2, head_dim=d)
+        for mod in (B.ScoreMod(softcap=cap), B.ScoreMod(softcap=cap, alibi_slopes=_slopes(8), window=150)):
+            got, _ = run(w, "bf16", mod)
+            check(got, w, "bf16", mod, str(mod))
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("kv", ["bf16", "q8"])
 def test_keys_that_nobody_sees_are_not_read(kv, d):
@@ -380,7 +389,7 @@ def test_arguments_are_checked():
     refused(5, (ds.k_pool, ds.v_pool[:3]))
     refused(kv="q8")
     refused(kv="fp8")
-    for mod in (B.ScoreMod(softcap=-1.0), B.ScoreMod(window=-2), B.ScoreMod(alibi_slopes=torch.ones(7, device="cuda")),
+    for mod in (B.ScoreMod(softcap=-1.0), B.ScoreMod(softcap=4097.0), B.ScoreMod(softcap=1e-7), B.ScoreMod(window=-2), B.ScoreMod(alibi_slopes=torch.ones(7, device="cuda")),
                 B.ScoreMod(alibi_slopes=torch.ones(8, dtype=torch.float64, device="cuda")),
                 B.ScoreMod(key_begin=ds.mod.key_begin[:5]), B.ScoreMod(key_end=ds.mod.key_begin.long())):
         refused(mod=mod)

@@ -141,7 +141,8 @@ def _call(fn="pkv_attention_mod", mod=None, info=None, null=False, d=64):
 
 @pytest.mark.parametrize("fn", ["pkv_attention_mod", "pkv_attention_mod_q8"])
 @pytest.mark.parametrize("mod", [(-1.0, 0, None, None, None), (math.inf, 0, None, None, None),
-                                 (math.nan, 0, None, None, None), (0.0, -1, None, None, None),
+                                 (math.nan, 0, None, None, None), (2.0 ** -21, 0, None, None, None),
+                                 (4097.0, 0, None, None, None), (1e38, 0, None, None, None), (0.0, -1, None, None, None),
                                  (0.0, 0, AT + 1, None, None), (0.0, 0, None, AT + 2, None), (0.0, 0, None, None, AT + 3)])
 def test_refused_modifications(fn, mod):
     assert _call(fn, mod) == 1
