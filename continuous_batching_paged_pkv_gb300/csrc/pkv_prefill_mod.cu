@@ -55,8 +55,10 @@ constexpr int kKStages = 3, kVStages = 2;
 constexpr int kTileBytes = kKeysPerTile * D * 2;  // Q, K or V tile: 128 rows x 128 B
 constexpr int kBoxBytes = kSubKeys * D * 2;
 constexpr int kBarOffset = (1 + kKStages + kVStages) * kTileBytes;
-constexpr int kSmem = kBarOffset + 256 + 1024;  // barriers/flags + alignment slack
-static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+constexpr int kRampOffset = kBarOffset + 256;  // after the barriers and flags: the bias step's operands
+template <int MODE>
+constexpr int kSmem = kRampOffset + (ramp_mode(MODE) ? 2 * kRampBytes : 0) + 1024;  // + alignment slack
+static_assert(2 * (kSmem<kModBias> + 1024) <= 228 * 1024, "two CTAs per SM");
 
 enum Bar : int {
   kQFull = 0,
@@ -110,6 +112,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kBarOffset);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  uint8_t *sRamp = smem + kRampOffset;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = blockIdx.y;
@@ -156,6 +159,13 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
     const int qrows = G * P;
     for (int i = threadIdx.x; i < (128 - qrows) * 8; i += blockDim.x)
       *reinterpret_cast<uint4 *>(sQ + (qrows + i / 8) * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+    if constexpr (ramp_mode(MODE)) {
+      const int r = threadIdx.x & 127;
+      if (threadIdx.x < 128)
+        store_ramp_slope(sRamp, r, r < qrows ? ramp_slope(a, g * G + r % G) : 0.f);
+      else
+        store_ramp_key(sRamp + kRampBytes, r, r);
+    }
     fence_proxy_async_smem();
   }
   if (warp == kWarpQK) {
@@ -241,6 +251,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
           for (int kk = 0; kk < D / 16; ++kk)
             tc_mma_ss(tmem, smem_desc_sw128(q_base + kk * 32, 16, 1024), smem_desc_sw128(k_base + kk * 32, 16, 1024),
                       idesc_qk, kk > 0 ? 1u : 0u);
+          if constexpr (ramp_mode(MODE)) tc_mma_ss(tmem, ramp_desc(sRamp), ramp_desc(sRamp + kRampBytes), idesc_qk, 1u);
           tc_commit(bar + kSFull);
           tc_commit(bar + kKEmpty + j % kKStages);
         }
@@ -360,7 +371,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
           tmem_st16(tmem + lane_base + kPCol + c * 16, pk);
         }
       };
-      if ((MODE & (kModCap | kModBias)) == 0 || found.raw)
+      if (!TileScores<MODE>::kCap && !TileScores<MODE>::kBias || found.raw)
         weigh(std::true_type{});
       else
         weigh(std::false_type{});
@@ -407,9 +418,9 @@ template <int MODE>
 cudaError_t launch_t(const StepArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                      int32_t rows_per_tile, int32_t num_items, const int32_t *items, cudaStream_t stream) {
   static std::atomic<uint64_t> configured{0};  // one bit per device
-  if (const cudaError_t e = allow_smem_once(prefill_mod_kernel<MODE>, kSmem, configured); e != cudaSuccess) return e;
+  if (const cudaError_t e = allow_smem_once(prefill_mod_kernel<MODE>, kSmem<MODE>, configured); e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(num_items), static_cast<unsigned>(a.num_kv_heads));
-  return launch_pdl(prefill_mod_kernel<MODE>, grid, dim3(kThreads), kSmem, stream, tq, tk, tv, a, items,
+  return launch_pdl(prefill_mod_kernel<MODE>, grid, dim3(kThreads), kSmem<MODE>, stream, tq, tk, tv, a, items,
                     rows_per_tile);
 }
 

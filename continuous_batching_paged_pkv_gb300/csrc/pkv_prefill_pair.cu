@@ -99,7 +99,7 @@ constexpr uint32_t kNegInfBits = 0xff800000u;
 
 // NST K/V tiles in flight: six when the chunk kernel has its SMs to itself (the
 // producer runs well ahead of the MMAs), three when a decode CTA shares each SM.
-template <int NST>
+template <int NST, bool RAMP = false>
 struct Layout {
   static constexpr int kStages = NST;
   static constexpr int kQHalf = 128 * 128;                 // 128 rows x 128 B: one 64-column half of D
@@ -108,7 +108,8 @@ struct Layout {
   static constexpr int kKBytes = (kKeysPerTile / 2 / kSubKeys) * kKSub;  // this CTA's 64 keys
   static constexpr int kVBytes = kKeysPerTile * 128;       // 128 keys x this CTA's 64 columns
   static constexpr int kStageBytes = kKBytes + kVBytes;    // 32 KiB: 4 K boxes of 4 KiB, 8 V boxes of 2 KiB
-  static constexpr int kBarOffset = kQBytes + kStages * kStageBytes;
+  static constexpr int kRampOffset = kQBytes + kStages * kStageBytes;  // the bias step's operands: 128 rows, 64 keys
+  static constexpr int kBarOffset = kRampOffset + (RAMP ? kRampBytes + kRampBytes / 2 : 0);
   static constexpr int kMaxOffset = kBarOffset + 320;      // two warpgroups: maxima, then sums, [2][128 rows] floats each
   template <int SG>
   static constexpr int kSmem = kMaxOffset + (SG == 2 ? 2048 : 0) + 1024;  // + alignment slack
@@ -170,7 +171,7 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
                                                                    const StepArgs a,
                                                                    const int32_t *__restrict__ items,
                                                                    int rows_per_tile) {
-  using Lay = Layout<NST>;
+  using Lay = Layout<NST, ramp_mode(MODE)>;
   constexpr int kWarpProducer = Roles<SG>::kWarpProducer, kWarpQK = Roles<SG>::kWarpQK, kWarpPV = Roles<SG>::kWarpPV;
   constexpr int kStages = NST;
   constexpr int kQFull = Bars<NST>::kQFull, kKVFull = Bars<NST>::kKVFull, kKVEmpty = Bars<NST>::kKVEmpty;
@@ -181,6 +182,7 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
   uint8_t *smem = align1024(smem_raw);
   uint8_t *sQ = smem;
   uint8_t *sKV = smem + Lay::kQBytes;
+  uint8_t *sRamp = smem + Lay::kRampOffset;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + Lay::kBarOffset);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -251,6 +253,13 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
       const int h = i / chunks, rem = i % chunks;
       *reinterpret_cast<uint4 *>(sQ + h * Lay::kQHalf + (qrows + rem / 8) * 128 + (rem % 8) * 16) =
           make_uint4(0, 0, 0, 0);
+    }
+    if constexpr (ramp_mode(MODE)) {
+      const int r = threadIdx.x & 127;
+      if (threadIdx.x < 128)
+        store_ramp_slope(sRamp, r, r < qrows ? ramp_slope(a, g * G + r % G) : 0.f);
+      else if (threadIdx.x < 192)
+        store_ramp_key(sRamp + kRampBytes, r, static_cast<int>(rank) * 64 + r);
     }
     fence_proxy_async_smem();
   }
@@ -348,6 +357,8 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
           tc_mma_ss_pair(tmem + s * 128, smem_desc_sw128(q_base + qoff, 16, 1024),
                          smem_desc_sw128(k_base + koff, 16, 2048), idesc_qk, kk > 0 ? 1u : 0u);
         }
+        if constexpr (ramp_mode(MODE))
+          tc_mma_ss_pair(tmem + s * 128, ramp_desc(sRamp), ramp_desc(sRamp + kRampBytes), idesc_qk, 1u);
         tc_commit_pair(bar + kSFull + s);
       }
       tc_commit_pair(bar + kDrain);
@@ -477,7 +488,7 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
           tmem_st16(tmem + lane_base + s * 128 + c * 16, pk);
         }
       };
-      if ((MODE & (kModCap | kModBias)) == 0 || found.raw)
+      if (!TileScores<MODE>::kCap && !TileScores<MODE>::kBias || found.raw)
         weigh(std::true_type{});
       else
         weigh(std::false_type{});
@@ -615,7 +626,7 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
 template <int NST, int MODE, int SG>
 cudaError_t launch_pair_t(const StepArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           int32_t rows_per_tile, int32_t num_items, const int32_t *items, cudaStream_t stream) {
-  constexpr int smem = Layout<NST>::template kSmem<SG>;
+  constexpr int smem = Layout<NST, ramp_mode(MODE)>::template kSmem<SG>;
   static std::atomic<uint64_t> configured{0};  // one bit per device
   if (const cudaError_t e = allow_smem_once(prefill_pair_kernel<NST, MODE, SG>, smem, configured); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -647,7 +658,7 @@ cudaError_t launch_pair_m(const StepArgs &a, const CUtensorMap &tq, const CUtens
     case kModMask | kModCap:
       return launch_pair_t<N2, kModMask | kModCap, SG>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
     case kModMask | kModBias:
-      return launch_pair_t<N2, kModMask | kModBias, SG>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+      return launch_pair_t<N2, kModMask | kModBias, 1>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
     default:
       return launch_pair_t<N2, kModMask | kModCap | kModBias, SG>(a, tq, tk, tv, rows_per_tile, num_items, items,
                                                                   stream);
