@@ -24,10 +24,18 @@
 // TMEM columns: [0, 128) S, [128, 192) P (bf16 pairs), [192, 256) O. P has
 // columns of its own, so S_{j+1} is computed while P_j is still to be written.
 // The kernel launches with 128 registers per thread; the softmax warpgroup raises
-// its share to 192 and the other lowers its own to 64. With a distance bias the
-// tiles go nearest first (as in the head_dim 128 kernel). Every mbarrier wait is
-// bounded; on expiry the CTA records PKV_DEV_TIMEOUT, drains its MMAs and frees
-// its TMEM before it returns.
+// its share to 192 and the other lowers its own to 64. A distance bias without a
+// cap comes with the scores (one more MMA per tile). Every mbarrier wait is bounded; on
+// expiry the CTA records PKV_DEV_TIMEOUT, drains its MMAs and frees its TMEM before
+// it returns.
+//
+// What it takes is two CTAs' chains of some 2800 cycles per tile (of which the
+// weights 960, their MMAs' issue 110 each) and, in short loops, a CTA's 6000 cycles
+// before its first tile and after its last. 8192 rows, 16 heads of 64, one stream
+// as the context: causal 207 us (665 TFLOP/s of what is seen), biased 217; windows of
+// 512 keys 49 us, of 128 keys 33 us; documents of 16 to 2048 tokens 57 us, biased
+// 63 us. The kernel for plain scores, with this one's masks and biases in its softmax
+// threads, took 1059 us (causal), 89 us (128 keys) and 228 us (documents, biased).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -146,8 +154,10 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
   const int kv_begin = min(u[0], u[1]), kv_end = u[1];
   const int base = kv_begin & ~(kSubKeys - 1);
   const int ntiles = (kv_end - base + kKeysPerTile - 1) / kKeysPerTile;  // 0: no row of the tile sees a key
+  // With a bias the nearest keys come first (as in the head_dim 128 kernel), but the cached ones before this step's.
   constexpr bool kDown = (MODE & kModBias) != 0;
-  auto tile_at = [&](int j) { return kDown ? ntiles - 1 - j : j; };
+  const int old = kDown ? min(max(L - n - base, 0) / kKeysPerTile, ntiles) : 0;
+  auto tile_at = [&](int j) { return !kDown ? j : j < old ? old - 1 - j : ntiles - 1 - (j - old); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(bar + i, i == kSFree || i == kPReady ? 4 : 1);
@@ -295,8 +305,10 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
     float m_used = -INFINITY;            // log2 units
     float l_sum = 0.f, l_odd = 0.f;      // row sum, as even and odd columns (packed adds)
     bool ok = true;
+    int tile_next = tile_at(0);
     for (int j = 0; j < ntiles; ++j) {
-      const int tile_j = tile_at(j), kt0 = base + tile_j * kKeysPerTile;
+      const int tile_j = tile_next, kt0 = base + tile_j * kKeysPerTile;
+      tile_next = kDown ? (j + 1 == old ? ntiles : tile_j) - 1 : j + 1;  // tile_at(j + 1) at less
       if (!(ok = warp_wait_or_abort(bar + kSFull, j & 1, abort_flag))) break;
       tc_fence_after();
       // Zero the V rows past the last visible key inside the final 16-key step,
@@ -371,7 +383,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
           tmem_st16(tmem + lane_base + kPCol + c * 16, pk);
         }
       };
-      if (!TileScores<MODE>::kCap && !TileScores<MODE>::kBias || found.raw)
+      if (!TileScores<MODE>::kCap || found.raw)
         weigh(std::true_type{});
       else
         weigh(std::false_type{});

@@ -42,8 +42,9 @@
 //
 // With modified scores (MODE) the pair's tiles start at the 16-key sub-tile of
 // the first key that some row sees and end with the last such key; each softmax
-// thread turns its row's scores into capped, biased logits, masks the keys
-// outside its row's interval and starts its running max at its first visible key.
+// thread turns its row's scores into capped logits, masks the keys outside its
+// row's interval and starts its running max at its first visible key. A distance
+// bias comes with the scores, as one more MMA per tile, or with a cap is added after it.
 //
 // TMEM columns (same in both CTAs): [128b, 128b+128) S/P buffer b for b < 3,
 // [384,512) O. Every mbarrier wait is
@@ -84,7 +85,7 @@ constexpr int kOCol = 384;
 // warpgroup of the other launches keeps the same two sums, so a row's bits do not
 // depend on which of the two ran. 384 threads launched with 168 registers, shares
 // of 208, 208 and 88, five K/V stages. 2048 rows at context 8192: capped 292 us
-// with one group, 273 us with two; biased 263 and 238 us; only masked 187 and 186 us
+// with one group, 271 us with two; biased 206 and 198 us; only masked 185 and 186 us
 // (the tensor core's chain S, P, O through three buffers sets the pace there).
 template <int SG>
 struct Roles {
@@ -235,9 +236,13 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
   // Tile taken at step j. A distance bias makes the nearest keys' logits the
   // largest, so those variants go from the last tile to the first: going up, the
   // running max would grow by slope * 128 with every tile and O be rescaled at
-  // each (2048 biased rows at context 8192 took 323 us going up).
+  // each. The tiles of cached keys come before those of this step's rows, at the
+  // price of one rescaling, since the latter wait for the kernel before (2048
+  // biased rows at context 8192, one call behind another: going up 272 us, straight
+  // down 233 us, so 206 us; with two softmax warpgroups 198 us).
   constexpr bool kDown = (MODE & kModBias) != 0;
-  auto tile_at = [&](int j) { return kDown ? ntiles - 1 - j : j; };
+  const int old = kDown ? min(max(L - n - base, 0) / kKeysPerTile, ntiles) : 0;
+  auto tile_at = [&](int j) { return !kDown ? j : j < old ? old - 1 - j : ntiles - 1 - (j - old); };
   const int32_t *bt_row = a.block_tables + static_cast<int64_t>(slot) * a.max_blocks_per_slot;
 
   if (threadIdx.x == 0) {
@@ -488,7 +493,7 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
           tmem_st16(tmem + lane_base + s * 128 + c * 16, pk);
         }
       };
-      if (!TileScores<MODE>::kCap && !TileScores<MODE>::kBias || found.raw)
+      if (!TileScores<MODE>::kCap || found.raw)
         weigh(std::true_type{});
       else
         weigh(std::false_type{});
@@ -658,7 +663,7 @@ cudaError_t launch_pair_m(const StepArgs &a, const CUtensorMap &tq, const CUtens
     case kModMask | kModCap:
       return launch_pair_t<N2, kModMask | kModCap, SG>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
     case kModMask | kModBias:
-      return launch_pair_t<N2, kModMask | kModBias, 1>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
+      return launch_pair_t<N2, kModMask | kModBias, SG>(a, tq, tk, tv, rows_per_tile, num_items, items, stream);
     default:
       return launch_pair_t<N2, kModMask | kModCap | kModBias, SG>(a, tq, tk, tv, rows_per_tile, num_items, items,
                                                                   stream);

@@ -150,13 +150,13 @@ __device__ __forceinline__ float tile_max(const uint32_t (&sv)[4][32]) {
 // The scores of a tile arrive as raw products; top() gives a reference for the
 // tile's running max (log2 units) and exponents() the pairs 2^x is taken of.
 //
-// A tile stays raw where it can: without a cap its unseen scores become -inf as
-// they are; with one, where every row of the warp sees it whole (most tiles). The
-// cap is then y P(y^2) with y = raw r, |y| <= 0.55 and P of degree 3, fitted here
+// Without a cap a tile's unseen scores become -inf as they are, and the bias is in
+// the scores but for `near`. With a cap a tile stays raw where every row of the warp
+// sees it whole (most tiles). The cap is then y P(y^2) with y = raw r, |y| <= 0.55 and P of degree 3, fitted here
 // to the least largest error of y P(y^2) (2^-21.5 in fp32 arithmetic), its
 // coefficients scaled so that a score costs 5 operations, the last of which also
 // subtracts the reference (2^x and 1/x would be two SFU operations of each score
-// beside the softmax's own 2^x); the bias is one more. The reference is then the
+// beside the softmax's own 2^x); a bias is one more. The reference is then the
 // largest raw score's logit plus the largest bias of a key the row sees: an upper
 // bound, at most kSpread above the row's largest logit. Weights then start as low
 // as 2^-80 instead of 1, which fp32 and bf16 hold as exactly; only weights under
@@ -164,7 +164,7 @@ __device__ __forceinline__ float tile_max(const uint32_t (&sv)[4][32]) {
 // out, masked, and their maximum taken.
 //
 // Capped 2048-row chunk at context 8192, head_dim 128: 379 us with 2^x and 1/x for
-// every score, 373 us with the cubic written out first, 292 us fused.
+// every score, 373 us with the cubic written out first, 292 us fused (271 us with two warpgroups).
 //
 // Products that a sum follows are rounded explicitly: the compiler must not fuse
 // them in one variant and not in another, or a row's last bits would depend on
@@ -178,7 +178,7 @@ struct TileScores {
   Cap cap;
   float sl2, slope;  // scale and bias per key in log2 units
   float r, p0, p1, p2, p3;
-  bool poly, flat;   // warp-uniform: the cap's r leaves the coefficients in range; a tile's biases stay within kSpread
+  bool poly, flat;   // warp-uniform: the cap's r leaves the coefficients in range; a tile's added biases stay within kSpread
   struct Tile {  // what top() found of a tile
     bool raw;    // warp-uniform
     float near;  // bias of its first key (0 without a bias)
@@ -216,46 +216,38 @@ struct TileScores {
       }
       if (!inside) mask_tile(sv, first, last);
       return fmaf(tile_max(sv), sl2, tile.near);
-    } else if constexpr (!kCap && !kBias) {
+    } else if constexpr (!kCap) {
       if (!inside) mask_tile(sv, first, last);
       return tile_max(sv) * sl2;
     } else {
       // rows that see keys past their own position take the distance's absolute value
       const bool ahead = kBias && __any_sync(kAll, min(last, kKeys - 1) > away);
       float mx = 0.f;
-      bool raw = (!kCap || (inside && poly)) && flat && !ahead;
+      bool raw = inside && poly && flat && !ahead;
       const float near = kBias ? __fmul_rn(-slope, static_cast<float>(away)) : 0.f;
       tile.near = near;
       if (raw) {
-        if (!kCap && !inside) mask_tile(sv, first, last);
         mx = tile_max(sv);
-        if constexpr (kCap) raw = __all_sync(kAll, fmaxf(mx, -tile_max<true>(sv)) * r <= 0.55f);
+        raw = __all_sync(kAll, fmaxf(mx, -tile_max<true>(sv)) * r <= 0.55f);
       }
       tile.raw = raw;
       if (raw) {
-        const float t = kCap ? cap(__fmul_rn(mx, sl2)) : __fmul_rn(mx, sl2);
-        const float b0 = fmaf(slope, static_cast<float>(max(first, 0)), near);
-        const float b1 = fmaf(slope, static_cast<float>(min(last, kKeys - 1)), near);
-        return kBias ? t + fmaxf(b0, b1) : t;
+        const float t = cap(__fmul_rn(mx, sl2));
+        return kBias ? t + fmaxf(near, fmaf(slope, kKeys - 1.f, near)) : t;
       }
       const float from = static_cast<float>(away);
       float b0 = 0.f, b1 = 0.f;
 #pragma unroll
       for (int i = 0; i < kKeys; i += 2) {
-        float x0 = score(sv, i), x1 = score(sv, i + 1);
-        if constexpr (kCap) {
-          x0 = cap(x0 * sl2);
-          x1 = cap(x1 * sl2);
-        }
+        float x0 = cap(score(sv, i) * sl2), x1 = cap(score(sv, i + 1) * sl2);
         if constexpr (kBias) {
-          const float unit = kCap ? 1.f : sl2;
           if (ahead) {
             b0 = -slope * fabsf(from - static_cast<float>(i));
             b1 = -slope * fabsf(from - static_cast<float>(i + 1));
           } else {
             bias(b0, b1, i, near);
           }
-          fma2(x0, x1, x0, x1, unit, unit, b0, b1);
+          add2(x0, x1, b0, b1);
         }
         sv[i >> 5][i & 31] = __float_as_uint(x0);
         sv[(i + 1) >> 5][(i + 1) & 31] = __float_as_uint(x1);
