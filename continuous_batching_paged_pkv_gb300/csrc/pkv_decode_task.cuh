@@ -157,9 +157,7 @@ struct TaskMod {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) x[nt][c][i] = cap(x[nt][c][i]);
+        for (int c = 0; c < 2; ++c) cap.both(x[nt][c][0], x[nt][c][1]);
     }
     if (bias) {
       const float away = static_cast<float>(pos0 - kbase) - static_cast<float>(ka);  // row 0 from key kbase + ka

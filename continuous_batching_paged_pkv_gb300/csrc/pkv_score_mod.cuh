@@ -37,6 +37,14 @@ struct Cap {
   __device__ __forceinline__ float operator()(float x) const {
     return fmaf(c2, rcp_approx(1.f + ex2_approx(__fmul_rn(x, k))), c);
   }
+  // Two scores, with the same results.
+  __device__ __forceinline__ void both(float &x0, float &x1) const {
+    float e0, e1;
+    mul2(e0, e1, x0, x1, k, k);
+    e0 = ex2_approx(e0), e1 = ex2_approx(e1);
+    add2(e0, e1, 1.f, 1.f);
+    fma2(x0, x1, rcp_approx(e0), rcp_approx(e1), c2, c2, c, c);
+  }
 };
 
 // Variants of the chunk kernels: plain, or modified scores with or without the
