@@ -54,6 +54,10 @@ def make_mod(kind, w, seed):
         return B.ScoreMod(key_end=end, alibi_slopes=_slopes(hq))
     if kind == "nothing":
         return B.ScoreMod(key_begin=ctx, key_end=np.zeros_like(pos))
+    if kind == "around":  # biases to both sides of a row, steep, flat and growing
+        return B.ScoreMod(alibi_slopes=_slopes(hq) * rng.choice([-0.05, 0.1, 1.0, 4.0], hq),
+                          key_begin=np.where(rng.random(len(pos)) < 0.5, 0, rng.integers(0, ctx)),
+                          key_end=np.where(rng.random(len(pos)) < 0.3, pos + 1, rng.integers(1, ctx + 3)))
     if kind == "everything":
         begin = rng.integers(-3, ctx + 3)
         begin[rng.random(len(pos)) < 0.5] = 0
@@ -120,7 +124,7 @@ SHAPES = {
     "mixed": [(40, 333), (1, 700), (1, 64), (17, 17), (2, 300)],
 }
 KINDS = ["none", "cap", "window1", "window5", "window100", "window400", "alibi", "documents", "prefix", "padding", "nothing",
-         "everything"]
+         "around", "everything"]
 HEADS = [(4, 2, 64), (32, 8, 128), (40, 8, 128), (8, 8, 64), (16, 1, 128), (6, 6, 128), (16, 1, 64)]
 
 
@@ -136,7 +140,7 @@ def test_shapes(case, kind):
 
 
 @pytest.mark.parametrize("kv", ["q8", "q4"])
-@pytest.mark.parametrize("kind", ["cap", "window100", "alibi", "documents", "padding", "nothing", "everything"])
+@pytest.mark.parametrize("kind", ["cap", "window100", "alibi", "documents", "padding", "nothing", "around", "everything"])
 def test_quantised_pools(kind, kv):
     for i, (hq, hkv, d) in enumerate([(32, 8, 128), (40, 8, 128), (16, 1, 128)] + ([(4, 2, 64), (8, 8, 64)] if kv == "q8" else [])):
         for case in ("decode", "runs", "mixed"):
