@@ -301,7 +301,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
     const bool stored = mrow < G * P && pos < rows;
     int lo = 0, hi = INT32_MAX;  // visible keys of this row; rows that are not stored mask nothing
     if (stored) row_sees(a, static_cast<int64_t>(row0) + pos0 + pos, p_row, L, lo, hi);
-    TileScores<MODE> ts(a, g * G + hh);
+    TileScores<MODE> ts(a, g * G + hh, stored);
     float m_used = -INFINITY;            // log2 units
     float l_sum = 0.f, l_odd = 0.f;      // row sum, as even and odd columns (packed adds)
     bool ok = true;

@@ -407,7 +407,7 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
     int lo = 0, hi = INT32_MAX;  // visible keys of this row (modified scores); rows that are not stored mask nothing
     const bool stored = mrow < G * P && pos < rows;
     if (MODE != kModNone && stored) row_sees(a, static_cast<int64_t>(row0) + pos0 + pos, p_row, L, lo, hi);
-    TileScores<MODE> ts(a, g * G + mrow % G);
+    TileScores<MODE> ts(a, g * G + mrow % G, stored);
     const uint32_t p_ready0 = cluster_addr(bar + kPReady, 0);
     float m_used = -INFINITY;  // log2 units
     bool ok = true;

@@ -164,7 +164,7 @@ __device__ __forceinline__ float tile_max(const uint32_t (&sv)[4][32]) {
 // to the least largest error of y P(y^2) (2^-21.5 in fp32 arithmetic), its
 // coefficients scaled so that a score costs 5 operations, the last of which also
 // subtracts the reference (2^x and 1/x would be two SFU operations of each score
-// beside the softmax's own 2^x); a bias is one more. The reference is then the
+// beside the softmax's own 2^x); a bias is one more. Only the segment's own rows decide. The reference is then the
 // largest raw score's logit plus the largest bias of a key the row sees: an upper
 // bound, at most kSpread above the row's largest logit. Weights then start as low
 // as 2^-80 instead of 1, which fp32 and bf16 hold as exactly; only weights under
@@ -186,14 +186,18 @@ struct TileScores {
   Cap cap;
   float sl2, slope;  // scale and bias per key in log2 units
   float r, p0, p1, p2, p3;
+  uint32_t rows;     // the warp's lanes with a row of the segment
   bool poly, flat;   // warp-uniform: the cap's r leaves the coefficients in range; a tile's added biases stay within kSpread
   struct Tile {  // what top() found of a tile
     bool raw;    // warp-uniform
     float near;  // bias of its first key (0 without a bias)
   };
 
-  __device__ __forceinline__ TileScores(const StepArgs &a, int head)
-      : cap(kCap ? a.softcap : 0.f), sl2(a.scale_log2), slope(0.f), r(0.f) {
+  // `stored`: the row is one of the segment's. The queries of the others are whatever follows in the
+  // packed axis, so their scores have no say in how the warp caps a tile.
+  __device__ __forceinline__ TileScores(const StepArgs &a, int head, bool stored)
+      : cap(kCap ? a.softcap : 0.f), sl2(a.scale_log2), slope(0.f), r(0.f),
+        rows(kCap ? __ballot_sync(0xffffffffu, stored) : 0u) {
     if constexpr (kBias || kRamp) slope = __ldg(a.alibi_slopes + head) * 1.4426950408889634f;
     flat = !kBias || __all_sync(0xffffffffu, fabsf(slope) * (kKeys - 1) <= kSpread);
     if constexpr (kCap) {
@@ -236,7 +240,7 @@ struct TileScores {
       tile.near = near;
       if (raw) {
         mx = tile_max(sv);
-        raw = __all_sync(kAll, fmaxf(mx, -tile_max<true>(sv)) * r <= 0.55f);
+        raw = (__ballot_sync(kAll, fmaxf(mx, -tile_max<true>(sv)) * r > 0.55f) & rows) == 0;
       }
       tile.raw = raw;
       if (raw) {
