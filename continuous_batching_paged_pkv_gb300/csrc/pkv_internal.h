@@ -39,7 +39,8 @@ struct StepArgs {
   // launch zeroes it on the stream first.
   uint32_t *task_counter;
   // The chunk kernel's K/V pool is written by the kernel right before it (the
-  // 8-bit and 4-bit paths' widening pass): wait for it before any K/V load.
+  // 8-bit and 4-bit paths' widening pass), and so is its block table: wait for
+  // it before reading either.
   // Otherwise only the tiles holding this step's rows wait for the cache write.
   int32_t kv_from_previous;
   // `out` is page-locked host memory reached through its device address: the

@@ -203,7 +203,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
       auto key_of = [&](int t0) { return base + tile_at(t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys; };
       auto group_ids = [&](int t0) -> int {
         const int key = key_of(t0);
-        return key >= base && key < kv_end ? __ldg(bt_row + key / a.block_size) : 0;
+        return key >= base && key < kv_end ? __ldcg(bt_row + key / a.block_size) : 0;
       };
       auto group_rows = [&](int t0, int blk) -> int {
         const int key = key_of(t0);
@@ -214,6 +214,13 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
         }
         return (blk * a.num_kv_heads + g) * a.block_size + key % a.block_size;
       };
+      // A scratch pool and its block table come whole from the kernel before, which may still be running:
+      // wait before the table is read, and read it through L2 (not as data that never changes).
+      bool waited = false;
+      if (a.kv_from_previous) {
+        grid_dependency_wait();
+        waited = true;
+      }
       int rows_cur = group_rows(0, group_ids(0)), ids_next = group_ids(4);
       if (lane == 0) {
         prefetch_tensormap(map);
@@ -222,7 +229,6 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
           tma_load_3d(sQ, &tmap_q, 0, g * G, row0 + pos0, bar + kQFull);
         }
       }
-      bool waited = false;
       int s = 0;
       uint32_t phase = 0;  // (j / stages) & 1
       for (int j = 0; j < ntiles; ++j) {
@@ -234,7 +240,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
         const int kt0 = base + tile_at(j) * kKeysPerTile;
         const int vs = min(kSubPerTile, (kv_end - kt0 + kSubKeys - 1) / kSubKeys);  // sub-tiles with a visible key
         const int row = __shfl_sync(kFull, rows_cur, (j & 3) * 8 + (lane & 7));
-        if (!waited && (a.kv_from_previous || kt0 + kKeysPerTile > L - n)) {
+        if (!waited && kt0 + kKeysPerTile > L - n) {
           grid_dependency_wait();
           waited = true;
         }

@@ -195,8 +195,8 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
   // grid starts (the kernel before it in the stream, the cache write, signals
   // dependents only after its own wait); only the keys this step appends come
   // from that kernel, and the producer waits for it before loading the first
-  // tile that holds them (before the first tile at all when the K/V source is
-  // a scratch pool the previous kernel fills).
+  // tile that holds them (before it reads the block table when the K/V source
+  // is a scratch pool that the previous kernel fills, its block table included).
   launch_dependents();
   const int4 it = reinterpret_cast<const int4 *>(items)[blockIdx.x >> 1];
   const int seg = it.x, slot = it.y, tile0 = it.z;
@@ -288,7 +288,7 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
     // group comes into use, so no block-table latency is ever waited on.
     auto group_ids = [&](int t0) -> int {
       const int key = base + tile_at(t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
-      return key >= base && key < kv_end ? __ldg(bt_row + key / a.block_size) : 0;
+      return key >= base && key < kv_end ? __ldcg(bt_row + key / a.block_size) : 0;
     };
     auto group_rows = [&](int t0, int blk) -> int {
       const int key = base + tile_at(t0 + (lane >> 3)) * kKeysPerTile + (lane & 7) * kSubKeys;
@@ -299,6 +299,13 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
       }
       return (blk * a.num_kv_heads + g) * a.block_size + key % a.block_size;
     };
+    // A scratch pool and its block table come whole from the kernel before, which may still be running:
+    // wait before the table is read, and read it through L2 (not as data that never changes).
+    bool waited = false;
+    if (a.kv_from_previous) {
+      grid_dependency_wait();
+      waited = true;
+    }
     int rows_cur = group_rows(0, group_ids(0)), ids_next = group_ids(4);
     const uint32_t q_full = cluster_addr(bar + kQFull, 0);
     if (lane == 0) {
@@ -315,7 +322,6 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
     const int u = is_k ? static_cast<int>(rank) * 4 + lane : lane - 8;
     const int dst_off = is_k ? lane * Lay::kKSub : Lay::kKBytes + (lane - 8) * kSubKeys * 128;
     const int bs_shift = 31 - __clz(a.block_size);  // block sizes are powers of two
-    bool waited = false;
     for (int j = 0; j < ntiles; ++j) {
       const int s = j % kStages;
       if (j >= kStages && !warp_wait_or_abort(bar + kKVEmpty + s, ((j - kStages) / kStages) & 1, abort_flag)) break;
@@ -329,9 +335,8 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
       // The pair loads 4 boxes per visible sub-tile: two K halves (one CTA) and two V halves (one each).
       if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar + kKVFull + s, vs * 4 * 2048);
       const int urow = __shfl_sync(kFull, rows_cur, (j & 3) * 8 + (u & 7));
-      // wait for the kernel before: at the first tile holding rows the cache write appends, or at once
-      // when that kernel wrote the whole K/V source
-      if (!waited && (a.kv_from_previous || kt0 + kKeysPerTile > L - n)) {
+      // wait for the kernel before at the first tile holding rows the cache write appends
+      if (!waited && kt0 + kKeysPerTile > L - n) {
         grid_dependency_wait();
         waited = true;
       }

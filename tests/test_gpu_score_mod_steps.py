@@ -52,3 +52,33 @@ def test_a_capped_chunk_does_not_depend_on_the_rows_behind_it(rows, biased, d):
         got, _ = _run(w, mod)
         differ = (got[:rows] != want).any((1, 2)).nonzero()[0]
         assert not len(differ), f"behind it {behind}: rows {differ} differ"
+
+
+@pytest.mark.parametrize("modified", [False, True])
+@pytest.mark.parametrize("kv,heads", [("q8", (32, 8, 128)), ("q4", (32, 8, 128)), ("q8", (8, 8, 64))])
+def test_a_widened_history_does_not_depend_on_what_the_workspace_held(heads, modified, kv):
+    """Prompt chunks over a block-scaled pool read a scratch pool through a scratch block table that the kernel before
+    fills: the same bits whatever an earlier call left there, called one behind another and replayed."""
+    hq, hkv, d = heads
+    w = W.random_step(43, [(40, 1500), (90, 600), (33, 2100), (200, 200), (1, 700)], num_q_heads=hq, num_kv_heads=hkv, head_dim=d)
+    mod = B.ScoreMod(window=900) if modified else None
+    want, ds = _run(w, mod, kv)
+    graph = torch.cuda.CUDAGraph()
+    fills = (0, 255, 1)
+    got = torch.empty((2 * len(fills),) + tuple(ds.out.shape), dtype=ds.out.dtype, device="cuda")
+
+    def calls(at):
+        for i, fill in enumerate(fills):
+            ds.workspace.fill_(fill)
+            R.run_attention(ds)
+            got[at + i].copy_(ds.out)
+
+    calls(0)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        calls(len(fills))
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert B.pkv_check_device_status(ds.status) == 0
+    assert all(np.array_equal(o.float().cpu().numpy(), want) for o in got)
