@@ -158,6 +158,10 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
   // wait); the rows written by that kernel itself (this step's K/V, the last
   // span of each row) are read only after waiting for it, in issue().
   bool waited = false;
+  auto wait_once = [&]() {
+    if (!waited) grid_dependency_wait();
+    waited = true;
+  };
 
   // A warp's tasks: t0, t0 + stride, t0 + 2 stride, then (with a task
   // counter) 3 stride + the counter's next value, else t0 + 3 stride, ...
@@ -185,10 +189,7 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
   const uint64_t policy = l2_evict_first_policy();
   auto issue = [&](const Task &T, int u) {
     // only the sub-tiles holding this step's rows wait for the cache write
-    if (!waited && T.reads_new && T.key0 + (u + 1) * kSubKeys > T.L - T.nrows) {
-      grid_dependency_wait();
-      waited = true;
-    }
+    if (T.reads_new && T.key0 + (u + 1) * kSubKeys > T.L - T.nrows) wait_once();
     const int row = __shfl_sync(kFull, T.row, u);
     if (lane == 0) {
       uint64_t *bar = full + pstage;
@@ -422,6 +423,9 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
 
     // ---- finish task A: the output row, or this span's partial ----
     if (A.ok) {
+      // Nothing is stored under the kernel before: it may be a call that writes the same output or
+      // uses the same workspace, and rows with modified scores need not see (and wait for) any new key.
+      wait_once();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -512,6 +516,8 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
     while (P - C < NST && issue_next()) {
     }
   }
+  // A grid ends after the kernel before it, whatever its tasks were: the next kernel waits for this grid only.
+  wait_once();
 }
 
 // Span merge. A row's result is fixed by its spans alone, whichever kernel

@@ -429,6 +429,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
   }
   __syncwarp();
   bool waited = false;  // rows written by the kernel before (this step's) are read after its wait
+  auto wait_once = [&]() {
+    if (!waited) grid_dependency_wait();
+    waited = true;
+  };
 
   // Tasks as in the bf16 decode kernel: three static rounds, then (with a
   // task counter) 3 stride + the counter's next value. A current, B
@@ -456,10 +460,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   const uint64_t policy = l2_evict_first_policy();
   auto issue = [&](const Task &T, int u) {
     // only the sub-tiles holding this step's rows wait for the cache write
-    if (!waited && T.reads_new && T.key0 + (u + 1) * kSubKeys > T.L - T.nrows) {
-      grid_dependency_wait();
-      waited = true;
-    }
+    if (T.reads_new && T.key0 + (u + 1) * kSubKeys > T.L - T.nrows) wait_once();
     const int row = __shfl_sync(kAll, T.row, u);
     if (lane == 0) {
       uint64_t *bar = full + pstage;
@@ -821,6 +822,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
 
     // ---- finish task A: the output row, or this span's partial ----
     if (A.ok) {
+      // Nothing is stored under the kernel before: it may be a call that writes the same output or
+      // uses the same workspace, and rows with modified scores need not see (and wait for) any new key.
+      wait_once();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -905,6 +909,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
     while (P - C < NST && issue_next()) {
     }
   }
+  // A grid ends after the kernel before it, whatever its tasks were: the next kernel waits for this grid only.
+  wait_once();
 }
 
 template <int D, int NT, bool MULTI, bool MOD, int NW, int BITS>

@@ -144,6 +144,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
   }
   if (bad) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
+    grid_dependency_wait();  // as below: this grid ends after the kernel before it
     return;
   }
   const int pos0 = tile * P;          // first query row of the tile within the segment
@@ -154,6 +155,7 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
   const int kv_begin = min(u[0], u[1]), kv_end = u[1];
   const int base = kv_begin & ~(kSubKeys - 1);
   const int ntiles = (kv_end - base + kKeysPerTile - 1) / kKeysPerTile;  // 0: no row of the tile sees a key
+  if (ntiles == 0) grid_dependency_wait();  // else the producers do, before a row is stored
   // With a bias the nearest keys come first (as in the head_dim 128 kernel), but the cached ones before this step's.
   constexpr bool kDown = (MODE & kModBias) != 0;
   const int old = kDown ? min(max(L - n - base, 0) / kKeysPerTile, ntiles) : 0;
@@ -240,7 +242,9 @@ __global__ void __maxnreg__(kLaunchRegs) prefill_mod_kernel(const __grid_constan
         const int kt0 = base + tile_at(j) * kKeysPerTile;
         const int vs = min(kSubPerTile, (kv_end - kt0 + kSubKeys - 1) / kSubKeys);  // sub-tiles with a visible key
         const int row = __shfl_sync(kFull, rows_cur, (j & 3) * 8 + (lane & 7));
-        if (!waited && kt0 + kKeysPerTile > L - n) {
+        // At the first tile with rows of this step, and with no such tile at the last one: the kernel before
+        // may write the same output, and the next kernel waits for this grid only.
+        if (!waited && (kt0 + kKeysPerTile > L - n || j == ntiles - 1)) {
           grid_dependency_wait();
           waited = true;
         }

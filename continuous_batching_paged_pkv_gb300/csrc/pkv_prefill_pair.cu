@@ -215,6 +215,7 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
   }
   if (bad) {
     if (threadIdx.x == 0 && rank == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
+    grid_dependency_wait();  // as below: this grid ends after the kernel before it
     return;
   }
   const int q_tiles = (n + P - 1) / P;
@@ -233,6 +234,7 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
   }
   const int base = kv_begin & ~(kSubKeys - 1);
   const int ntiles = (kv_end - base + kKeysPerTile - 1) / kKeysPerTile;  // 0: no row of the pair sees a key
+  if (MODE != kModNone && ntiles == 0) grid_dependency_wait();  // else the producer does, before a row is stored
   // Tile taken at step j. A distance bias makes the nearest keys' logits the
   // largest, so those variants go from the last tile to the first: going up, the
   // running max would grow by slope * 128 with every tile and O be rescaled at
@@ -335,8 +337,10 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
       // The pair loads 4 boxes per visible sub-tile: two K halves (one CTA) and two V halves (one each).
       if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar + kKVFull + s, vs * 4 * 2048);
       const int urow = __shfl_sync(kFull, rows_cur, (j & 3) * 8 + (u & 7));
-      // wait for the kernel before at the first tile holding rows the cache write appends
-      if (!waited && kt0 + kKeysPerTile > L - n) {
+      // wait for the kernel before at the first tile holding rows the cache write appends; with modified scores
+      // and no such tile at the last one (that kernel may write the same output, and the next kernel waits for
+      // this grid only)
+      if (!waited && (kt0 + kKeysPerTile > L - n || j == ntiles - 1)) {
         grid_dependency_wait();
         waited = true;
       }

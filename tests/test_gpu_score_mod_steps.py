@@ -82,3 +82,64 @@ def test_a_widened_history_does_not_depend_on_what_the_workspace_held(heads, mod
     torch.cuda.synchronize()
     assert B.pkv_check_device_status(ds.status) == 0
     assert all(np.array_equal(o.float().cpu().numpy(), want) for o in got)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "q8"])
+@pytest.mark.parametrize("heads", [(32, 8, 128), (8, 8, 64)])
+@pytest.mark.parametrize("shapes", [[(1, 2500), (1, 900), (1, 40)], [(2, 2500), (1, 130)], [(300, 2300), (40, 90)],
+                                    [(200, 1800), (1, 1200), (1, 60)]])
+def test_rows_that_see_no_new_key_keep_the_order_of_calls(shapes, heads, kv):
+    """Calls whose rows see only cached keys, or none, between calls and appends that write the same output and pool,
+    on one stream without a host wait: the same bits as with one."""
+    hq, hkv, d = heads
+    w = W.random_step(41, shapes, num_q_heads=hq, num_kv_heads=hkv, head_dim=d)
+    first = np.concatenate([np.full(s.q_len, s.ctx - s.q_len) for s in w.segments])
+    mods = [B.ScoreMod(window=700), B.ScoreMod(key_end=first // 3), B.ScoreMod(key_end=np.zeros_like(first)),
+            B.ScoreMod(key_end=first)]
+    steps = [R.prepare(w, kv=kv, mod=m) for m in mods]
+    base = steps[0]
+    room = torch.empty(max([1] + [int(max(s.info.workspace_bytes_q8, s.info.workspace_bytes)) for s in steps]),
+                       dtype=torch.uint8, device="cuda")
+    g = torch.Generator("cuda").manual_seed(2)
+    news = [tuple(torch.randn(base.k_new.shape, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+            for _ in range(2)]
+    for s in steps[1:]:
+        s.k_pool, s.v_pool, s.k_scales, s.v_scales, s.out, s.status = (base.k_pool, base.v_pool, base.k_scales,
+                                                                       base.v_scales, base.out, base.status)
+    for s in steps:
+        s.workspace = room
+
+    def run(s, new, wait):
+        if new is not None:
+            s.k_new, s.v_new = news[new]
+            R.run_cache_write(s)
+        if wait:
+            torch.cuda.synchronize()
+        R.run_attention(s)
+        if wait:
+            torch.cuda.synchronize()
+
+    # (step, which rows it appends first, whether its output is looked at)
+    chain = [(0, 0, False), (2, None, True), (1, None, False), (0, None, True), (1, 1, False), (0, 0, True), (0, None, False),
+             (1, None, True), (3, 1, False), (2, 0, False), (0, 1, True), (3, None, False), (2, None, True)]
+    rounds = 6
+
+    def outputs(wait, seen):
+        base.out.fill_(3.0)
+        for _ in range(rounds):
+            for i, new, keep in chain:
+                run(steps[i], new, wait)
+                if keep:
+                    seen.append(base.out.clone())
+        return seen
+
+    want, got, graph, replayed = outputs(True, []), outputs(False, []), torch.cuda.CUDAGraph(), []
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        outputs(False, replayed)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert (want[0] == 0).all() and B.pkv_check_device_status(base.status) == 0
+    for i, (a, b, c) in enumerate(zip(want, got, replayed)):
+        assert torch.equal(a, b) and torch.equal(a, c), f"output {i}"
