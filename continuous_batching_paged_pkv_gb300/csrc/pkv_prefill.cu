@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     L = a.context_lens[slot];
     bad = a.seq_slot[seg] != slot || n < 2 || n > L ||
           static_cast<int64_t>(L) > static_cast<int64_t>(a.max_blocks_per_slot) * a.block_size ||
-          tile * P >= n || row0 < 0 || static_cast<int64_t>(row0) + n > a.total_q;
+          static_cast<int64_t>(tile) * P >= n || row0 < 0 || static_cast<int64_t>(row0) + n > a.total_q;
   }
   if (bad) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);

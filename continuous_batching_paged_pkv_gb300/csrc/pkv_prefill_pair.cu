@@ -211,7 +211,7 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
     L = a.context_lens[slot];
     bad = a.seq_slot[seg] != slot || n < 2 || n > L ||
           static_cast<int64_t>(L) > static_cast<int64_t>(a.max_blocks_per_slot) * a.block_size ||
-          tile0 * P >= n || row0 < 0 || static_cast<int64_t>(row0) + n > a.total_q;
+          static_cast<int64_t>(tile0) * P >= n || row0 < 0 || static_cast<int64_t>(row0) + n > a.total_q;
   }
   if (bad) {
     if (threadIdx.x == 0 && rank == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);

@@ -143,3 +143,28 @@ def test_rows_that_see_no_new_key_keep_the_order_of_calls(shapes, heads, kv):
     assert (want[0] == 0).all() and B.pkv_check_device_status(base.status) == 0
     for i, (a, b, c) in enumerate(zip(want, got, replayed)):
         assert torch.equal(a, b) and torch.equal(a, c), f"output {i}"
+
+
+@pytest.mark.parametrize("kv,d", [("bf16", 64), ("bf16", 128), ("q8", 64), ("q8", 128)])
+@pytest.mark.parametrize("modified", [False, True])
+def test_chunk_items_outside_the_segment_are_reported_not_followed(modified, kv, d):
+    """Query tiles past the segment's rows, also those whose first row leaves 32 bits, and wrong segments and slots."""
+    w = W.random_step(5, [(150, 400), (40, 90)], num_q_heads=8, num_kv_heads=2, head_dim=d)
+    mod = B.ScoreMod(window=90, key_begin=np.zeros(190, np.int64), alibi_slopes=_slopes(8)) if modified else None
+    want, ds = _run(w, mod, kv)
+    good = ds.work.clone()
+    at = 4 * ds.info.num_decode_items
+    tiles = 32  # rows of a tile: 128 / group
+    assert good[at] == 0 and good[at + 2] % 2 == 0
+    for word, value in ((2, 5), (2, 6), (2, 2 ** 31 - 1), (2, 2 ** 31 // tiles), (2, 2 ** 32 // tiles), (2, 2 ** 32 // tiles + 2),
+                        (2, 3 * 2 ** 31 // tiles), (2, -2), (0, 2), (0, -1), (0, 1), (1, 1), (1, 2 ** 31 - 1), (1, -1)):
+        bad = good.clone()
+        bad[at + word] = value
+        ds.work.copy_(bad)
+        R.run_attention(ds)
+        assert B.pkv_check_device_status(ds.status) & 4, (word, value)
+    ds.work.copy_(good)
+    ds.out.zero_()
+    R.run_attention(ds)
+    assert B.pkv_check_device_status(ds.status) == 0
+    assert np.array_equal(R.out_f32(ds), want)
