@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(256) cache_write_quant_kernel(
 // Item (segment, slot, first scratch block, blocks); with modified scores (MOD)
 // word 1 is the first logical block that some row of the segment sees. CTA (item, y) widens the
 // item's blocks y, y + gridDim.y, ... : block j of the item becomes scratch
-// block first + j, and the scratch table row of the slot points there.
+// block first + j, and the scratch table row of the slot points there (with
+// modified scores its entries of the other blocks are -1).
 template <int D, int BITS, bool MOD>
 __global__ void __launch_bounds__(256) widen_quant_kernel(const StepArgs a, const int32_t *__restrict__ items,
                                                        const int8_t *__restrict__ k_codes,
@@ -166,9 +167,10 @@ __global__ void __launch_bounds__(256) widen_quant_kernel(const StepArgs a, cons
             static_cast<int64_t>(blk0) + nblk <= a.max_blocks_per_slot;
   const int slot = !ok ? -1 : MOD ? __ldg(a.seq_slot + seg) : it.y;
   ok = ok && slot >= 0 && slot < a.max_slots;
+  int have = 0;  // blocks of the slot's history
   if (ok) {
     const int L = __ldg(a.context_lens + slot);
-    const int have = (L + a.block_size - 1) / a.block_size;
+    have = (L + a.block_size - 1) / a.block_size;
     ok = MOD ? blk0 + nblk <= have : __ldg(a.seq_slot + seg) == slot && have == nblk;
   }
   grid_dependency_wait();  // the codes come from the cache write before this kernel
@@ -180,11 +182,16 @@ __global__ void __launch_bounds__(256) widen_quant_kernel(const StepArgs a, cons
   constexpr int NG = D / 32;
   const int64_t rows = static_cast<int64_t>(a.num_kv_heads) * a.block_size;  // rows of one block
   const int64_t vecs = rows * (D / 8);                                      // 8 values per vector
+  int32_t *table = scratch_table + static_cast<int64_t>(slot) * a.max_blocks_per_slot;
+  if constexpr (MOD) {  // the blocks that the list leaves out: rows that see them all the same report it
+    for (int j = blockIdx.y * blockDim.x + threadIdx.x; j < have; j += gridDim.y * blockDim.x)
+      if (j < blk0 || j >= blk0 + nblk) table[j] = -1;
+  }
   for (int j = blockIdx.y; j < nblk; j += gridDim.y) {
     const int bid = __ldg(a.block_tables + static_cast<int64_t>(slot) * a.max_blocks_per_slot + blk0 + j);
     const bool in_pool = bid >= 0 && bid < a.num_blocks;
     if (!in_pool && threadIdx.x == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_BLOCK);
-    if (threadIdx.x == 0) scratch_table[static_cast<int64_t>(slot) * a.max_blocks_per_slot + blk0 + j] = first + j;
+    if (threadIdx.x == 0) table[blk0 + j] = first + j;
     const int64_t src_row0 = static_cast<int64_t>(in_pool ? bid : 0) * rows;
     const int64_t dst_row0 = static_cast<int64_t>(first + j) * rows;
     for (int64_t i = threadIdx.x; i < 2 * vecs; i += blockDim.x) {

@@ -646,7 +646,8 @@ pkv_status pkv_plan_work_mod(const int32_t *cu_seqlens_q, int32_t num_seqs, cons
  * values that pkv_plan_work_mod saw; like q, they are read before the wait for
  * the previous kernel) and a work list and info from pkv_plan_work_mod. Items
  * that do not fit the step are skipped and set PKV_DEV_BAD_SEGMENT; bounds that
- * reach past the keys the list covers set it where a segment has a single span.
+ * reach past the keys the list covers set it where a segment has a single span,
+ * and PKV_DEV_BAD_BLOCK where a chunk's history would have to be widened further.
  */
 pkv_status pkv_attention_mod(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
                              const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,

@@ -168,3 +168,27 @@ def test_chunk_items_outside_the_segment_are_reported_not_followed(modified, kv,
     R.run_attention(ds)
     assert B.pkv_check_device_status(ds.status) == 0
     assert np.array_equal(R.out_f32(ds), want)
+
+
+@pytest.mark.parametrize("kv,d", [("q8", 64), ("q8", 128), ("q4", 128)])
+def test_chunk_bounds_wider_than_the_widened_history_are_reported(kv, d):
+    """Also where an earlier call has left block IDs of the scratch pool in the workspace's block table."""
+    w = W.random_step(6, [(60, 900), (33, 700)], num_q_heads=8, num_kv_heads=2, head_dim=d)
+    _, whole = _run(w, B.ScoreMod(), kv)
+    want, ds = _run(w, B.ScoreMod(key_begin=np.full(93, 640)), kv)
+    narrow = ds.mod.key_begin.clone()
+    for at, begin in ((slice(0, 60), 100), (slice(0, 1), 0), (slice(60, 93), 500)):
+        for fill in (0, None):
+            whole.workspace.fill_(0)
+            if fill is None:
+                R.run_attention(whole)
+            ds.workspace = whole.workspace
+            ds.mod.key_begin.copy_(narrow)
+            ds.mod.key_begin[at] = begin
+            R.run_attention(ds)
+            assert B.pkv_check_device_status(ds.status) & 2, (at, begin, fill)
+            assert B.pkv_check_device_status(whole.status) == 0
+    ds.mod.key_begin.copy_(narrow)
+    R.run_attention(ds)
+    assert B.pkv_check_device_status(ds.status) == 0
+    assert np.array_equal(R.out_f32(ds), want)
