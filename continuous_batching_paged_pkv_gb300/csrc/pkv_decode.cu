@@ -46,7 +46,7 @@
 // deterministic and independent of the rest of the batch.
 //
 // With modified scores (MOD) a work item names the 16-key sub-tiles of its span
-// that some row of the segment sees; each column masks the keys outside its own
+// from the first to the last that some row of the segment sees; each column masks the keys outside its own
 // row's interval, and the logits take the cap and the distance bias before the
 // softmax. A few more instructions per 16-key sub-tile; the kernel stays bound by
 // HBM.
@@ -305,7 +305,7 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
       const int kbase = A.key0 + u * kSubKeys;
       // keys of the sub-tile that take part (0 for a block ID outside the pool)
       int v = row >= 0 ? min(kSubKeys, A.key1 - kbase) : 0, v0 = 0;
-      if constexpr (MOD) {  // [v0, v): the keys that some row sees
+      if constexpr (MOD) {  // [v0, v): the keys from the first to the last that some row sees
         v0 = max(0, tm.u_lo - kbase);
         v = min(v, tm.u_hi - kbase);
       }

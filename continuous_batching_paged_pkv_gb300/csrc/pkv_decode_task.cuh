@@ -112,7 +112,7 @@ struct TaskMod {
   int lo[N][C], hi[N][C];  // visible keys [lo, hi) of the column
   float row[N][C];         // index of the column's row within the segment
   float slope[NT][2];      // distance bias per key, log2 units
-  int u_lo, u_hi;          // keys that some row of the segment sees
+  int u_lo, u_hi;          // from the first to past the last key that some row of the segment sees
   int a_lo, a_hi;          // keys that every row of the segment sees
   int pos0;                // position of the segment's first row
 

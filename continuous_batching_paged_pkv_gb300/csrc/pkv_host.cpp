@@ -349,7 +349,7 @@ struct KeyRange {
   int64_t lo, hi;  // keys [lo, hi); lo >= hi: none
 };
 
-// The keys that some of rows [i0, i1) of a segment sees (packed rows row0 + i,
+// The keys from the first to the last that some of rows [i0, i1) of a segment sees (packed rows row0 + i,
 // position first + i, context L): pkv_score_mod's bounds, on the host.
 KeyRange rows_see(const pkv_score_mod *mod, int64_t row0, int64_t first, int64_t L, int64_t i0, int64_t i1) {
   KeyRange u{INT64_MAX, 0};

@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       const int row = __shfl_sync(kAll, A.row, u);
       const int kbase = A.key0 + u * kSubKeys;
       int v = row >= 0 ? min(kSubKeys, A.key1 - kbase) : 0, v0 = 0;
-      if constexpr (MOD) {  // [v0, v): the keys that some row sees
+      if constexpr (MOD) {  // [v0, v): the keys from the first to the last that some row sees
         v0 = max(0, tm.u_lo - kbase);
         v = min(v, tm.u_hi - kbase);
       }

@@ -603,12 +603,16 @@ pkv_status pkv_attention_q4(const void *q, const int32_t *cu_seqlens_q, int32_t 
  * window: a sliding window of `window` keys, the row's own among them (local
  * layers). key_begin: documents packed behind one another in one slot (each
  * row's document's first position). key_end: a bidirectional prefix (the
- * larger of p + 1 and the prefix's length), or 0 for padding rows. Keys that no
- * row of a segment sees are not read, at the granularity of 16 keys: their
- * blocks may have been given back, and their table entries may be anything. A
- * key or value that is not finite reaches the rows that see it, and through
- * 0 * infinity may reach other rows of the same segment; one that no row of
- * the segment's tile sees reaches none.
+ * larger of p + 1 and the prefix's length), or 0 for padding rows. Keys before
+ * the first and behind the last one that some row of a segment sees are not
+ * read, at the granularity of 16 keys: their blocks may have been given back,
+ * and their table entries may be anything. Keys in between are read also where
+ * the rows' intervals leave a gap that none of them sees: their table entries
+ * must name blocks of the pool (PKV_DEV_BAD_BLOCK otherwise) and their values
+ * must be finite. A key or value that is not finite reaches the rows that see
+ * it, and a value through 0 * infinity may reach other rows of the same
+ * segment; one before the first or behind the last key that some row of a tile
+ * (at head_dim 128 a pair of tiles) sees reaches none of its rows.
  * ---------------------------------------------------------------------- */
 typedef struct pkv_score_mod {
     float softcap;             /* 0: none; else 2^-20 .. 2^12 (the capped score is within softcap * 2^-21) */
@@ -622,8 +626,8 @@ typedef struct pkv_score_mod {
  * pkv_plan_work for a step whose rows see only the keys that `mod` leaves them
  * (key_begin and key_end are HOST copies here; softcap and alibi_slopes are
  * not looked at). The key spans of the decode path and the tiles of the chunk
- * path cover the keys that some row of the segment (of the tile pair) sees,
- * and nothing else. Spans are cut at multiples of PKV_SPLIT_KEYS, or of 64 or
+ * path cover the keys from the first to the last that some row of the segment
+ * (of the tile pair) sees, and nothing else. Spans are cut at multiples of PKV_SPLIT_KEYS, or of 64 or
  * 128 keys where the slots are so few that every span of a full step has a warp
  * of its own; the cut depends on the keys that the segment sees, max_slots and
  * num_kv_heads, not on the other segments of the step. Same

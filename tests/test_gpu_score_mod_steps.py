@@ -8,6 +8,7 @@ from continuous_batching_paged_pkv_gb300 import binding as B
 from continuous_batching_paged_pkv_gb300 import build as libbuild
 from continuous_batching_paged_pkv_gb300 import runtime as R
 from continuous_batching_paged_pkv_gb300 import workloads as W
+from tests import test_gpu_score_mod as score_mod
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -192,3 +193,34 @@ def test_chunk_bounds_wider_than_the_widened_history_are_reported(kv, d):
     R.run_attention(ds)
     assert B.pkv_check_device_status(ds.status) == 0
     assert np.array_equal(R.out_f32(ds), want)
+
+
+@pytest.mark.parametrize("kv,d", [("bf16", 64), ("bf16", 128), ("q8", 64), ("q4", 128)])
+def test_rows_with_a_gap_between_their_keys(kv, d):
+    """A run and a chunk whose rows' intervals leave a gap: right results, whatever finite values lie in the gap, and
+    with NaN and blocks outside the pool before the first and behind the last key that a row sees."""
+    w = W.random_step(7, [(2, 1500), (60, 2500)], num_q_heads=8, num_kv_heads=2, head_dim=d)
+    low = np.arange(60) < 30
+    mod = B.ScoreMod(key_begin=np.concatenate([[33, 1000], np.where(low, 100, 2000)]),
+                     key_end=np.concatenate([[100, 1100], np.where(low, 150, 2050)]))
+    want, ds = _run(w, mod, kv)
+    score_mod.check(want, w, kv, mod, "a gap")
+    tables, arrays = ds.block_tables, [t for t in (ds.k_pool, ds.v_pool, ds.k_scales, ds.v_scales) if t is not None]
+    for slot, first, gap, last in ((0, 33, (100, 1000), 1100), (1, 100, (150, 2000), 2050)):
+        inside = tables[slot, -(-gap[0] // 16):gap[1] // 16].long()
+        for t in arrays:
+            t[inside] = 7 if t.dtype != torch.bfloat16 else 1e30 if kv == "bf16" else 0.25
+        dead = [*range(0, first // 16), *range(-(-last // 16), tables.shape[1])]
+        for t in (arrays if kv == "bf16" else arrays[2:]):
+            t[tables[slot, first // 16].long(), :, :first % 16] = float("nan")
+            if last % 16:
+                t[tables[slot, last // 16].long(), :, last % 16:] = float("nan")
+        tables[slot, dead] = torch.tensor([-1, 1 << 30] * len(dead), dtype=torch.int32, device="cuda")[:len(dead)]
+    ds.out.fill_(float("nan"))
+    R.run_attention(ds)
+    assert B.pkv_check_device_status(ds.status) == 0
+    got = R.out_f32(ds)
+    score_mod.check(got, w, kv, mod, "other keys in the gap")
+    # (decode over codes scales its weights by the largest value scale that it has loaded)
+    rows = slice(None) if kv == "bf16" else slice(2, None)
+    assert np.array_equal(got[rows], want[rows])

@@ -214,3 +214,20 @@ def test_oracle_closed_forms():
     # a prefix is seen from before its end
     lo, hi = SM.bounds([2, 9], 12, key_end=[6, 10], key_begin=[-4, 8])
     assert lo.tolist() == [0, 8] and hi.tolist() == [6, 10]
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+def test_a_gap_between_rows_is_covered(head_dim):
+    """Rows whose intervals leave a gap: spans and widened blocks run from the first to the last key that one sees."""
+    shape = dict(max_slots=2, max_blocks_per_slot=200, block_size=16, num_q_heads=8, num_kv_heads=2, head_dim=head_dim)
+    begin = np.concatenate([[33, 1000], np.where(np.arange(60) < 30, 100, 2000)])
+    end = np.concatenate([[100, 1100], np.where(np.arange(60) < 30, 150, 2050)])
+    work, info = B.pkv_plan_work_mod([0, 2, 62], [0, 1], [1500, 2500], key_begin=begin, key_end=end, **shape)
+    items = work[:info.work_words].reshape(-1, 4)
+    words = items[:info.num_decode_items, 2].astype(np.int64) & 0xFFFFFFFF
+    k0 = (words & 0x7FFFFF) * 256 + ((words >> 23) & 15) * 16
+    keys = sorted(zip(k0.tolist(), (k0 + (words >> 27) * 16).tolist()))
+    assert keys[0][0] == 32 and keys[-1][1] == 1104
+    assert all(a[1] == b[0] for a, b in zip(keys, keys[1:]))
+    (scratch,) = items[len(items) - info.num_scratch_items:]
+    assert scratch[1] == 100 // 16 and scratch[1] + scratch[3] == -(-2050 // 16)
