@@ -447,7 +447,7 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
               const int i = MULTI ? col / G : 0, hh = MULTI ? col % G : col;
               __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) +
                                    ((static_cast<size_t>(A.row0) + i) * a.num_q_heads + hbase) * D + (lane >> 2);
-              const float inv = MOD && l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];  // a row that sees nothing gives zeros
+              const float inv = MOD && tm.nothing(nt, c) ? 0.f : 1.f / l[nt][c];  // a row that sees nothing gives zeros
 #pragma unroll
               for (int mt = 0; mt < KT; ++mt) {
                 out[static_cast<size_t>(hh) * D + mt * 16] = __float2bfloat16_rn(acc[nt][mt][c] * inv);
@@ -538,7 +538,7 @@ constexpr int kPiece = 64;  // spans staged in shared memory at a time (a multip
 
 struct MergeRow {
   int row, spans, pbase, nrows;
-  bool bad;
+  bool bad, none;  // none: the row sees no key (modified scores)
 };
 
 // Decode a merge item and check it against the step metadata.
@@ -553,6 +553,7 @@ __device__ __forceinline__ MergeRow merge_row(const StepArgs &a, const int32_t *
   const int ri = (it.z >> 16) & 0xFF;
   r.nrows = ((it.z >> 24) & 0xFF) + 1;
   r.row = 0;
+  r.none = false;
   r.bad = seg < 0 || seg >= a.num_seqs || slot < 0 || slot >= a.max_slots || r.spans < 2 || r.pbase < 0 ||
           ri >= r.nrows;
   if (!r.bad) {
@@ -563,10 +564,15 @@ __device__ __forceinline__ MergeRow merge_row(const StepArgs &a, const int32_t *
             row0 < 0 || row0 + r.nrows > a.total_q ||
             r.nrows > L;
     // modified scores: spans of 64 keys or more over part of the history, partials inside the workspace
-    if (a.modified)
+    if (a.modified) {
       r.bad |= L / 64 + 2 < r.spans ||
                r.pbase + static_cast<int64_t>(r.spans - 1) * r.nrows >= static_cast<int64_t>(a.num_partials);
-    else
+      if (!r.bad) {
+        int lo, hi;
+        row_sees(a, r.row, L - r.nrows + ri, L, lo, hi);
+        r.none = lo >= hi;
+      }
+    } else
       r.bad |= (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS != r.spans;
   }
   return r;
@@ -591,13 +597,14 @@ __device__ __forceinline__ void add_group(float &lt, float4 &at, float lg, const
 }
 
 template <int D>
-__device__ __forceinline__ void store_merged(const StepArgs &a, int row, int h, int col, float lt, const float4 &at) {
-  const float inv = lt == 0.f ? 0.f : 1.f / lt;  // 0 only where modified scores leave a row no key
+__device__ __forceinline__ void store_merged(const StepArgs &a, const MergeRow &r, int h, int col, float lt,
+                                             const float4 &at) {
+  const float inv = r.none ? 0.f : 1.f / lt;  // a row that sees nothing gives zeros
   uint2 packed;
   packed.x = pack_bf16x2(__fmul_rn(at.x, inv), __fmul_rn(at.y, inv));
   packed.y = pack_bf16x2(__fmul_rn(at.z, inv), __fmul_rn(at.w, inv));
   *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) +
-                             (static_cast<size_t>(row) * a.num_q_heads + h) * D + 4 * col) = packed;
+                             (static_cast<size_t>(r.row) * a.num_q_heads + h) * D + 4 * col) = packed;
 }
 
 // Four lanes per float4 column: lane w of a column folds groups w, w + 4,
@@ -683,7 +690,7 @@ __device__ __forceinline__ void merge_small_body(const StepArgs &a, const int32_
       if (rd * 4 + j < groups) add_group(lt, at, lj, aj);
     }
   }
-  if (w == 0) store_merged<D>(a, r.row, h, col, lt, at);
+  if (w == 0) store_merged<D>(a, r, h, col, lt, at);
 }
 
 // One-dimensional grids, item-major: every head group of the first (longest)
@@ -763,7 +770,7 @@ __device__ __forceinline__ void merge_wide_body(const StepArgs &a, const int32_t
       add_group(lt, at, lg, ag);
     }
   }
-  if (live) store_merged<D>(a, r.row, h, col, lt, at);
+  if (live) store_merged<D>(a, r, h, col, lt, at);
 }
 
 template <int D>

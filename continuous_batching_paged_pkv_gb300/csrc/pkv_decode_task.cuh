@@ -149,6 +149,9 @@ struct TaskMod {
       }
   }
 
+  // Whether the row of column (nt, c) sees no key.
+  __device__ __forceinline__ bool nothing(int nt, int c) const { return hi[MULTI ? nt : 0][MULTI ? c : 0] == 0; }
+
   // A sub-tile's scores (log2 units) of keys kbase + ka and kbase + ka + 8
   // become logits; keys past the loaded ones (`v` of them) or outside the
   // column's interval become -inf. Most sub-tiles lie inside every row's interval.

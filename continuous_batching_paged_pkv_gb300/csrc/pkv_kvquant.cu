@@ -864,8 +864,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
             if (A.pbase < 0) {
               __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) +
                                    ((static_cast<size_t>(A.row0) + i) * a.num_q_heads + hbase + hh) * D + 4 * r;
-              // l also carries the 2^7; it is 0 for a row that sees nothing, which gives zeros
-              const float inv = MOD && l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];
+              // l also carries the 2^7; a row that sees nothing gives zeros
+              const float inv = MOD && tm.nothing(nt, c) ? 0.f : 1.f / l[nt][c];
 #pragma unroll
               for (int g = 0; g < NG; ++g) {
                 uint2 pk;

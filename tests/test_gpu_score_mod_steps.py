@@ -224,3 +224,28 @@ def test_rows_with_a_gap_between_their_keys(kv, d):
     # (decode over codes scales its weights by the largest value scale that it has loaded)
     rows = slice(None) if kv == "bf16" else slice(2, None)
     assert np.array_equal(got[rows], want[rows])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shapes", [[(1, 60), (1, 900)], [(2, 50), (2, 1300)], [(150, 700)]])
+def test_a_row_whose_logits_are_all_minus_infinity(shapes, d):
+    """0 / 0 by the definition, in every path alike; zeros are for rows that see no key."""
+    w = W.random_step(9, shapes, num_q_heads=8, num_kv_heads=2, head_dim=d)
+    q = W.bf16_bits_to_f32(w.q).copy()
+    q[..., 0] = 1.0
+    w.q = W.f32_to_bf16_bits(q)
+    pos = np.concatenate([np.arange(s.ctx - s.q_len, s.ctx) for s in w.segments])
+    end = np.where(pos % 2 == 0, 0, pos + 1)
+    for mod in (None, B.ScoreMod(), B.ScoreMod(window=40), B.ScoreMod(alibi_slopes=_slopes(8)), B.ScoreMod(key_end=end),
+                B.ScoreMod(key_end=end, softcap=5.0)):
+        _, ds = _run(w, mod)
+        ds.k_pool[:, 0, :, 0] = float("-inf")
+        R.run_attention(ds)
+        got = R.out_f32(ds)
+        assert B.pkv_check_device_status(ds.status) == 0
+        blind = mod is not None and mod.key_end is not None and end == 0
+        if mod is None or not mod.softcap:
+            assert np.array_equal(np.isnan(got[:, :4]), np.broadcast_to(~np.atleast_1d(blind)[:, None, None], got[:, :4].shape)), mod
+        else:
+            assert np.isfinite(got).all()
+        assert np.isfinite(got[:, 4:]).all() and (got[np.broadcast_to(blind, len(pos))] == 0).all(), mod
