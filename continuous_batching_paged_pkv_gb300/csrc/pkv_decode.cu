@@ -542,6 +542,7 @@ struct MergeRow {
 };
 
 // Decode a merge item and check it against the step metadata.
+template <bool MOD>
 __device__ __forceinline__ MergeRow merge_row(const StepArgs &a, const int32_t *items, int item) {
   const int4 it = __ldg(reinterpret_cast<const int4 *>(items) + item);
   // word 2: spans | row index << 16 | (rows - 1) << 24; word 3: the partial
@@ -564,7 +565,7 @@ __device__ __forceinline__ MergeRow merge_row(const StepArgs &a, const int32_t *
             row0 < 0 || row0 + r.nrows > a.total_q ||
             r.nrows > L;
     // modified scores: spans of 64 keys or more over part of the history, partials inside the workspace
-    if (a.modified) {
+    if constexpr (MOD) {
       r.bad |= L / 64 + 2 < r.spans ||
                r.pbase + static_cast<int64_t>(r.spans - 1) * r.nrows >= static_cast<int64_t>(a.num_partials);
       if (!r.bad) {
@@ -572,8 +573,9 @@ __device__ __forceinline__ MergeRow merge_row(const StepArgs &a, const int32_t *
         row_sees(a, r.row, L - r.nrows + ri, L, lo, hi);
         r.none = lo >= hi;
       }
-    } else
+    } else {
       r.bad |= (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS != r.spans;
+    }
   }
   return r;
 }
@@ -610,7 +612,7 @@ __device__ __forceinline__ void store_merged(const StepArgs &a, const MergeRow &
 // Four lanes per float4 column: lane w of a column folds groups w, w + 4,
 // ...; the column's maximum and its ordered group sums go across the four
 // lanes by shuffles. 128 threads hold D / 4 columns x 4 lanes of 128 / D q heads.
-template <int D>
+template <int D, bool MOD>
 __device__ __forceinline__ void merge_small_body(const StepArgs &a, const int32_t *__restrict__ items, int item,
                                                  int head_group) {
   constexpr int F = D / 4;             // float4 columns per q head
@@ -621,7 +623,7 @@ __device__ __forceinline__ void merge_small_body(const StepArgs &a, const int32_
   // The work item and step metadata are final when this grid starts (the
   // decode kernel starts only after everything before the cache write has
   // finished); only the partials need the decode grid to finish (the wait below).
-  const MergeRow r = merge_row(a, items, item);
+  const MergeRow r = merge_row<MOD>(a, items, item);
   grid_dependency_wait();  // partials come from the decode kernel
   if (r.bad) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
@@ -695,17 +697,17 @@ __device__ __forceinline__ void merge_small_body(const StepArgs &a, const int32_
 
 // One-dimensional grids, item-major: every head group of the first (longest)
 // rows is issued before any CTA of a later row.
-template <int D>
+template <int D, bool MOD>
 __global__ void __launch_bounds__(kMergeThreads) merge_small_kernel(const StepArgs a,
                                                                     const int32_t *__restrict__ items, int groups) {
-  merge_small_body<D>(a, items, static_cast<int>(blockIdx.x) / groups, static_cast<int>(blockIdx.x) % groups);
+  merge_small_body<D, MOD>(a, items, static_cast<int>(blockIdx.x) / groups, static_cast<int>(blockIdx.x) % groups);
 }
 
 // One thread per float4 column; 128 threads hold 128 / (D / 4) q heads. The
 // CTA stages its heads' (max, denominator) pairs kPiece spans at a time in
 // shared memory; each thread reads the maxima from there, then folds its
 // groups in order, each group's eight sums loaded at once.
-template <int D>
+template <int D, bool MOD>
 __device__ __forceinline__ void merge_wide_body(const StepArgs &a, const int32_t *__restrict__ items, int item,
                                                 int head_group) {
   constexpr int F = D / 4;                // float4 columns per q head
@@ -713,7 +715,7 @@ __device__ __forceinline__ void merge_wide_body(const StepArgs &a, const int32_t
   __shared__ float s_m[HPC][kPiece], s_l[HPC][kPiece];
   const int hl = static_cast<int>(threadIdx.x) / F, col = threadIdx.x % F;
   const int h0 = head_group * HPC, h = h0 + hl;
-  const MergeRow r = merge_row(a, items, item);
+  const MergeRow r = merge_row<MOD>(a, items, item);
   grid_dependency_wait();  // partials come from the decode kernel
   if (r.bad) {  // uniform over the CTA
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
@@ -773,24 +775,24 @@ __device__ __forceinline__ void merge_wide_body(const StepArgs &a, const int32_t
   if (live) store_merged<D>(a, r, h, col, lt, at);
 }
 
-template <int D>
+template <int D, bool MOD>
 __global__ void __launch_bounds__(kMergeThreads) merge_wide_kernel(const StepArgs a,
                                                                    const int32_t *__restrict__ items, int groups) {
-  merge_wide_body<D>(a, items, static_cast<int>(blockIdx.x) / groups, static_cast<int>(blockIdx.x) % groups);
+  merge_wide_body<D, MOD>(a, items, static_cast<int>(blockIdx.x) / groups, static_cast<int>(blockIdx.x) % groups);
 }
 
 // Both layouts in one grid: the first `num_long` items (rows of more than two
 // span groups, first in the list) take four lanes per column, the rest one;
 // the grid's first long_ctas CTAs are the long items' (item, head group)s.
-template <int D>
+template <int D, bool MOD>
 __global__ void __launch_bounds__(kMergeThreads) merge_mixed_kernel(const StepArgs a,
                                                                     const int32_t *__restrict__ items,
                                                                     int num_long, int long_groups, int wide_groups) {
   const int b = static_cast<int>(blockIdx.x), long_ctas = num_long * long_groups;
   if (b < long_ctas)
-    merge_small_body<D>(a, items, b / long_groups, b % long_groups);
+    merge_small_body<D, MOD>(a, items, b / long_groups, b % long_groups);
   else
-    merge_wide_body<D>(a, items, num_long + (b - long_ctas) / wide_groups, (b - long_ctas) % wide_groups);
+    merge_wide_body<D, MOD>(a, items, num_long + (b - long_ctas) / wide_groups, (b - long_ctas) % wide_groups);
 }
 
 int sm_count() {
@@ -877,10 +879,10 @@ cudaError_t launch_decode(const StepArgs &a, const CUtensorMap &tk, const CUtens
                     : launch_decode_m<false>(a, tk, tv, num_items, items, beside_chunk, stream);
 }
 
-cudaError_t launch_merge(const StepArgs &a, int32_t num_items, int32_t num_long, const int32_t *items,
+template <int D, bool MOD>
+static cudaError_t launch_merge_t(const StepArgs &a, int32_t num_items, int32_t num_long, const int32_t *items,
                          cudaStream_t stream) {
-  if (num_items <= 0) return cudaSuccess;
-  const int f = a.head_dim / 4;  // float4 columns per q head
+  constexpr int f = D / 4;  // float4 columns per q head
   const dim3 block(kMergeThreads);
   const int small_groups = (a.num_q_heads * 4 * f + kMergeThreads - 1) / kMergeThreads;
   const int wide_groups = (a.num_q_heads * f + kMergeThreads - 1) / kMergeThreads;
@@ -891,20 +893,26 @@ cudaError_t launch_merge(const StepArgs &a, int32_t num_items, int32_t num_long,
   const int64_t small_ctas = static_cast<int64_t>(num_items) * small_groups;
   if (small_ctas <= 6ll * sm_count()) {
     const dim3 grid(static_cast<unsigned>(small_ctas));
-    if (a.head_dim == 128) return launch_pdl(merge_small_kernel<128>, grid, block, 0, stream, a, items, small_groups);
-    return launch_pdl(merge_small_kernel<64>, grid, block, 0, stream, a, items, small_groups);
+    return launch_pdl(merge_small_kernel<D, MOD>, grid, block, 0, stream, a, items, small_groups);
   }
   if (num_long <= 0) {
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(num_items) * wide_groups));
-    if (a.head_dim == 128) return launch_pdl(merge_wide_kernel<128>, grid, block, 0, stream, a, items, wide_groups);
-    return launch_pdl(merge_wide_kernel<64>, grid, block, 0, stream, a, items, wide_groups);
+    return launch_pdl(merge_wide_kernel<D, MOD>, grid, block, 0, stream, a, items, wide_groups);
   }
   const int64_t ctas = static_cast<int64_t>(num_long) * small_groups +
                        static_cast<int64_t>(num_items - num_long) * wide_groups;
   const dim3 grid(static_cast<unsigned>(ctas));
+  return launch_pdl(merge_mixed_kernel<D, MOD>, grid, block, 0, stream, a, items, num_long, small_groups, wide_groups);
+}
+
+cudaError_t launch_merge(const StepArgs &a, int32_t num_items, int32_t num_long, const int32_t *items,
+                         cudaStream_t stream) {
+  if (num_items <= 0) return cudaSuccess;
   if (a.head_dim == 128)
-    return launch_pdl(merge_mixed_kernel<128>, grid, block, 0, stream, a, items, num_long, small_groups, wide_groups);
-  return launch_pdl(merge_mixed_kernel<64>, grid, block, 0, stream, a, items, num_long, small_groups, wide_groups);
+    return a.modified ? launch_merge_t<128, true>(a, num_items, num_long, items, stream)
+                      : launch_merge_t<128, false>(a, num_items, num_long, items, stream);
+  return a.modified ? launch_merge_t<64, true>(a, num_items, num_long, items, stream)
+                    : launch_merge_t<64, false>(a, num_items, num_long, items, stream);
 }
 
 }  // namespace pkv
