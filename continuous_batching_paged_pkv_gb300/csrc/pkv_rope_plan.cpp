@@ -65,18 +65,25 @@ pkv_status pkv_rope_plan(const pkv_rope_config *c, double *frequencies, uint64_t
   };
   const double first = c->scaling == PKV_ROPE_YARN ? std::max(std::floor(index_of(c->high)), 0.0) : 0.0;
   const double last = c->scaling == PKV_ROPE_YARN ? std::min(std::ceil(index_of(c->low)), n - 1.0) : 0.0;
-  for (int32_t i = 0; i < pairs; ++i) {
-    double f = std::pow(base, -2.0 * i / n);
-    if (c->scaling == PKV_ROPE_LINEAR) {
-      f /= s;
-    } else if (c->scaling == PKV_ROPE_BY_PARTS) {
+  auto frequency = [&](int32_t i) {
+    const double f = std::pow(base, -2.0 * i / n);
+    if (c->scaling == PKV_ROPE_LINEAR) return f / s;
+    if (c->scaling == PKV_ROPE_BY_PARTS) {
       const double g =
           std::min(1.0, std::max(0.0, (c->original_len * f / kTwoPi - c->low) / (c->high - c->low)));
-      f *= g + (1.0 - g) / s;
-    } else if (c->scaling == PKV_ROPE_YARN) {
-      const double g = std::min(1.0, std::max(0.0, (i - first) / std::max(last - first, 0.001)));
-      f *= (1.0 - g) + g / s;
+      return f * (g + (1.0 - g) / s);
     }
+    if (c->scaling == PKV_ROPE_YARN) {
+      const double g = std::min(1.0, std::max(0.0, (i - first) / std::max(last - first, 0.001)));
+      return f * ((1.0 - g) + g / s);
+    }
+    return f;
+  };
+  // A factor near 0 can take a frequency past the largest double (and base past the smallest).
+  for (int32_t i = 0; i < pairs; ++i)
+    if (!std::isfinite(frequency(i))) return PKV_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < pairs; ++i) {
+    const double f = frequency(i);
     if (frequencies) frequencies[i] = f;
     if (phases) phases[i] = phase_of(f);
   }

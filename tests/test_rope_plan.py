@@ -126,3 +126,18 @@ def test_unsupported_head_dim_and_empty_steps():
     assert _write(t=0) == B.PKV_OK
     assert B._lib().pkv_rope(AT, 512, AT, ctypes.byref(_table()), 0, 4, 128, AT, 512, None) == B.PKV_OK
     assert B._lib().pkv_rope(AT, 512, AT, ctypes.byref(_table()), 4, 4, 128, AT + 32, 512, None) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(scaling=B.PKV_ROPE_LINEAR, factor=5e-324), dict(scaling=B.PKV_ROPE_LINEAR, factor=1e-309),
+                                dict(scaling=B.PKV_ROPE_NTK, factor=1e-200, rot_dim=4),
+                                dict(scaling=B.PKV_ROPE_BY_PARTS, factor=5e-324, original_len=4096),
+                                dict(scaling=B.PKV_ROPE_YARN, factor=5e-324, original_len=4096)])
+def test_frequencies_past_the_largest_double_are_refused(kw):
+    kw = dict(rot_dim=64) | kw
+    n = kw["rot_dim"] // 2
+    cfg = B.RopeConfig(kw["rot_dim"], kw["scaling"], 10000.0, kw["factor"], kw.get("original_len", 0), 1.0, 32.0)
+    freqs, phases, mag = np.full(n, 7.0), np.full(n, 7, np.uint64), ctypes.c_float(7)
+    assert B._lib().pkv_rope_plan(ctypes.byref(cfg), B._np_ptr(freqs), B._np_ptr(phases), ctypes.byref(mag)) == 1
+    assert (freqs == 7).all() and (phases == 7).all() and mag.value == 7
+    small = B.pkv_rope_plan(64, scaling=B.PKV_ROPE_LINEAR, factor=1e-300)  # far out, but finite
+    assert np.isfinite(small.frequencies).all()
