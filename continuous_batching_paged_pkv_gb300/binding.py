@@ -304,6 +304,24 @@ def pkv_plan_work(cu_seqlens_q, seq_slot, context_lens, *, max_slots: int, max_b
     return work, info
 
 
+def _host_bounds(a, rows: int, what: str):
+    """Host key bounds as int32, one per packed row; values that int32 does not hold are refused, not wrapped."""
+    if a is None:
+        return None
+    b = np.asarray(a)
+    if b.shape != (rows,):
+        raise ValueError(f"{what} must have one entry per packed row ({rows}), got {b.shape}")
+    if rows and (b.dtype.kind not in "iu" or b.min() < -2 ** 31 or b.max() >= 2 ** 31):
+        raise ValueError(f"{what} must hold integers within 32 bits")
+    return np.ascontiguousarray(b, dtype=np.int32)
+
+
+def _window(window) -> int:
+    if window != int(window) or not -2 ** 31 <= window < 2 ** 31:
+        raise ValueError(f"window must be an integer within 32 bits, got {window}")
+    return int(window)
+
+
 def pkv_plan_work_mod(cu_seqlens_q, seq_slot, context_lens, *, max_slots: int, max_blocks_per_slot: int,
                       block_size: int, num_q_heads: int, num_kv_heads: int, head_dim: int, window: int = 0,
                       key_begin=None, key_end=None):
@@ -312,11 +330,8 @@ def pkv_plan_work_mod(cu_seqlens_q, seq_slot, context_lens, *, max_slots: int, m
     cu = np.ascontiguousarray(cu_seqlens_q, dtype=np.int32)
     ss = np.ascontiguousarray(seq_slot, dtype=np.int32)
     cl = np.ascontiguousarray(context_lens, dtype=np.int32)
-    kb, ke = (None if a is None else np.ascontiguousarray(a, dtype=np.int32) for a in (key_begin, key_end))
-    for a, nm in ((kb, "key_begin"), (ke, "key_end")):
-        if a is not None and a.shape != (int(cu[-1]),):
-            raise ValueError(f"{nm} must have one entry per packed row ({int(cu[-1])}), got {a.shape}")
-    mod = ScoreModArgs(0.0, window, None, _np_ptr(kb), _np_ptr(ke))
+    kb, ke = (_host_bounds(a, int(cu[-1]), nm) for a, nm in ((key_begin, "key_begin"), (key_end, "key_end")))
+    mod = ScoreModArgs(0.0, _window(window), None, _np_ptr(kb), _np_ptr(ke))
     info = WorkInfo()
     args = (_np_ptr(cu), len(cu) - 1, _np_ptr(ss), _np_ptr(cl), max_slots, max_blocks_per_slot, block_size,
             num_q_heads, num_kv_heads, head_dim, ctypes.byref(mod))
@@ -575,7 +590,7 @@ class ScoreMod:
                 if t.numel() != n:
                     raise ValueError(f"{nm} must hold {n} values, got {t.numel()}")
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        return ScoreModArgs(float(self.softcap), int(self.window), ptr(self.alibi_slopes), ptr(self.key_begin),
+        return ScoreModArgs(float(self.softcap), _window(self.window), ptr(self.alibi_slopes), ptr(self.key_begin),
                             ptr(self.key_end))
 
 

@@ -231,3 +231,27 @@ def test_a_gap_between_rows_is_covered(head_dim):
     assert all(a[1] == b[0] for a, b in zip(keys, keys[1:]))
     (scratch,) = items[len(items) - info.num_scratch_items:]
     assert scratch[1] == 100 // 16 and scratch[1] + scratch[3] == -(-2050 // 16)
+
+
+def test_bounds_and_windows_that_32_bits_do_not_hold_are_refused():
+    """ "No bound" written as 2^31 or more must not wrap to a row that sees nothing, nor a huge window to a small one."""
+    shape = dict(max_slots=1, max_blocks_per_slot=4, block_size=16, num_q_heads=4, num_kv_heads=2, head_dim=64)
+    for value in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1, 2 ** 63 - 1):
+        for name in ("key_begin", "key_end"):
+            for kind in (np.int64, list):
+                a = np.full(2, value, np.int64)
+                with pytest.raises(ValueError):
+                    B.pkv_plan_work_mod([0, 2], [0], [40], **{name: a if kind is np.int64 else a.tolist()}, **shape)
+    for value in (2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 31 - 1, 2.5):
+        with pytest.raises(ValueError):
+            B.pkv_plan_work_mod([0, 2], [0], [40], window=value, **shape)
+        with pytest.raises(ValueError):
+            B.ScoreMod(window=value).marshal(4, 2)
+    for a in (np.array([0.0, 1.0]), np.array([np.inf, 0.0]), np.array([True, False])):
+        with pytest.raises(ValueError):
+            B.pkv_plan_work_mod([0, 2], [0], [40], key_end=a, **shape)
+    most, least = 2 ** 31 - 1, -2 ** 31
+    wide, _ = B.pkv_plan_work_mod([0, 2], [0], [40], key_begin=[least] * 2, key_end=np.full(2, most), window=most, **shape)
+    same, _ = B.pkv_plan_work_mod([0, 2], [0], [40], key_end=[40, 40], **shape)
+    assert np.array_equal(wide, same)
+    assert B.ScoreMod(window=most).marshal(4, 2).window == most
