@@ -255,3 +255,16 @@ def test_bounds_and_windows_that_32_bits_do_not_hold_are_refused():
     same, _ = B.pkv_plan_work_mod([0, 2], [0], [40], key_end=[40, 40], **shape)
     assert np.array_equal(wide, same)
     assert B.ScoreMod(window=most).marshal(4, 2).window == most
+
+
+def test_arrays_shorter_than_their_counts_are_refused():
+    """seq_slot has one entry per segment, context_lens one per slot: the planner would read past shorter ones."""
+    shape = dict(max_blocks_per_slot=4, block_size=16, num_q_heads=4, num_kv_heads=2, head_dim=64)
+    for cu, ss, cl, slots in (([0, 1, 2], [0], [40, 40], 2), ([0, 1], [0, 1], [40, 40], 2), ([0, 1], [0], [40], 2),
+                              ([0, 1], [3], [40, 40], 4), ([], [], [40], 1)):
+        with pytest.raises(ValueError):
+            B.pkv_plan_work_mod(cu, ss, cl, max_slots=slots, **shape)
+    B.pkv_plan_work_mod([0, 1], [0], [40, 40, 40], max_slots=2, **shape)
+    for cu, ss in (([], []), ([0, 1], []), ([0, 1], [0, 1])):
+        with pytest.raises(ValueError):
+            B.pkv_plan_positions(cu, ss, [40, 40])
