@@ -500,10 +500,12 @@ class _BoundCall:
         kinds = getattr(_lib(), name).argtypes
         self._args = tuple(t(a) if isinstance(a, (int, float)) else a for a, t in zip(args, kinds))
         self._name, self._keep, self._device = name, keep, device.index
-        self._current = torch._C._cuda_getCurrentRawStream
+        self._current, self._current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         self._on = None if stream is None else _stream(stream)
 
     def __call__(self) -> None:
+        if self._current_device() != self._device:  # the library launches on the current device
+            raise ValueError(f"tensors are on cuda:{self._device}, the current device is cuda:{self._current_device()}")
         rc = self._fn(*self._args, ctypes.c_void_p(self._current(self._device)) if self._on is None else self._on)
         if rc != PKV_OK:
             raise PkvError(rc, self._name)

@@ -141,3 +141,21 @@ def test_frequencies_past_the_largest_double_are_refused(kw):
     assert (freqs == 7).all() and (phases == 7).all() and mag.value == 7
     small = B.pkv_rope_plan(64, scaling=B.PKV_ROPE_LINEAR, factor=1e-300)  # far out, but finite
     assert np.isfinite(small.frequencies).all()
+
+
+def test_a_bound_call_refuses_another_current_device(monkeypatch):
+    """A call is bound on its tensors' device and runs on the current one: they must be the same at every call."""
+    torch = pytest.importorskip("torch")
+    current = [0]
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    table = _table()
+    call = object.__new__(B._BoundCall)
+    call._bind("pkv_rope", (AT, 512, AT, ctypes.byref(table), 0, 4, 128, AT + (1 << 20), 512), (table,),
+               torch.device("cuda:0"), None)  # no tokens: nothing is launched
+    call()
+    current[0] = 1
+    with pytest.raises(ValueError):
+        call()
+    current[0] = 0
+    call()
