@@ -556,6 +556,16 @@ pkv_status plan_work(const int32_t *cu, int32_t num_seqs, const int32_t *seq_slo
   return PKV_OK;
 }
 
+// No exception leaves a C entry: sizes that the host has no memory for are refused.
+template <typename Fn, typename... Args>
+pkv_status no_throw(Fn fn, Args... args) {
+  try {
+    return fn(args...);
+  } catch (...) {
+    return PKV_ERR_INVALID_ARG;
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -565,8 +575,8 @@ pkv_status pkv_plan_work(const int32_t *cu, int32_t num_seqs, const int32_t *seq
                          int32_t max_blocks_per_slot, int32_t block_size, int32_t num_q_heads,
                          int32_t num_kv_heads, int32_t head_dim, int32_t *work,
                          int64_t work_capacity, pkv_work_info *info) {
-  return plan_work(cu, num_seqs, seq_slot, context_lens, max_slots, max_blocks_per_slot, block_size, num_q_heads,
-                   num_kv_heads, head_dim, nullptr, work, work_capacity, info);
+  return no_throw(plan_work, cu, num_seqs, seq_slot, context_lens, max_slots, max_blocks_per_slot, block_size,
+                  num_q_heads, num_kv_heads, head_dim, nullptr, work, work_capacity, info);
 }
 
 pkv_status pkv_plan_work_mod(const int32_t *cu, int32_t num_seqs, const int32_t *seq_slot,
@@ -574,8 +584,8 @@ pkv_status pkv_plan_work_mod(const int32_t *cu, int32_t num_seqs, const int32_t 
                              int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                              const pkv_score_mod *mod, int32_t *work, int64_t work_capacity, pkv_work_info *info) {
   if (!mod || mod->window < 0) return PKV_ERR_INVALID_ARG;
-  return plan_work(cu, num_seqs, seq_slot, context_lens, max_slots, max_blocks_per_slot, block_size, num_q_heads,
-                   num_kv_heads, head_dim, mod, work, work_capacity, info);
+  return no_throw(plan_work, cu, num_seqs, seq_slot, context_lens, max_slots, max_blocks_per_slot, block_size,
+                  num_q_heads, num_kv_heads, head_dim, mod, work, work_capacity, info);
 }
 
 }  // extern "C"

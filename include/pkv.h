@@ -272,7 +272,8 @@ typedef struct pkv_work_info {
  * length <= max_blocks_per_slot * block_size; supported head shape.
  * `work` receives info->work_words int32 values; if `work_capacity` is too
  * small (or `work` is NULL) the call fills `info` and returns
- * PKV_ERR_WORKSPACE_TOO_SMALL, so it can size the array first.
+ * PKV_ERR_WORKSPACE_TOO_SMALL, so it can size the array first. Sizes whose
+ * lists the host has no memory for are PKV_ERR_INVALID_ARG.
  */
 pkv_status pkv_plan_work(const int32_t *cu_seqlens_q, int32_t num_seqs,
                          const int32_t *seq_slot, const int32_t *context_lens,

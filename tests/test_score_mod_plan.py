@@ -2,6 +2,8 @@
 
 import ctypes
 import math
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -10,6 +12,7 @@ import oracle
 from oracle import scoremod as SM
 from continuous_batching_paged_pkv_gb300 import binding as B
 from continuous_batching_paged_pkv_gb300 import build as libbuild
+from tests.conftest import ROOT
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -268,3 +271,24 @@ def test_arrays_shorter_than_their_counts_are_refused():
     for cu, ss in (([], []), ([0, 1], []), ([0, 1], [0, 1])):
         with pytest.raises(ValueError):
             B.pkv_plan_positions(cu, ss, [40, 40])
+
+
+@pytest.mark.parametrize("fn", ["pkv_plan_work", "pkv_plan_work_mod"])
+def test_sizes_without_host_memory_are_refused(fn):
+    """A planner that cannot allocate its lists returns a status; an exception through the C entry would end the process."""
+    code = f"""
+import ctypes, resource
+import numpy as np
+from continuous_batching_paged_pkv_gb300 import binding as B
+L = B._lib()
+used = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (used + (256 << 20), used + (256 << 20)))
+cu, ss, cl = (np.array(a, np.int32) for a in ([0, 1], [0], [40]))
+mod, info, work = B.ScoreModArgs(), B.WorkInfo(), np.zeros(64, np.int32)
+mods = (ctypes.byref(mod),) if {fn!r} == "pkv_plan_work_mod" else ()
+call = lambda slots: getattr(L, {fn!r})(B._np_ptr(cu), 1, B._np_ptr(ss), B._np_ptr(cl), slots, 4, 16, 4, 2, 64, *mods,
+                                        B._np_ptr(work), 64, ctypes.byref(info))
+print(call(2 ** 31 - 1), call(1))
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert (done.returncode, done.stdout.split()) == (0, ["1", "0"]), done
