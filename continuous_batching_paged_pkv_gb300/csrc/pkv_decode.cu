@@ -472,8 +472,10 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
                 pacc[mt * 16 + 8] = acc[nt][mt][c + 2];
               }
               if (lane < 4) {
-                a.partial_ml[(pi + hh) * 2] = m[nt][c];
-                a.partial_ml[(pi + hh) * 2 + 1] = l[nt][c];
+                // a row that sees nothing: sums of 0 over a denominator that is not 0 merge to zeros
+                const bool nothing = MOD && tm.nothing(nt, c);
+                a.partial_ml[(pi + hh) * 2] = nothing ? 0.f : m[nt][c];
+                a.partial_ml[(pi + hh) * 2 + 1] = nothing ? 1.f : l[nt][c];
               }
             }
           }
@@ -538,7 +540,7 @@ constexpr int kPiece = 64;  // spans staged in shared memory at a time (a multip
 
 struct MergeRow {
   int row, spans, pbase, nrows;
-  bool bad, none;  // none: the row sees no key (modified scores)
+  bool bad;
 };
 
 // Decode a merge item and check it against the step metadata.
@@ -554,7 +556,6 @@ __device__ __forceinline__ MergeRow merge_row(const StepArgs &a, const int32_t *
   const int ri = (it.z >> 16) & 0xFF;
   r.nrows = ((it.z >> 24) & 0xFF) + 1;
   r.row = 0;
-  r.none = false;
   r.bad = seg < 0 || seg >= a.num_seqs || slot < 0 || slot >= a.max_slots || r.spans < 2 || r.pbase < 0 ||
           ri >= r.nrows;
   if (!r.bad) {
@@ -565,17 +566,11 @@ __device__ __forceinline__ MergeRow merge_row(const StepArgs &a, const int32_t *
             row0 < 0 || row0 + r.nrows > a.total_q ||
             r.nrows > L;
     // modified scores: spans of 64 keys or more over part of the history, partials inside the workspace
-    if constexpr (MOD) {
+    if constexpr (MOD)
       r.bad |= L / 64 + 2 < r.spans ||
                r.pbase + static_cast<int64_t>(r.spans - 1) * r.nrows >= static_cast<int64_t>(a.num_partials);
-      if (!r.bad) {
-        int lo, hi;
-        row_sees(a, r.row, L - r.nrows + ri, L, lo, hi);
-        r.none = lo >= hi;
-      }
-    } else {
+    else
       r.bad |= (L + PKV_SPLIT_KEYS - 1) / PKV_SPLIT_KEYS != r.spans;
-    }
   }
   return r;
 }
@@ -599,14 +594,13 @@ __device__ __forceinline__ void add_group(float &lt, float4 &at, float lg, const
 }
 
 template <int D>
-__device__ __forceinline__ void store_merged(const StepArgs &a, const MergeRow &r, int h, int col, float lt,
-                                             const float4 &at) {
-  const float inv = r.none ? 0.f : 1.f / lt;  // a row that sees nothing gives zeros
+__device__ __forceinline__ void store_merged(const StepArgs &a, int row, int h, int col, float lt, const float4 &at) {
+  const float inv = 1.f / lt;
   uint2 packed;
   packed.x = pack_bf16x2(__fmul_rn(at.x, inv), __fmul_rn(at.y, inv));
   packed.y = pack_bf16x2(__fmul_rn(at.z, inv), __fmul_rn(at.w, inv));
   *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) +
-                             (static_cast<size_t>(r.row) * a.num_q_heads + h) * D + 4 * col) = packed;
+                             (static_cast<size_t>(row) * a.num_q_heads + h) * D + 4 * col) = packed;
 }
 
 // Four lanes per float4 column: lane w of a column folds groups w, w + 4,
@@ -692,7 +686,7 @@ __device__ __forceinline__ void merge_small_body(const StepArgs &a, const int32_
       if (rd * 4 + j < groups) add_group(lt, at, lj, aj);
     }
   }
-  if (w == 0) store_merged<D>(a, r, h, col, lt, at);
+  if (w == 0) store_merged<D>(a, r.row, h, col, lt, at);
 }
 
 // One-dimensional grids, item-major: every head group of the first (longest)
@@ -772,7 +766,7 @@ __device__ __forceinline__ void merge_wide_body(const StepArgs &a, const int32_t
       add_group(lt, at, lg, ag);
     }
   }
-  if (live) store_merged<D>(a, r, h, col, lt, at);
+  if (live) store_merged<D>(a, r.row, h, col, lt, at);
 }
 
 template <int D, bool MOD>

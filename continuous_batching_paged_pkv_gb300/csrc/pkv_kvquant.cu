@@ -883,8 +883,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 *reinterpret_cast<float4 *>(pacc + 32 * g) =
                     make_float4(o[g][0] * kDown, o[g][1] * kDown, o[g][2] * kDown, o[g][3] * kDown);
               if (r == 0) {
-                a.partial_ml[pi * 2] = m[nt][c];
-                a.partial_ml[pi * 2 + 1] = l[nt][c] * kDown;
+                const bool nothing = MOD && tm.nothing(nt, c);  // as in the bf16 decode kernel
+                a.partial_ml[pi * 2] = nothing ? 0.f : m[nt][c];
+                a.partial_ml[pi * 2 + 1] = nothing ? 1.f : l[nt][c] * kDown;
               }
             }
           }

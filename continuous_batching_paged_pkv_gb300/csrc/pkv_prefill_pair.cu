@@ -85,7 +85,7 @@ constexpr int kOCol = 384;
 // warpgroup of the other launches keeps the same two sums, so a row's bits do not
 // depend on which of the two ran. 384 threads launched with 168 registers, shares
 // of 208, 208 and 88, five K/V stages. 2048 rows at context 8192: capped 292 us
-// with one group, 271 us with two; biased 206 and 198 us; only masked 185 and 186 us
+// with one group, 270 us with two; biased 206 and 196 us; only masked 185 and 186 us
 // (the tensor core's chain S, P, O through three buffers sets the pace there).
 template <int SG>
 struct Roles {
@@ -241,7 +241,7 @@ __global__ void __maxnreg__(Roles<SG>::kLaunchRegs) prefill_pair_kernel(const __
   // each. The tiles of cached keys come before those of this step's rows, at the
   // price of one rescaling, since the latter wait for the kernel before (2048
   // biased rows at context 8192, one call behind another: going up 272 us, straight
-  // down 233 us, so 206 us; with two softmax warpgroups 198 us).
+  // down 233 us, so 206 us; with two softmax warpgroups 196 us).
   constexpr bool kDown = (MODE & kModBias) != 0;
   const int old = kDown ? min(max(L - n - base, 0) / kKeysPerTile, ntiles) : 0;
   auto tile_at = [&](int j) { return !kDown ? j : j < old ? old - 1 - j : ntiles - 1 - (j - old); };

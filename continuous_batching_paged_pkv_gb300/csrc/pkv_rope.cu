@@ -7,7 +7,8 @@
 // (i, i + rot_dim / 2) in the half layout, (2 i, 2 i + 1) interleaved; elements
 // from rot_dim on pass through. The angle comes as a fraction of a turn: f is
 // a 64-bit fixed-point phase, p * phase modulo 2^64 is exact for every 32-bit
-// position, and its top 32 bits (2^-33 of a turn, 7e-10 rad) feed sincospi. An
+// position, and its top 32 bits feed sincospi as an fp32 fraction of half a turn:
+// off by at most pi 2^-25 (9e-8 rad, the rounding to 24 bits) at any position. An
 // angle in fp32 radians would be off by 4e-3 at position 131072. Products and
 // sums are fp32 and round once, to bf16.
 #include <cuda_bf16.h>
@@ -71,7 +72,10 @@ __device__ __forceinline__ HeadRow head_row(const RopeArgs &a, int64_t t, int h,
   return r;
 }
 
-// Any even rot_dim: one CTA per token, one pair of elements per thread.
+// Any even rot_dim: one CTA per token, one pair of elements per thread, with two
+// 2-byte loads and stores and an index division a pair. 24500 tokens of 64 + 8 heads
+// of 128, 120 elements rotated: 393 us, where whole vectors (rope_vectors_kernel, 128
+// elements) take 155.
 __global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const RopeArgs a) {
   __shared__ float2 turn[kMaxPairs];
   grid_dependency_wait();  // every input may come from the previous kernel in the stream
@@ -134,9 +138,10 @@ __device__ __forceinline__ void turn_pairs(uint4 &x, const float2 *w) {
 // the angles are computed. gridDim.y CTAs share a token's units where tokens are few.
 //
 // Bound by HBM: T (2 Hq + 4 Hkv) D 2 bytes move and the angles are shared by a
-// token's heads. What counts is CTAs in flight (12 of 128 threads per SM at 42
-// registers, or 24 of 64), since a CTA waits in turn for position, vectors and
-// stores: 24500 tokens of 64 + 8 heads of 128 take 155 us (6480 GB/s, 96% of the
+// token's heads. What counts is CTAs in flight (12 of 128 threads per SM at 40
+// registers and 32 spilled bytes, or 24 of 64), since a CTA waits in turn for
+// position, vectors and stores: 24500 tokens of 64 + 8 heads of 128 take 155 us
+// (6480 GB/s, 96% of the
 // measured copy rate); with three units in flight per thread and 80 registers
 // they took 223 us, and one pair of elements per thread 379 us.
 template <int D, bool INTERLEAVED>
@@ -202,8 +207,12 @@ cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream) {
   // Fewer tokens than SMs: one unit per thread, a token over several CTAs. Else one
   // CTA per token, with more units per thread (fewer, smaller CTAs reuse the angles
   // longer) the more tokens there are to fill the SMs. Measured with 3 / 5 / 10
-  // units: 256 tokens of 64 + 8 heads 4.3 / 4.9 / 6.8 us, 2048 of 32 + 8 13.7 /
-  // 10.9 / 11.9 us, 24500 of 64 + 8 175 / 162 / 152 us.
+  // units: 256 tokens of 64 + 8 heads 4.8 / 4.8 / 6.3 us, 2048 of 32 + 8 14.8 /
+  // 12.0 / 12.7 us, 24500 of 64 + 8 163 / 163 / 154 us (heads of 128). Over eight
+  // shapes from 4 + 2 heads of 64 to 64 + 8 of 128 and 256 to 24500 tokens the rule
+  // is within 0.5 us or 6% of the best of 1, 2, 3, 5 and 10 units, but for 256
+  // tokens of 8 + 8 or 14 + 2 heads of 64 (3.4 us, 2.7 with one unit) and 2048 of
+  // 64 + 8 heads of 128 (21.1 us, 18.4 with ten).
   const bool few = a.num_tokens < 152;
   const int per_thread = few ? 1 : a.num_tokens < 1024 ? 3 : a.num_tokens < 8192 ? 5 : 10;
   const int want = (units + per_thread - 1) / per_thread;

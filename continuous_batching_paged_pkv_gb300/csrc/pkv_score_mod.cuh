@@ -172,7 +172,7 @@ __device__ __forceinline__ float tile_max(const uint32_t (&sv)[4][32]) {
 // out, masked, and their maximum taken.
 //
 // Capped 2048-row chunk at context 8192, head_dim 128: 379 us with 2^x and 1/x for
-// every score, 373 us with the cubic written out first, 292 us fused (271 us with two warpgroups).
+// every score, 373 us with the cubic written out first, 292 us fused (270 us with two warpgroups).
 //
 // Products that a sum follows are rounded explicitly: the compiler must not fuse
 // them in one variant and not in another, or a row's last bits would depend on

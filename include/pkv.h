@@ -344,7 +344,8 @@ pkv_status pkv_cache_write(const void *k_new, const void *v_new, const int64_t *
  * The decode and chunk kernels read the step metadata, q and the cached
  * history at once and wait for that previous kernel only before reading the
  * 16-key sub-tiles (decode) or 128-key tiles (chunk) that hold this step's
- * new rows. So the previous kernel must not signal dependents before the
+ * new rows, and before they store anything; a call's kernels end only after it.
+ * So the previous kernel must not signal dependents before the
  * data it leaves for this call is complete: pkv_cache_write signals only
  * after every kernel before it has finished, and a kernel that does not use
  * programmatic dependent launch signals at its end. When a step has both prompt
