@@ -73,9 +73,9 @@ __device__ __forceinline__ HeadRow head_row(const RopeArgs &a, int64_t t, int h,
 }
 
 // Any even rot_dim: one CTA per token, one pair of elements per thread, with two
-// 2-byte loads and stores and an index division a pair. 24500 tokens of 64 + 8 heads
-// of 128, 120 elements rotated: 393 us, where whole vectors (rope_vectors_kernel, 128
-// elements) take 155.
+// 2-byte loads and stores and an index division a pair, which bind it (59% ALU, 65%
+// issue, 25% of DRAM). 24500 tokens of 64 + 8 heads of 128, 120 elements rotated: 393
+// us, where whole vectors (rope_vectors_kernel, 128 elements) take 155.
 __global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const RopeArgs a) {
   __shared__ float2 turn[kMaxPairs];
   grid_dependency_wait();  // every input may come from the previous kernel in the stream
@@ -141,9 +141,8 @@ __device__ __forceinline__ void turn_pairs(uint4 &x, const float2 *w) {
 // token's heads. What counts is CTAs in flight (12 of 128 threads per SM at 40
 // registers and 32 spilled bytes, or 24 of 64), since a CTA waits in turn for
 // position, vectors and stores: 24500 tokens of 64 + 8 heads of 128 take 155 us
-// (6480 GB/s, 96% of the
-// measured copy rate); with three units in flight per thread and 80 registers
-// they took 223 us, and one pair of elements per thread 379 us.
+// (6480 GB/s, 96% of the measured copy rate); with three units in flight per thread
+// and 80 registers they took 223 us, and one pair of elements per thread 379 us.
 template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 12) rope_vectors_kernel(const RopeArgs a) {
   constexpr int U = D / 16;  // units per head
