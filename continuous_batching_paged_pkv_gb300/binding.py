@@ -330,8 +330,8 @@ def pkv_plan_work_mod(cu_seqlens_q, seq_slot, context_lens, *, max_slots: int, m
     cu = np.ascontiguousarray(cu_seqlens_q, dtype=np.int32)
     ss = np.ascontiguousarray(seq_slot, dtype=np.int32)
     cl = np.ascontiguousarray(context_lens, dtype=np.int32)
-    if len(cu) < 1 or len(ss) != len(cu) - 1 or len(cl) < max_slots:
-        raise ValueError("cu_seqlens_q must have one entry more than seq_slot, context_lens one per slot")
+    if len(cu) < 1 or len(ss) < len(cu) - 1 or len(cl) < max_slots:
+        raise ValueError("seq_slot must have one entry per segment, context_lens one per slot")
     kb, ke = (_host_bounds(a, int(cu[-1]), nm) for a, nm in ((key_begin, "key_begin"), (key_end, "key_end")))
     mod = ScoreModArgs(0.0, _window(window), None, _np_ptr(kb), _np_ptr(ke))
     info = WorkInfo()

@@ -263,11 +263,11 @@ def test_bounds_and_windows_that_32_bits_do_not_hold_are_refused():
 def test_arrays_shorter_than_their_counts_are_refused():
     """seq_slot has one entry per segment, context_lens one per slot: the planner would read past shorter ones."""
     shape = dict(max_blocks_per_slot=4, block_size=16, num_q_heads=4, num_kv_heads=2, head_dim=64)
-    for cu, ss, cl, slots in (([0, 1, 2], [0], [40, 40], 2), ([0, 1], [0, 1], [40, 40], 2), ([0, 1], [0], [40], 2),
-                              ([0, 1], [3], [40, 40], 4), ([], [], [40], 1)):
+    for cu, ss, cl, slots in (([0, 1, 2], [0], [40, 40], 2), ([0, 1], [0], [40], 2), ([0, 1], [3], [40, 40], 4),
+                              ([], [], [40], 1)):
         with pytest.raises(ValueError):
             B.pkv_plan_work_mod(cu, ss, cl, max_slots=slots, **shape)
-    B.pkv_plan_work_mod([0, 1], [0], [40, 40, 40], max_slots=2, **shape)
+    B.pkv_plan_work_mod([0, 1], [0, 1], [40, 40, 40], max_slots=2, **shape)  # longer ones are not
     for cu, ss in (([], []), ([0, 1], []), ([0, 1], [0, 1])):
         with pytest.raises(ValueError):
             B.pkv_plan_positions(cu, ss, [40, 40])
