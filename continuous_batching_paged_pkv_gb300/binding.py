@@ -59,6 +59,12 @@ class ScoreModArgs(ctypes.Structure):
                 ("key_begin", ctypes.c_void_p), ("key_end", ctypes.c_void_p)]
 
 
+class SparseArgs(ctypes.Structure):
+    """``pkv_sparse``."""
+
+    _fields_ = [("top_blocks", ctypes.c_int32), ("keep_first", ctypes.c_int32), ("keep_last", ctypes.c_int32)]
+
+
 class StageLayout(ctypes.Structure):
     _fields_ = [("total_q", ctypes.c_int64), ("num_seqs", ctypes.c_int32), ("max_slots", ctypes.c_int32),
                 ("max_blocks_per_slot", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
@@ -143,6 +149,21 @@ def _lib():
             "pkv_rope": ([p, i64, p, ctypes.POINTER(RopeTable), i64, i32, i32, p, i64, p], ctypes.c_int),
             "pkv_rope_cache_write": ([p, i64, p, i64, p, i64, p, p, ctypes.POINTER(RopeTable), i64, i32, i32, i32, p,
                                       i64, p, p, i64, i32, p, p], ctypes.c_int),
+            "pkv_pool_truncate": ([p, i32, i64], ctypes.c_int),
+            "pkv_key_bounds": ([p, i64, p, i64, i32, i32, i32, p, p, p], ctypes.c_int),
+            "pkv_plan_work_sparse": ([p, i32, p, p, i32, i32, i32, i32, i32, i32, ctypes.POINTER(SparseArgs), p, i64,
+                                      ctypes.POINTER(WorkInfo)], ctypes.c_int),
+            "pkv_select_blocks": ([p, p, i32, i64, p, p, p, i32, i32, i32, p, i64, i32, i32, i32,
+                                   ctypes.POINTER(SparseArgs), p, ctypes.POINTER(WorkInfo), p, p, u64, p, p],
+                                  ctypes.c_int),
+            "pkv_attention_sparse": ([p, p, i32, i64, p, p, p, i32, i32, i32, p, p, i64, i32, i32, i32, f32,
+                                      ctypes.POINTER(SparseArgs), p, p, ctypes.POINTER(WorkInfo), p, p, u64, p, p],
+                                     ctypes.c_int),
+            "pkv_tree_masks": ([p, p, i32, i32, p, p], ctypes.c_int),
+            "pkv_plan_work_tree": ([p, i32, p, p, i32, i32, i32, i32, i32, i32, p, i64, ctypes.POINTER(WorkInfo)],
+                                   ctypes.c_int),
+            "pkv_accept_rows": ([p, i32, i64, p, p, p, i32, i32, i32, i32, p, i32, ctypes.POINTER(ctypes.c_void_p),
+                                 ctypes.POINTER(ctypes.c_int64), i32, i64, p, p], ctypes.c_int),
             "pkv_stage_layout_init": ([ctypes.POINTER(StageLayout), i64, i32, i32, i32, i32, i32, i32], ctypes.c_int),
             "pkv_step": ([ctypes.POINTER(StageLayout), p, u64, p, u64, p, p, i64, i32, f32, p, u64, p, p, p, p,
                           ctypes.POINTER(WorkInfo), ctypes.c_uint32], ctypes.c_int),
@@ -151,6 +172,10 @@ def _lib():
             sig[f"pkv_attention_mod_q{bits}"] = ([p, p, i32, i64, p, p, p, i32, i32, i32, p, p, p, p, i64, i32, i32, i32,
                                                   f32, ctypes.POINTER(ScoreModArgs), p, ctypes.POINTER(WorkInfo), p, p,
                                                   u64, p, p], ctypes.c_int)
+            sig[f"pkv_key_bounds_q{bits}"] = ([p, i64, p, p, i64, i32, i32, i32, p, p, p], ctypes.c_int)
+            sig[f"pkv_attention_sparse_q{bits}"] = ([p, p, i32, i64, p, p, p, i32, i32, i32, p, p, p, p, i64, i32, i32,
+                                                     i32, f32, ctypes.POINTER(SparseArgs), p, p,
+                                                     ctypes.POINTER(WorkInfo), p, p, u64, p, p], ctypes.c_int)
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
@@ -239,6 +264,10 @@ class Pool:
     def adopt(self, slot: int, donor_slot: int, num_tokens: int, reserve_tokens: int = 0) -> int:
         """``pkv_pool_adopt``; returns the status code (PKV_ERR_NO_BLOCKS is an answer, not an error)."""
         return _lib().pkv_pool_adopt(self._h, slot, donor_slot, num_tokens, reserve_tokens)
+
+    def truncate(self, slot: int, num_tokens: int) -> None:
+        """``pkv_pool_truncate``: the slot keeps its first ``num_tokens`` tokens."""
+        _check(_lib().pkv_pool_truncate(self._h, slot, num_tokens), "pkv_pool_truncate")
 
     def block_refs(self, block: int) -> int:
         return _lib().pkv_pool_block_refs(self._h, block)
@@ -343,6 +372,70 @@ def pkv_plan_work_mod(cu_seqlens_q, seq_slot, context_lens, *, max_slots: int, m
     work = np.zeros(max(info.work_words, PKV_WORK_WORDS_PER_ITEM), np.int32)
     _check(_lib().pkv_plan_work_mod(*args, _np_ptr(work), len(work), ctypes.byref(info)), "pkv_plan_work_mod")
     return work, info
+
+
+@dataclass(frozen=True)
+class Sparse:
+    """``pkv_sparse``: blocks read per segment, of them the first ones and those before the step's rows that are
+    always read."""
+
+    top_blocks: int
+    keep_first: int = 1
+    keep_last: int = 1
+
+    def marshal(self) -> SparseArgs:
+        for v, nm in ((self.top_blocks, "top_blocks"), (self.keep_first, "keep_first"), (self.keep_last, "keep_last")):
+            if v != int(v) or not 0 <= v < 2 ** 31:
+                raise ValueError(f"{nm} must be a non-negative integer within 32 bits, got {v}")
+        return SparseArgs(int(self.top_blocks), int(self.keep_first), int(self.keep_last))
+
+
+def _plan_list(name, cu_seqlens_q, seq_slot, context_lens, max_slots, *shape_and_more):
+    """(work, WorkInfo) of a planner: sized first, then filled."""
+    cu = np.ascontiguousarray(cu_seqlens_q, dtype=np.int32)
+    ss = np.ascontiguousarray(seq_slot, dtype=np.int32)
+    cl = np.ascontiguousarray(context_lens, dtype=np.int32)
+    if len(cu) < 1 or len(ss) < len(cu) - 1 or len(cl) < max_slots:
+        raise ValueError("seq_slot must have one entry per segment, context_lens one per slot")
+    info = WorkInfo()
+    args = (_np_ptr(cu), len(cu) - 1, _np_ptr(ss), _np_ptr(cl), max_slots, *shape_and_more)
+    fn = getattr(_lib(), name)
+    rc = fn(*args, None, 0, ctypes.byref(info))
+    if rc != PKV_ERR_WORKSPACE_TOO_SMALL:
+        _check(rc, name)
+    work = np.zeros(max(info.work_words, PKV_WORK_WORDS_PER_ITEM), np.int32)
+    _check(fn(*args, _np_ptr(work), len(work), ctypes.byref(info)), name)
+    return work, info
+
+
+def pkv_plan_work_sparse(cu_seqlens_q, seq_slot, context_lens, *, max_slots: int, max_blocks_per_slot: int,
+                         block_size: int, num_q_heads: int, num_kv_heads: int, head_dim: int, sparse: Sparse):
+    """``pkv_plan_work`` for a block-sparse step: (work int32 array, WorkInfo)."""
+    return _plan_list("pkv_plan_work_sparse", cu_seqlens_q, seq_slot, context_lens, max_slots, max_blocks_per_slot,
+                      block_size, num_q_heads, num_kv_heads, head_dim, ctypes.byref(sparse.marshal()))
+
+
+def pkv_plan_work_tree(cu_seqlens_q, seq_slot, context_lens, *, max_slots: int, max_blocks_per_slot: int,
+                       block_size: int, num_q_heads: int, num_kv_heads: int, head_dim: int):
+    """``pkv_plan_work`` for a step of trees: (work int32 array, WorkInfo)."""
+    return _plan_list("pkv_plan_work_tree", cu_seqlens_q, seq_slot, context_lens, max_slots, max_blocks_per_slot,
+                      block_size, num_q_heads, num_kv_heads, head_dim)
+
+
+def pkv_tree_masks(parents, cu_seqlens_q, mask_words: int | None = None):
+    """(masks uint32 [rows, words], depths int32 [rows]) of a packed step's trees; ``parents``: per packed row, the
+    parent within its segment or -1. Rows before the first segment's are zero."""
+    cu = np.ascontiguousarray(cu_seqlens_q, dtype=np.int32)
+    pa = np.ascontiguousarray(parents, dtype=np.int32)
+    rows = int(cu[-1]) if len(cu) else 0
+    if len(cu) < 1 or len(pa) < rows:
+        raise ValueError("parents must have one entry per packed row")
+    if mask_words is None:
+        mask_words = max(1, -(-int(np.diff(cu).max(initial=0)) // 32))
+    masks, depths = np.zeros((max(rows, 0), mask_words), np.uint32), np.zeros(max(rows, 0), np.int32)
+    _check(_lib().pkv_tree_masks(_np_ptr(pa), _np_ptr(cu), len(cu) - 1, mask_words, _np_ptr(masks), _np_ptr(depths)),
+           "pkv_tree_masks")
+    return masks, depths
 
 
 def pkv_plan_positions(cu_seqlens_q, seq_slot, context_lens) -> np.ndarray:
@@ -660,6 +753,190 @@ def pkv_attention_mod_q4(q, cu_seqlens_q, seq_slot, context_lens, block_tables, 
                          device_status=None, stream=None) -> None:
     AttentionModCall(q, cu_seqlens_q, seq_slot, context_lens, block_tables, (k_codes, k_scales, v_codes, v_scales), work,
                      info, out, workspace, mod=mod, kv="q4", scale=scale, device_status=device_status, stream=stream)()
+
+
+def _need_pool(pool, kv: str):
+    """(blocks, kv heads, block_size, head_dim) of a pool: (k, v) in bf16, (codes, scales) of each in 8 and 4 bits."""
+    if kv not in ("bf16", "q8", "q4") or len(pool) != (2 if kv == "bf16" else 4):
+        raise ValueError(f"a pool is 2 (bf16) or 4 (q8, q4) tensors, got {len(pool)} as {kv!r}")
+    if kv != "bf16":
+        return _need_quant_pool(*pool, int(kv[1]))
+    for t, nm in zip(pool, ("k_pool", "v_pool")):
+        _need(t, "torch.bfloat16", nm)
+    if pool[0].dim() != 4 or pool[1].shape != pool[0].shape:
+        raise ValueError("k_pool and v_pool must be [blocks, kv heads, block_size, head_dim], alike")
+    return tuple(pool[0].shape)
+
+
+def _need_step(q, cu_seqlens_q, seq_slot, context_lens, block_tables, work, info, head_dim, num_kv_heads):
+    """Shapes of a step's device metadata; returns (segments, max_slots, max_blocks_per_slot)."""
+    _need(q, "torch.bfloat16", "q")
+    for t, nm in ((cu_seqlens_q, "cu_seqlens_q"), (seq_slot, "seq_slot"), (context_lens, "context_lens"),
+                  (block_tables, "block_tables"), (work, "work")):
+        _need(t, "torch.int32", nm)
+    if q.dim() != 3 or q.shape[2] != head_dim or q.shape[1] % num_kv_heads:
+        raise ValueError(f"q must be [rows, q heads, {head_dim}] with a multiple of {num_kv_heads} heads")
+    ms, mbps = block_tables.shape
+    segs = cu_seqlens_q.numel() - 1
+    if segs < 0 or context_lens.numel() != ms or seq_slot.numel() < segs:
+        raise ValueError("context_lens must have one entry per slot, seq_slot one per segment")
+    if work.numel() < info.work_words:
+        raise ValueError(f"work holds {work.numel()} words, info names {info.work_words}")
+    return segs, ms, mbps
+
+
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+class KeyBoundsCall(_BoundCall):
+    """``pkv_key_bounds`` (``kv="bf16"``, ``keys`` = (k_pool,)) or ``pkv_key_bounds_q8`` / ``_q4`` (``keys`` =
+    (k_codes, k_scales)) bound once. ``bounds``: bf16 [blocks, kv heads, 2, head_dim]."""
+
+    def __init__(self, slot_mapping, keys, bounds, *, kv: str = "bf16", device_status=None, stream=None):
+        _need(slot_mapping, "torch.int64", "slot_mapping")
+        _need(bounds, "torch.bfloat16", "bounds")
+        if len(keys) != (1 if kv == "bf16" else 2):
+            raise ValueError(f"keys are 1 (bf16) or 2 (q8, q4) tensors, got {len(keys)} as {kv!r}")
+        nb, hkv, bs, d = _need_pool((*keys, *keys), kv)
+        if tuple(bounds.shape) != (nb, hkv, 2, d):
+            raise ValueError(f"bounds must be [{nb}, {hkv}, 2, {d}], got {tuple(bounds.shape)}")
+        _need_on(slot_mapping.device, *keys, bounds, device_status)
+        self._bind("pkv_key_bounds" + ("" if kv == "bf16" else f"_{kv}"),
+                   (_t_ptr(slot_mapping), slot_mapping.numel(), *map(_t_ptr, keys), nb, bs, hkv, d, _t_ptr(bounds),
+                    _t_ptr(device_status)), (slot_mapping, tuple(keys), bounds, device_status), slot_mapping.device,
+                   stream)
+
+
+def pkv_key_bounds(slot_mapping, k_pool, bounds, *, device_status=None, stream=None) -> None:
+    KeyBoundsCall(slot_mapping, (k_pool,), bounds, device_status=device_status, stream=stream)()
+
+
+def pkv_key_bounds_q8(slot_mapping, k_codes, k_scales, bounds, *, device_status=None, stream=None) -> None:
+    KeyBoundsCall(slot_mapping, (k_codes, k_scales), bounds, kv="q8", device_status=device_status, stream=stream)()
+
+
+def pkv_key_bounds_q4(slot_mapping, k_codes, k_scales, bounds, *, device_status=None, stream=None) -> None:
+    KeyBoundsCall(slot_mapping, (k_codes, k_scales), bounds, kv="q4", device_status=device_status, stream=stream)()
+
+
+class SelectBlocksCall(_BoundCall):
+    """``pkv_select_blocks`` bound once. ``selected``: int32 [segments, kv heads, top_blocks]."""
+
+    def __init__(self, q, cu_seqlens_q, seq_slot, context_lens, block_tables, bounds, work, info: WorkInfo, selected,
+                 workspace=None, *, sparse: Sparse, block_size: int, device_status=None, stream=None):
+        _need(bounds, "torch.bfloat16", "bounds")
+        _need(selected, "torch.int32", "selected")
+        if bounds.dim() != 4 or bounds.shape[2] != 2:
+            raise ValueError("bounds must be [blocks, kv heads, 2, head_dim]")
+        nb, hkv, _, d = bounds.shape
+        segs, ms, mbps = _need_step(q, cu_seqlens_q, seq_slot, context_lens, block_tables, work, info, d, hkv)
+        args, info = sparse.marshal(), WorkInfo.from_buffer_copy(info)
+        if tuple(selected.shape) != (segs, hkv, args.top_blocks):
+            raise ValueError(f"selected must be [{segs}, {hkv}, {args.top_blocks}], got {tuple(selected.shape)}")
+        _need_on(q.device, cu_seqlens_q, seq_slot, context_lens, block_tables, bounds, work, selected, workspace,
+                 device_status)
+        self._bind("pkv_select_blocks",
+                   (_t_ptr(q), _t_ptr(cu_seqlens_q), segs, q.shape[0], _t_ptr(seq_slot), _t_ptr(context_lens),
+                    _t_ptr(block_tables), ms, mbps, block_size, _t_ptr(bounds), nb, q.shape[1], hkv, d,
+                    ctypes.byref(args), _t_ptr(work), ctypes.byref(info), _t_ptr(selected), _t_ptr(workspace),
+                    _bytes(workspace), _t_ptr(device_status)),
+                   (q, cu_seqlens_q, seq_slot, context_lens, block_tables, bounds, work, info, selected, workspace, args,
+                    device_status), q.device, stream)
+
+
+def pkv_select_blocks(q, cu_seqlens_q, seq_slot, context_lens, block_tables, bounds, work, info: WorkInfo, selected,
+                      workspace=None, *, sparse: Sparse, block_size: int, device_status=None, stream=None) -> None:
+    SelectBlocksCall(q, cu_seqlens_q, seq_slot, context_lens, block_tables, bounds, work, info, selected, workspace,
+                     sparse=sparse, block_size=block_size, device_status=device_status, stream=stream)()
+
+
+class AttentionSparseCall(_BoundCall):
+    """``pkv_attention_sparse`` (``kv="bf16"``, ``pool`` = (k_pool, v_pool)) or ``pkv_attention_sparse_q8`` / ``_q4``
+    (``pool`` = (k_codes, k_scales, v_codes, v_scales)) bound once."""
+
+    def __init__(self, q, cu_seqlens_q, seq_slot, context_lens, block_tables, pool, selected, work, info: WorkInfo, out,
+                 workspace=None, *, sparse: Sparse, kv: str = "bf16", scale: float = 0.0, device_status=None, stream=None):
+        nb, hkv, bs, d = _need_pool(pool, kv)
+        segs, ms, mbps = _need_step(q, cu_seqlens_q, seq_slot, context_lens, block_tables, work, info, d, hkv)
+        _need(out, "torch.bfloat16", "out")
+        _need(selected, "torch.int32", "selected")
+        args, info = sparse.marshal(), WorkInfo.from_buffer_copy(info)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if tuple(selected.shape) != (segs, hkv, args.top_blocks):
+            raise ValueError(f"selected must be [{segs}, {hkv}, {args.top_blocks}], got {tuple(selected.shape)}")
+        _need_on(q.device, cu_seqlens_q, seq_slot, context_lens, block_tables, *pool, selected, work, out, workspace,
+                 device_status)
+        self._bind("pkv_attention_sparse" + ("" if kv == "bf16" else f"_{kv}"),
+                   (_t_ptr(q), _t_ptr(cu_seqlens_q), segs, q.shape[0], _t_ptr(seq_slot), _t_ptr(context_lens),
+                    _t_ptr(block_tables), ms, mbps, bs, *map(_t_ptr, pool), nb, q.shape[1], hkv, d, float(scale),
+                    ctypes.byref(args), _t_ptr(selected), _t_ptr(work), ctypes.byref(info), _t_ptr(out),
+                    _t_ptr(workspace), _bytes(workspace), _t_ptr(device_status)),
+                   (q, cu_seqlens_q, seq_slot, context_lens, block_tables, tuple(pool), selected, work, info, out,
+                    workspace, args, device_status), q.device, stream)
+
+
+def pkv_attention_sparse(q, cu_seqlens_q, seq_slot, context_lens, block_tables, k_pool, v_pool, selected, work,
+                         info: WorkInfo, out, workspace=None, *, sparse: Sparse, scale: float = 0.0, device_status=None,
+                         stream=None) -> None:
+    AttentionSparseCall(q, cu_seqlens_q, seq_slot, context_lens, block_tables, (k_pool, v_pool), selected, work, info,
+                        out, workspace, sparse=sparse, scale=scale, device_status=device_status, stream=stream)()
+
+
+def pkv_attention_sparse_q8(q, cu_seqlens_q, seq_slot, context_lens, block_tables, k_codes, k_scales, v_codes, v_scales,
+                            selected, work, info: WorkInfo, out, workspace=None, *, sparse: Sparse, scale: float = 0.0,
+                            device_status=None, stream=None) -> None:
+    AttentionSparseCall(q, cu_seqlens_q, seq_slot, context_lens, block_tables, (k_codes, k_scales, v_codes, v_scales),
+                        selected, work, info, out, workspace, sparse=sparse, kv="q8", scale=scale,
+                        device_status=device_status, stream=stream)()
+
+
+def pkv_attention_sparse_q4(q, cu_seqlens_q, seq_slot, context_lens, block_tables, k_codes, k_scales, v_codes, v_scales,
+                            selected, work, info: WorkInfo, out, workspace=None, *, sparse: Sparse, scale: float = 0.0,
+                            device_status=None, stream=None) -> None:
+    AttentionSparseCall(q, cu_seqlens_q, seq_slot, context_lens, block_tables, (k_codes, k_scales, v_codes, v_scales),
+                        selected, work, info, out, workspace, sparse=sparse, kv="q4", scale=scale,
+                        device_status=device_status, stream=stream)()
+
+
+class AcceptRowsCall(_BoundCall):
+    """``pkv_accept_rows`` bound once. ``paths``: int32 [segments, depths]; ``arrays``: the pool's arrays, each
+    [blocks, kv heads, block_size, ...]."""
+
+    def __init__(self, cu_seqlens_q, seq_slot, context_lens, block_tables, paths, arrays, *, total_q: int | None = None,
+                 device_status=None, stream=None):
+        for t, nm in ((cu_seqlens_q, "cu_seqlens_q"), (seq_slot, "seq_slot"), (context_lens, "context_lens"),
+                      (block_tables, "block_tables"), (paths, "paths")):
+            _need(t, "torch.int32", nm)
+        ms, mbps = block_tables.shape
+        segs = cu_seqlens_q.numel() - 1
+        if segs < 0 or context_lens.numel() != ms or seq_slot.numel() < segs:
+            raise ValueError("context_lens must have one entry per slot, seq_slot one per segment")
+        if paths.dim() != 2 or paths.shape[0] != segs:
+            raise ValueError("paths must be [segments, depths]")
+        if not arrays or len(arrays) > 4:
+            raise ValueError("pkv_accept_rows takes one to four pool arrays")
+        for t in arrays:
+            if not t.is_cuda or not t.is_contiguous() or t.dim() != 4 or t.shape[:3] != arrays[0].shape[:3]:
+                raise ValueError("pool arrays must be contiguous CUDA tensors [blocks, kv heads, block_size, ...], alike")
+        nb, hkv, bs = arrays[0].shape[:3]
+        ptrs = (ctypes.c_void_p * len(arrays))(*[t.data_ptr() for t in arrays])
+        sizes = (ctypes.c_int64 * len(arrays))(*[t.shape[3] * t.element_size() for t in arrays])
+        _need_on(paths.device, cu_seqlens_q, seq_slot, context_lens, block_tables, *arrays, device_status)
+        self._bind("pkv_accept_rows",
+                   (_t_ptr(cu_seqlens_q), segs, 2 ** 31 - 1 if total_q is None else total_q, _t_ptr(seq_slot),
+                    _t_ptr(context_lens), _t_ptr(block_tables), ms, mbps, bs, hkv, _t_ptr(paths), paths.shape[1], ptrs,
+                    sizes, len(arrays), nb, _t_ptr(device_status)),
+                   (cu_seqlens_q, seq_slot, context_lens, block_tables, paths, tuple(arrays), ptrs, sizes, device_status),
+                   paths.device, stream)
+
+
+def pkv_accept_rows(cu_seqlens_q, seq_slot, context_lens, block_tables, paths, arrays, *, total_q: int | None = None,
+                    device_status=None, stream=None) -> None:
+    """Move each segment's accepted rows to its front in every pool array."""
+    AcceptRowsCall(cu_seqlens_q, seq_slot, context_lens, block_tables, paths, arrays, total_q=total_q,
+                   device_status=device_status, stream=stream)()
 
 
 def _need_quant_pool(k_codes, k_scales, v_codes, v_scales, bits: int):

@@ -565,6 +565,200 @@ pkv_status pkv_attention_mod_q4(const void *q, const int32_t *cu_seqlens_q, int3
                          head_dim, scale, work, info, out, workspace, workspace_bytes, device_status, stream, mod);
 }
 
+}  // extern "C"
+
+// Block-sparse steps.
+
+namespace {
+
+// The arguments that the calls over a listed step share, checked and laid out. Returns PKV_OK with `empty` set
+// where there is nothing to do.
+pkv_status list_args(pkv::StepArgs &a, bool &empty, int32_t kind, const void *q, const int32_t *cu_seqlens_q,
+                     int32_t num_seqs, int64_t total_q, const int32_t *seq_slot, const int32_t *context_lens,
+                     const int32_t *block_tables, int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size,
+                     int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                     const int32_t *work, const pkv_work_info *info, uint32_t *device_status) {
+  if (!info || num_seqs < 0 || total_q < 0 || max_slots <= 0 || max_blocks_per_slot <= 0 || num_blocks <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (!supported_shape(block_size, num_q_heads, num_kv_heads, head_dim)) return PKV_ERR_UNSUPPORTED;
+  if (num_kv_heads > 65535 || total_q > INT32_MAX || num_blocks > INT32_MAX / num_kv_heads / block_size)
+    return PKV_ERR_UNSUPPORTED;
+  const int64_t items = static_cast<int64_t>(info->num_decode_items) + info->num_prefill_items +
+                        info->num_combine_items + info->num_scratch_items;
+  if (info->modified != kind || info->num_decode_items < 0 || info->num_prefill_items < 0 ||
+      info->num_combine_items < 0 || info->num_scratch_items < 0 || info->num_partials < 0 ||
+      info->scratch_blocks < 0 || info->num_long_combine_items < 0 ||
+      info->num_long_combine_items > info->num_combine_items ||
+      (info->num_combine_items > 0) != (info->num_partials > 0) ||
+      info->work_words != items * PKV_WORK_WORDS_PER_ITEM || info->decode_rows_max < 0)
+    return PKV_ERR_INVALID_ARG;
+  empty = items == 0 || total_q == 0;
+  if (empty) return PKV_OK;
+  if (!q || !cu_seqlens_q || !seq_slot || !context_lens || !block_tables || !work || !aligned(q, 16) ||
+      !aligned(work, 16))
+    return PKV_ERR_INVALID_ARG;
+  a.q = q;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.seq_slot = seq_slot;
+  a.context_lens = context_lens;
+  a.block_tables = block_tables;
+  a.num_seqs = num_seqs;
+  a.max_slots = max_slots;
+  a.max_blocks_per_slot = max_blocks_per_slot;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.total_q = total_q;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = num_q_heads / num_kv_heads;
+  a.head_dim = head_dim;
+  a.decode_rows_max = info->decode_rows_max;
+  a.modified = kind;
+  a.num_partials = info->num_partials;
+  a.work = work;
+  a.status = device_status;
+  return PKV_OK;
+}
+
+// The output, the scale and the span partials in the workspace.
+pkv_status partial_args(pkv::StepArgs &a, float scale, void *out, void *workspace, uint64_t workspace_bytes) {
+  if (!out || !aligned(out, 16)) return PKV_ERR_INVALID_ARG;
+  const uint64_t need = pkv::partial_bytes(a.num_partials, a.num_q_heads, a.head_dim);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return PKV_ERR_WORKSPACE_TOO_SMALL;
+  const float s = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(a.head_dim));
+  a.scale_log2 = s * 1.4426950408889634f;
+  a.out = out;
+  if (need == 0) return PKV_OK;
+  const uint64_t acc_bytes = align256(uint64_t(a.num_partials) * a.num_q_heads * a.head_dim * 4);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.partial_acc = reinterpret_cast<float *>(ws);
+  a.partial_ml = reinterpret_cast<float *>(ws + acc_bytes);
+  a.task_counter = reinterpret_cast<uint32_t *>(ws + need - pkv::kCounterBytes);
+  return PKV_OK;
+}
+
+pkv_status sparse_args(pkv::StepArgs &a, const pkv_sparse *sparse, const pkv_work_info *info) {
+  if (!sparse || sparse->top_blocks < 1 || sparse->keep_first < 0 || sparse->keep_last < 0 ||
+      (info->num_decode_items > 0 && info->decode_rows_max * a.group > 16))
+    return PKV_ERR_INVALID_ARG;
+  a.top_blocks = sparse->top_blocks;
+  a.keep_first = sparse->keep_first;
+  a.keep_last = sparse->keep_last;
+  return PKV_OK;
+}
+
+// bits 16 (bf16: k and v are the pools), 8 or 4.
+pkv_status attention_sparse(int32_t bits, const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs,
+                            int64_t total_q, const int32_t *seq_slot, const int32_t *context_lens,
+                            const int32_t *block_tables, int32_t max_slots, int32_t max_blocks_per_slot,
+                            int32_t block_size, const void *k, const void *k_scales, const void *v,
+                            const void *v_scales, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                            int32_t head_dim, float scale, const pkv_sparse *sparse, const int32_t *selected,
+                            const int32_t *work, const pkv_work_info *info, void *out, void *workspace,
+                            uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream) {
+  if (bits == 4 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  pkv::StepArgs a{};
+  bool empty = false;
+  if (const pkv_status st = list_args(a, empty, pkv::kListSparse, q, cu_seqlens_q, num_seqs, total_q, seq_slot,
+                                      context_lens, block_tables, max_slots, max_blocks_per_slot, block_size, num_blocks,
+                                      num_q_heads, num_kv_heads, head_dim, work, info, device_status);
+      st != PKV_OK || empty)
+    return st;
+  if (const pkv_status st = sparse_args(a, sparse, info); st != PKV_OK) return st;
+  if (!k || !v || !selected || !aligned(k, 16) || !aligned(v, 16) || !aligned(selected, 4) ||
+      (bits != 16 && (!k_scales || !v_scales || !aligned(k_scales, 16) || !aligned(v_scales, 16))))
+    return PKV_ERR_INVALID_ARG;
+  if (const pkv_status st = partial_args(a, scale, out, workspace, workspace_bytes); st != PKV_OK) return st;
+  a.k_pool = k;
+  a.v_pool = v;
+  a.selected = selected;
+  const int64_t rows = num_blocks * num_kv_heads * block_size;
+  CUtensorMap tk, tv;
+  const bool encoded = bits != 16        ? encode_codes(&tk, k, rows, head_dim, bits) && encode_codes(&tv, v, rows, head_dim, bits)
+                       : head_dim == 128 ? encode_pool_subtiles(&tk, k, num_blocks * num_kv_heads, block_size) &&
+                                               encode_pool_subtiles(&tv, v, num_blocks * num_kv_heads, block_size)
+                                         : encode_pool(&tk, k, rows, head_dim) && encode_pool(&tv, v, rows, head_dim);
+  if (!encoded) return PKV_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int32_t *comb = work + (static_cast<int64_t>(info->num_decode_items) + info->num_prefill_items) *
+                                   PKV_WORK_WORDS_PER_ITEM;
+  cudaError_t e = bits == 16 ? pkv::launch_decode(a, tk, tv, info->num_decode_items, work, false, st)
+                             : pkv::launch_decode_quant(a, tk, tv, k_scales, v_scales, info->num_decode_items, work, bits, st);
+  if (e == cudaSuccess) e = pkv::launch_merge(a, info->num_combine_items, info->num_long_combine_items, comb, st);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_select_blocks(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                             const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                             int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size, const void *bounds,
+                             int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                             const pkv_sparse *sparse, const int32_t *work, const pkv_work_info *info,
+                             int32_t *selected, void *workspace, uint64_t workspace_bytes, uint32_t *device_status,
+                             pkv_stream_t stream) {
+  pkv::StepArgs a{};
+  bool empty = false;
+  if (const pkv_status st = list_args(a, empty, pkv::kListSparse, q, cu_seqlens_q, num_seqs, total_q, seq_slot,
+                                      context_lens, block_tables, max_slots, max_blocks_per_slot, block_size, num_blocks,
+                                      num_q_heads, num_kv_heads, head_dim, work, info, device_status);
+      st != PKV_OK || empty)
+    return st;
+  if (const pkv_status st = sparse_args(a, sparse, info); st != PKV_OK) return st;
+  if (!bounds || !selected || !aligned(bounds, 16) || !aligned(selected, 4) ||
+      (info->scratch_blocks > 0) != (info->num_scratch_items > 0))
+    return PKV_ERR_INVALID_ARG;
+  const uint64_t need = pkv::select_layout(info->scratch_blocks, info->num_scratch_items, num_kv_heads).bytes;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return PKV_ERR_WORKSPACE_TOO_SMALL;
+  const cudaError_t e = pkv::launch_select_blocks(a, bounds, *info, workspace, selected, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_attention_sparse(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                                const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                                int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size, const void *k_pool,
+                                const void *v_pool, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float scale, const pkv_sparse *sparse, const int32_t *selected,
+                                const int32_t *work, const pkv_work_info *info, void *out, void *workspace,
+                                uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream) {
+  return attention_sparse(16, q, cu_seqlens_q, num_seqs, total_q, seq_slot, context_lens, block_tables, max_slots,
+                          max_blocks_per_slot, block_size, k_pool, nullptr, v_pool, nullptr, num_blocks, num_q_heads,
+                          num_kv_heads, head_dim, scale, sparse, selected, work, info, out, workspace, workspace_bytes,
+                          device_status, stream);
+}
+
+pkv_status pkv_attention_sparse_q8(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                                   const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                                   int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size,
+                                   const int8_t *k_codes, const void *k_scales, const int8_t *v_codes,
+                                   const void *v_scales, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, float scale, const pkv_sparse *sparse, const int32_t *selected,
+                                   const int32_t *work, const pkv_work_info *info, void *out, void *workspace,
+                                   uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream) {
+  return attention_sparse(8, q, cu_seqlens_q, num_seqs, total_q, seq_slot, context_lens, block_tables, max_slots,
+                          max_blocks_per_slot, block_size, k_codes, k_scales, v_codes, v_scales, num_blocks,
+                          num_q_heads, num_kv_heads, head_dim, scale, sparse, selected, work, info, out, workspace,
+                          workspace_bytes, device_status, stream);
+}
+
+pkv_status pkv_attention_sparse_q4(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                                   const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                                   int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size,
+                                   const uint8_t *k_codes, const void *k_scales, const uint8_t *v_codes,
+                                   const void *v_scales, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, float scale, const pkv_sparse *sparse, const int32_t *selected,
+                                   const int32_t *work, const pkv_work_info *info, void *out, void *workspace,
+                                   uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream) {
+  return attention_sparse(4, q, cu_seqlens_q, num_seqs, total_q, seq_slot, context_lens, block_tables, max_slots,
+                          max_blocks_per_slot, block_size, k_codes, k_scales, v_codes, v_scales, num_blocks,
+                          num_q_heads, num_kv_heads, head_dim, scale, sparse, selected, work, info, out, workspace,
+                          workspace_bytes, device_status, stream);
+}
+
 pkv_status pkv_check_device_status(uint32_t *device_status, pkv_stream_t stream, uint32_t *bits_out) {
   if (!device_status) return PKV_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

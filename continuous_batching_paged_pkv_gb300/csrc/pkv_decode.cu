@@ -118,19 +118,20 @@ constexpr int kDecodeRegs = NW == kDecodeWarpsBesideChunk && NS == kDecodeStages
 // NW, NS: warps per CTA and stages per warp ring. A warp's stream of
 // sub-tiles is latency-bound (its ring's bytes per HBM round trip), so steps
 // with fewer tasks than warps run fewer warps with deeper rings; the math of
-// a task does not depend on them. MOD: modified scores (see above).
-template <int D, int NT, bool MULTI, bool MOD, int NW, int NS>
+// a task does not depend on them. LIST: the planner of the work list (see above).
+template <int D, int NT, bool MULTI, int LIST, int NW, int NS>
 __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const StepArgs a, const int32_t *__restrict__ items, int num_items) {
   using Cfg = DecodeCfg<D, NW, NS>;
+  constexpr bool MOD = LIST == kListMod, kListed = LIST != kListPlain;
   constexpr int KT = D / 16;  // k-steps of QK^T, m-tiles of PV
   constexpr int NST = Cfg::kStages;
   constexpr int kMaxRows = MULTI ? 16 : 1;
-  // Modified scores at head_dim 128: a sub-tile of K or V is one 4 KiB box (as the
+  // Listed sub-tiles at head_dim 128: a sub-tile of K or V is one 4 KiB box (as the
   // chunk kernel loads K), [8-key group][half][8 keys][128 B], two TMA instructions
   // a stage instead of four.
-  constexpr bool kWholeBoxes = MOD && D == 128;
+  constexpr bool kWholeBoxes = kListed && D == 128;
   constexpr int kHalfStep = kWholeBoxes ? 1024 : Cfg::kHalfBytes;  // from one 64-column half to the other
   const int block_shift = 31 - __clz(a.block_size);                // block sizes are powers of two
   extern __shared__ uint8_t smem_raw[];
@@ -167,17 +168,18 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
   // counter) 3 stride + the counter's next value, else t0 + 3 stride, ...
   // A is current, B expanded, tC the task whose work item is in rawC.
   uint32_t *const counter = a.task_counter;
+  if constexpr (LIST == kListSparse) wait_once();  // the kernel before may have chosen the blocks
   Task A, B;
   int4 rawC = make_int4(0, 0, 0, 0);
-  expand<MOD>(A, t0, load_item(items, t0, hkv), a, lane);
+  expand<LIST>(A, t0, load_item(items, t0, hkv), a, lane);
   int tC;
   {
     const int t1 = t0 + stride;
-    expand<MOD>(B, t1 < num_tasks ? t1 : -1, t1 < num_tasks ? load_item(items, t1, hkv) : rawC, a, lane);
+    expand<LIST>(B, t1 < num_tasks ? t1 : -1, t1 < num_tasks ? load_item(items, t1, hkv) : rawC, a, lane);
     tC = t1 + stride;
     if (tC < num_tasks) rawC = load_item(items, tC, hkv);
   }
-  finalize<MOD>(A, a, lane, 8 * NT, kMaxRows);
+  finalize<LIST>(A, a, lane, 8 * NT, kMaxRows);
   uint32_t qA[NT][KT][2], qB[NT][KT][2];
   if (A.ok) load_q<D, NT, MULTI>(qA, A, a, lane);
   bool qB_loaded = false;
@@ -221,7 +223,7 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
     }
     if (B.t >= 0) {
       if (!B.finalized) {
-        finalize<MOD>(B, a, lane, 8 * NT, kMaxRows);
+        finalize<LIST>(B, a, lane, 8 * NT, kMaxRows);
         if (B.ok) {
           load_q<D, NT, MULTI>(qB, B, a, lane);
           qB_loaded = true;
@@ -464,7 +466,7 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
             if (col < nrows * G) {
               // partial entry of (span, row i)
               const int i = MULTI ? col / G : 0, hh = MULTI ? col % G : col;
-              const size_t pi = static_cast<size_t>(A.pbase + (MOD ? 0 : A.span * nrows) + i) * a.num_q_heads + hbase;
+              const size_t pi = static_cast<size_t>(A.pbase + (kListed ? 0 : A.span * nrows) + i) * a.num_q_heads + hbase;
               float *pacc = a.partial_acc + (pi + hh) * D + (lane >> 2);
 #pragma unroll
               for (int mt = 0; mt < KT; ++mt) {
@@ -498,7 +500,7 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
     pa = pb;
     pb = 0;
     if (A.t >= 0) {
-      if (!A.finalized) finalize<MOD>(A, a, lane, 8 * NT, kMaxRows);
+      if (!A.finalized) finalize<LIST>(A, a, lane, 8 * NT, kMaxRows);
       if (qB_loaded) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -512,7 +514,7 @@ __global__ void __maxnreg__((kDecodeRegs<NW, NS>))
       }
     }
     qB_loaded = false;
-    expand<MOD>(B, next_t < num_tasks ? next_t : -1, rawC, a, lane);
+    expand<LIST>(B, next_t < num_tasks ? next_t : -1, rawC, a, lane);
     tC = after;
     if (tC < num_tasks) rawC = load_item(items, tC, hkv);
     while (P - C < NST && issue_next()) {
@@ -802,12 +804,12 @@ int sm_count() {
   return count[dev];
 }
 
-template <int D, int NT, bool MULTI, bool MOD, int NW = kWarps, int NS = 0>
+template <int D, int NT, bool MULTI, int LIST, int NW = kWarps, int NS = 0>
 cudaError_t launch_decode_t(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int32_t num_items,
                             const int32_t *items, cudaStream_t stream) {
   constexpr int smem = DecodeCfg<D, NW, NS>::kSmem;
   static std::atomic<uint64_t> configured{0};  // one bit per device
-  if (const cudaError_t e = allow_smem_once(decode_kernel<D, NT, MULTI, MOD, NW, NS>, smem, configured);
+  if (const cudaError_t e = allow_smem_once(decode_kernel<D, NT, MULTI, LIST, NW, NS>, smem, configured);
       e != cudaSuccess)
     return e;
   const int64_t tasks = static_cast<int64_t>(num_items) * a.num_kv_heads;
@@ -821,46 +823,46 @@ cudaError_t launch_decode_t(const StepArgs &a, const CUtensorMap &tk, const CUte
   } else {
     b.task_counter = nullptr;
   }
-  return launch_pdl(decode_kernel<D, NT, MULTI, MOD, NW, NS>, dim3(grid), dim3(NW * 32), smem, stream, tk, tv, b, items,
+  return launch_pdl(decode_kernel<D, NT, MULTI, LIST, NW, NS>, dim3(grid), dim3(NW * 32), smem, stream, tk, tv, b, items,
                     num_items);
 }
 
 // Single-row decode at head_dim 128: with at most 4, 5 or 6 tasks per SM,
 // 4 warps x 6 stages, 5 x 5 or 6 x 4 (192-200 KiB of rings) keep more bytes
 // in flight per busy warp than 8 x 3.
-template <int NT, bool MOD>
+template <int NT, int LIST>
 cudaError_t launch_decode_128(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int32_t num_items,
                               const int32_t *items, cudaStream_t stream) {
   const int64_t tasks = static_cast<int64_t>(num_items) * a.num_kv_heads;
   const int64_t per_sm = (tasks + sm_count() - 1) / sm_count();
-  if (per_sm <= 4) return launch_decode_t<128, NT, false, MOD, 4, 6>(a, tk, tv, num_items, items, stream);
-  if (per_sm == 5) return launch_decode_t<128, NT, false, MOD, 5, 5>(a, tk, tv, num_items, items, stream);
-  if (per_sm == 6) return launch_decode_t<128, NT, false, MOD, 6, 4>(a, tk, tv, num_items, items, stream);
-  return launch_decode_t<128, NT, false, MOD>(a, tk, tv, num_items, items, stream);
+  if (per_sm <= 4) return launch_decode_t<128, NT, false, LIST, 4, 6>(a, tk, tv, num_items, items, stream);
+  if (per_sm == 5) return launch_decode_t<128, NT, false, LIST, 5, 5>(a, tk, tv, num_items, items, stream);
+  if (per_sm == 6) return launch_decode_t<128, NT, false, LIST, 6, 4>(a, tk, tv, num_items, items, stream);
+  return launch_decode_t<128, NT, false, LIST>(a, tk, tv, num_items, items, stream);
 }
 
-template <bool MOD>
+template <int LIST>
 cudaError_t launch_decode_m(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int32_t num_items,
                             const int32_t *items, bool beside_chunk, cudaStream_t stream) {
   // one column per (row, q head) of a segment: 8 columns per tile, 16 at most
   const bool multi = a.decode_rows_max > 1;
   const bool wide = a.group * (multi ? a.decode_rows_max : 1) > 8;
-  if (beside_chunk && a.head_dim == 128 && !wide) {
+  if constexpr (LIST != kListSparse) if (beside_chunk && a.head_dim == 128 && !wide) {
     // one 8-column tile (at most ~208 registers): small enough to share an SM with a chunk CTA
     constexpr int W = kDecodeWarpsBesideChunk, S = kDecodeStagesBesideChunk;
-    return multi ? launch_decode_t<128, 1, true, MOD, W, S>(a, tk, tv, num_items, items, stream)
-                 : launch_decode_t<128, 1, false, MOD, W, S>(a, tk, tv, num_items, items, stream);
+    return multi ? launch_decode_t<128, 1, true, LIST, W, S>(a, tk, tv, num_items, items, stream)
+                 : launch_decode_t<128, 1, false, LIST, W, S>(a, tk, tv, num_items, items, stream);
   }
   const int v = (a.head_dim == 128 ? 4 : 0) + (wide ? 2 : 0) + (multi ? 1 : 0);
   switch (v) {
-    case 0: return launch_decode_t<64, 1, false, MOD>(a, tk, tv, num_items, items, stream);
-    case 1: return launch_decode_t<64, 1, true, MOD>(a, tk, tv, num_items, items, stream);
-    case 2: return launch_decode_t<64, 2, false, MOD>(a, tk, tv, num_items, items, stream);
-    case 3: return launch_decode_t<64, 2, true, MOD>(a, tk, tv, num_items, items, stream);
-    case 4: return launch_decode_128<1, MOD>(a, tk, tv, num_items, items, stream);
-    case 5: return launch_decode_t<128, 1, true, MOD>(a, tk, tv, num_items, items, stream);
-    case 6: return launch_decode_128<2, MOD>(a, tk, tv, num_items, items, stream);
-    default: return launch_decode_t<128, 2, true, MOD>(a, tk, tv, num_items, items, stream);
+    case 0: return launch_decode_t<64, 1, false, LIST>(a, tk, tv, num_items, items, stream);
+    case 1: return launch_decode_t<64, 1, true, LIST>(a, tk, tv, num_items, items, stream);
+    case 2: return launch_decode_t<64, 2, false, LIST>(a, tk, tv, num_items, items, stream);
+    case 3: return launch_decode_t<64, 2, true, LIST>(a, tk, tv, num_items, items, stream);
+    case 4: return launch_decode_128<1, LIST>(a, tk, tv, num_items, items, stream);
+    case 5: return launch_decode_t<128, 1, true, LIST>(a, tk, tv, num_items, items, stream);
+    case 6: return launch_decode_128<2, LIST>(a, tk, tv, num_items, items, stream);
+    default: return launch_decode_t<128, 2, true, LIST>(a, tk, tv, num_items, items, stream);
   }
 }
 
@@ -869,8 +871,11 @@ cudaError_t launch_decode_m(const StepArgs &a, const CUtensorMap &tk, const CUte
 cudaError_t launch_decode(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int32_t num_items,
                           const int32_t *items, bool beside_chunk, cudaStream_t stream) {
   if (num_items <= 0) return cudaSuccess;
-  return a.modified ? launch_decode_m<true>(a, tk, tv, num_items, items, beside_chunk, stream)
-                    : launch_decode_m<false>(a, tk, tv, num_items, items, beside_chunk, stream);
+  switch (a.modified) {
+    case kListMod: return launch_decode_m<kListMod>(a, tk, tv, num_items, items, beside_chunk, stream);
+    case kListSparse: return launch_decode_m<kListSparse>(a, tk, tv, num_items, items, beside_chunk, stream);
+    default: return launch_decode_m<kListPlain>(a, tk, tv, num_items, items, beside_chunk, stream);
+  }
 }
 
 template <int D, bool MOD>

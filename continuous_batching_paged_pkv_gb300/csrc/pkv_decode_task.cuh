@@ -25,7 +25,7 @@ struct Task {
   int row;  // per lane: tensor-map row of sub-tile `lane`, -1 if its block ID is outside the pool
   bool raw_ok, finalized, ok;
   bool reads_new;  // the span reaches this step's rows (written by the kernel before in the stream)
-  // modified scores only
+  // modified scores and block-sparse steps only
   int subs;        // 16-key sub-tiles that the work item names (0: the segment sees nothing)
   int begin, end;  // per lane: key_begin / key_end of row `lane` as given (finalize issues the loads)
 };
@@ -34,9 +34,11 @@ __device__ __forceinline__ int4 load_item(const int32_t *items, int t, int hkv) 
   return __ldg(reinterpret_cast<const int4 *>(items) + t / hkv);
 }
 
-// Issue every load the task needs; nothing here waits for a result. MOD:
-// modified scores, whose items name the sub-tiles of the span that some row sees.
-template <bool MOD = false>
+// Issue every load the task needs; nothing here waits for a result, but that a
+// block-sparse task's blocks are looked up through its list. LIST: the planner
+// of the work list; with modified scores and in block-sparse steps items name the
+// sub-tiles of the span, in the latter those of the segment's list of blocks.
+template <int LIST = kListPlain>
 __device__ __forceinline__ void expand(Task &T, int t, int4 raw, const StepArgs &a, int lane) {
   T.t = t;
   T.finalized = false;
@@ -51,7 +53,8 @@ __device__ __forceinline__ void expand(Task &T, int t, int4 raw, const StepArgs 
   T.span = raw.z;
   T.pbase = raw.w;
   T.g = t % a.num_kv_heads;
-  if constexpr (MOD) {
+  constexpr bool kListed = LIST != kListPlain;
+  if constexpr (kListed) {
     const uint32_t w = static_cast<uint32_t>(raw.z);
     T.span = static_cast<int>(w & 0x7FFFFFu);
     T.key0 = T.span * PKV_SPLIT_KEYS + static_cast<int>((w >> 23) & 15u) * kSubKeys;
@@ -66,35 +69,52 @@ __device__ __forceinline__ void expand(Task &T, int t, int4 raw, const StepArgs 
   T.L = __ldg(a.context_lens + T.slot);
   T.sslot = __ldg(a.seq_slot + T.seg);
   const int64_t key = static_cast<int64_t>(T.key0) + lane * kSubKeys;
-  if ((MOD ? lane < T.subs : lane * kSubKeys < PKV_SPLIT_KEYS) &&
-      key < static_cast<int64_t>(a.max_blocks_per_slot) * a.block_size)
+  if constexpr (LIST == kListSparse) {
+    T.bid = -1;  // a place that is not one of the slot's blocks counts as a block outside the pool
+    const int64_t i = key / a.block_size;
+    if (lane < T.subs && i < a.top_blocks) {
+      const int place = __ldcg(a.selected + (static_cast<int64_t>(T.seg) * a.num_kv_heads + T.g) * a.top_blocks + i);
+      if (place >= 0 && place < a.max_blocks_per_slot && static_cast<int64_t>(place) * a.block_size < T.L)
+        T.bid = __ldg(a.block_tables + static_cast<int64_t>(T.slot) * a.max_blocks_per_slot + place);
+    }
+  } else if ((kListed ? lane < T.subs : lane * kSubKeys < PKV_SPLIT_KEYS) &&
+             key < static_cast<int64_t>(a.max_blocks_per_slot) * a.block_size) {
     T.bid = __ldg(a.block_tables + static_cast<int64_t>(T.slot) * a.max_blocks_per_slot + key / a.block_size);
+  }
 }
 
 // Check the metadata against the work item and derive the key range.
-template <bool MOD = false>
+template <int LIST = kListPlain>
 __device__ __forceinline__ void finalize(Task &T, const StepArgs &a, int lane, int max_cols, int max_rows) {
   if (T.finalized) return;
   T.finalized = true;
   if (T.t < 0) return;
+  constexpr bool MOD = LIST == kListMod, kListed = LIST != kListPlain;
   T.nrows = T.row1 - T.row0;
   T.ok = T.raw_ok && T.sslot == T.slot && T.nrows >= 1 && T.nrows <= max_rows && T.nrows * a.group <= max_cols && T.nrows <= T.L &&
          T.L >= 1 &&
          static_cast<int64_t>(T.L) <= static_cast<int64_t>(a.max_blocks_per_slot) * a.block_size &&
          (T.key0 < T.L || (MOD && T.subs == 0)) && T.row0 >= 0 &&
          static_cast<int64_t>(T.row0) + T.nrows <= a.total_q;
-  if constexpr (MOD)  // at most a span's sub-tiles, and the partials inside the workspace
+  if constexpr (LIST == kListSparse) {  // from here on the context is the listed blocks' keys, the rows their last
+    const int blocks = (T.L + a.block_size - 1) / a.block_size;
+    T.L -= max(0, blocks - a.top_blocks) * a.block_size;
+    T.ok = T.ok && T.nrows <= T.L && T.key0 < T.L && T.subs > 0;
+  }
+  if constexpr (kListed)  // at most a span's sub-tiles, and the partials inside the workspace
     T.ok = T.ok && T.subs <= PKV_SPLIT_KEYS / kSubKeys && (T.pbase < 0 || T.pbase <= a.num_partials - T.nrows);
   if (!T.ok) {
     if (lane == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
     return;
   }
-  if constexpr (MOD) {
+  if constexpr (kListed) {
     T.key1 = T.subs == 0 ? T.key0 : T.key0 + min(T.L - T.key0, T.subs * kSubKeys);
-    T.begin = lane < T.nrows && a.key_begin ? __ldg(a.key_begin + T.row0 + lane) : 0;
-    T.end = lane < T.nrows && a.key_end ? __ldg(a.key_end + T.row0 + lane) : INT32_MAX;
   } else {
     T.key1 = min(T.L, T.key0 + PKV_SPLIT_KEYS);
+  }
+  if constexpr (MOD) {
+    T.begin = lane < T.nrows && a.key_begin ? __ldg(a.key_begin + T.row0 + lane) : 0;
+    T.end = lane < T.nrows && a.key_end ? __ldg(a.key_end + T.row0 + lane) : INT32_MAX;
   }
   T.units = (T.key1 - T.key0 + kSubKeys - 1) / kSubKeys;
   T.reads_new = T.key1 > T.L - T.nrows;

@@ -185,6 +185,26 @@ pkv_status pkv_pool_release(pkv_pool *p, int32_t slot) {
   return PKV_OK;
 }
 
+pkv_status pkv_pool_truncate(pkv_pool *p, int32_t slot, int64_t num_tokens) {
+  if (!p) return PKV_ERR_INVALID_ARG;
+  if (slot < 0 || slot >= p->max_slots) return PKV_ERR_OUT_OF_RANGE;
+  pkv_pool::Slot &s = p->slots[slot];
+  if (!s.live || num_tokens < 0 || num_tokens > s.length) return PKV_ERR_INVALID_ARG;
+  s.length = num_tokens;
+  // Appending copies a shared block only where it begins (pkv_plan_lower): whole blocks behind the cut that
+  // another table holds too are given up, and with them what stands behind.
+  size_t keep = static_cast<size_t>(ceil_div(num_tokens, p->block_size));
+  while (keep < s.blocks.size() && p->refs[s.blocks[keep]] == 1) ++keep;
+  while (s.blocks.size() > keep) {
+    const int32_t b = s.blocks.back();
+    s.blocks.pop_back();
+    if (--p->refs[b] > 0) continue;
+    p->free_stack.push_back(b);
+    p->on_free[b] = 1;
+  }
+  return PKV_OK;
+}
+
 pkv_status pkv_pool_adopt(pkv_pool *p, int32_t slot, int32_t donor_slot, int64_t num_tokens,
                           int64_t reserve_tokens) {
   if (!p || num_tokens < 0 || reserve_tokens < 0) return PKV_ERR_INVALID_ARG;
@@ -341,6 +361,23 @@ pkv_status pkv_plan_lower(pkv_pool *p, const pkv_segment *plan, int32_t num_segm
 
 }  // extern "C"
 
+// Keys per span of a segment whose rows see `keys` keys, with modified scores: 64
+// or 128 instead of PKV_SPLIT_KEYS while a step with all slots so long would still
+// have a warp of its own for each of its tasks (eight on each of 152 SMs), since a
+// warp takes its sub-tiles one after the other; but no more than 64 spans, whose
+// merge then costs more than they save. It depends on the segment and the tables'
+// shape, not on the rest of the step. Measured with spans of 64 / 128 / 256 keys:
+// five slots of 1024 keys, 8 kv heads: 10.0 / 11.1 / 15.4 us; one of 1000: 8.3 /
+// 10.4 / 14.7; one of 8000 (126 spans of 64): 16.8 / 13.8 / 15.5; sixteen of 2000
+// stay at 256: 25.7 (26.6 with 64).
+int32_t pkv::span_keys(int64_t keys, int32_t max_slots, int32_t num_kv_heads) {
+  for (int32_t s = 64; s < PKV_SPLIT_KEYS; s *= 2) {
+    const int64_t spans = ceil_div(keys, s);
+    if (spans <= pkv::kLongMergeSpans && spans * max_slots * num_kv_heads <= 8 * 152) return s;
+  }
+  return PKV_SPLIT_KEYS;
+}
+
 namespace {
 
 constexpr int64_t kSubsPerSpan = PKV_SPLIT_KEYS / pkv::kSubKeys;
@@ -364,23 +401,6 @@ KeyRange rows_see(const pkv_score_mod *mod, int64_t row0, int64_t first, int64_t
   }
   if (u.lo >= u.hi) u = {0, 0};
   return u;
-}
-
-// Keys per span of a segment whose rows see `keys` keys, with modified scores: 64
-// or 128 instead of PKV_SPLIT_KEYS while a step with all slots so long would still
-// have a warp of its own for each of its tasks (eight on each of 152 SMs), since a
-// warp takes its sub-tiles one after the other; but no more than 64 spans, whose
-// merge then costs more than they save. It depends on the segment and the tables'
-// shape, not on the rest of the step. Measured with spans of 64 / 128 / 256 keys:
-// five slots of 1024 keys, 8 kv heads: 10.0 / 11.1 / 15.4 us; one of 1000: 8.3 /
-// 10.4 / 14.7; one of 8000 (126 spans of 64): 16.8 / 13.8 / 15.5; sixteen of 2000
-// stay at 256: 25.7 (26.6 with 64).
-int32_t span_keys(int64_t keys, int32_t max_slots, int32_t num_kv_heads) {
-  for (int32_t s = 64; s < PKV_SPLIT_KEYS; s *= 2) {
-    const int64_t spans = ceil_div(keys, s);
-    if (spans <= pkv::kLongMergeSpans && spans * max_slots * num_kv_heads <= 8 * 152) return s;
-  }
-  return PKV_SPLIT_KEYS;
 }
 
 // The work list of a step: of pkv_plan_work without `mod`, of pkv_plan_work_mod with it.
@@ -449,7 +469,7 @@ pkv_status plan_work(const int32_t *cu, int32_t num_seqs, const int32_t *seq_slo
         // starts under the one before (only its merge then shows); behind another kind
         // of kernel 9.7 and 8.8 us. Up to sixteen sub-tiles the one measure would gain
         // 3.3 us and the other lose 5.4.
-        const int32_t sk = span_keys(u.hi - u.lo, max_slots, num_kv_heads);
+        const int32_t sk = pkv::span_keys(u.hi - u.lo, max_slots, num_kv_heads);
         const int64_t subs = ceil_div(u.hi, pkv::kSubKeys) - u.lo / pkv::kSubKeys;
         const bool whole = subs <= (sk == PKV_SPLIT_KEYS ? kSubsPerSpan : kSubsPerSpan / 2);
         const int64_t sp0 = whole ? 0 : u.lo / sk, sp1 = whole ? 0 : (u.hi - 1) / sk;

@@ -55,7 +55,16 @@ struct StepArgs {
   const float *alibi_slopes;
   const int32_t *key_begin, *key_end;
   int32_t num_partials;  // span partials in the workspace: a modified list's items must stay among them
+  // Block-sparse steps: int32 [num_seqs][Hkv][top_blocks], the places of the blocks that a segment reads.
+  const int32_t *selected;
+  int32_t top_blocks, keep_first, keep_last;
+  // Trees: uint32 [total_q][mask_words], the step's rows that a row sees.
+  const uint32_t *masks;
+  int32_t mask_words;
 };
+
+// pkv_work_info::modified: which planner made a list, and StepArgs::modified.
+constexpr int32_t kListPlain = 0, kListMod = 1, kListSparse = 2, kListTree = 3;
 
 // pkv_attention with the output's location: out_on_host marks `out` as host
 // memory (pkv_step's output written straight to the caller's host buffer).
@@ -68,12 +77,56 @@ pkv_status attention(const void *q, const int32_t *cu_seqlens_q, int32_t num_seq
                      void *workspace, uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream,
                      bool out_on_host, const pkv_score_mod *mod = nullptr);
 
+// Keys per decode span of a segment whose rows read `keys` keys, in the lists of listed sub-tiles (pkv_host.cpp).
+int32_t span_keys(int64_t keys, int32_t max_slots, int32_t num_kv_heads);
+
 // Rows of more spans than this are merged with four lanes per column.
 constexpr int kLongMergeSpans = 64;
 
 // Bytes of workspace after the span partials: the decode kernel's task counter.
 constexpr uint64_t kCounterBytes = 256;
 
+// Candidate blocks that one CTA of the selection scores.
+constexpr int kScoreBlocks = 128;
+
+// Workspace of pkv_select_blocks: scores (fp32) and exact scores (fp64) of every (candidate, kv head), and per
+// (scoring item, kv head) the largest sum of magnitudes. Offsets in bytes.
+struct SelectLayout {
+  uint64_t exact, scores, sums, bytes;
+};
+inline SelectLayout select_layout(int64_t candidates, int64_t score_items, int32_t num_kv_heads) {
+  auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
+  SelectLayout l;
+  l.exact = 0;
+  l.scores = up(static_cast<uint64_t>(candidates) * num_kv_heads * 8);
+  l.sums = l.scores + up(static_cast<uint64_t>(candidates) * num_kv_heads * 4);
+  l.bytes = l.sums + up(static_cast<uint64_t>(score_items) * num_kv_heads * 4);
+  return candidates == 0 ? SelectLayout{0, 0, 0, 0} : l;
+}
+
+// Blocks of a slot of L keys, n of them this step's rows, in a block-sparse step: all of them, the candidates
+// [first, last), and how many are read. Everything else is always kept.
+struct SparseBlocks {
+  int64_t blocks, first, last, read;
+};
+inline __host__ __device__ SparseBlocks sparse_blocks(int64_t L, int64_t n, int32_t block_size, int32_t top,
+                                                      int32_t keep_first, int32_t keep_last) {
+  SparseBlocks b;
+  b.blocks = (L + block_size - 1) / block_size;
+  b.last = (L - n) / block_size - keep_last;
+  if (b.last < 0) b.last = 0;
+  b.first = keep_first < b.last ? keep_first : b.last;
+  b.read = top < b.blocks ? top : b.blocks;
+  return b;
+}
+
+// Workspace of the span partials: sums, (max, denominator) pairs, the task counter.
+inline uint64_t partial_bytes(int64_t partials, int32_t num_q_heads, int32_t head_dim) {
+  auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
+  return partials == 0 ? 0
+                       : up(static_cast<uint64_t>(partials) * num_q_heads * head_dim * 4) +
+                             up(static_cast<uint64_t>(partials) * num_q_heads * 2 * 4) + kCounterBytes;
+}
 cudaError_t launch_cache_write(const void *k_new, const void *v_new, const int64_t *slot_mapping,
                                int64_t num_tokens, void *k_pool, void *v_pool, int64_t num_blocks,
                                int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
@@ -98,6 +151,26 @@ cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const int32_t *pairs, int64_t num_pairs, void *const *arrays,
                                const int64_t *block_bytes, int32_t num_arrays, int64_t num_blocks, uint32_t *status,
                                cudaStream_t stream);
+
+// Bounds of the blocks that a step touched (pkv_key_bounds.cu); bits 16 (bf16 pool, no scales), 8 or 4.
+cudaError_t launch_key_bounds(const int64_t *slot_mapping, int64_t num_tokens, const void *keys, const void *scales,
+                              void *bounds, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t bits, uint32_t *status, cudaStream_t stream);
+
+// Selection of a block-sparse step's blocks (pkv_select.cu); `workspace` laid out by select_layout.
+cudaError_t launch_select_blocks(const StepArgs &a, const void *bounds, const pkv_work_info &info, void *workspace,
+                                 int32_t *selected, cudaStream_t stream);
+
+// Rows of accepted paths (pkv_accept.cu).
+struct AcceptArgs {
+  const int32_t *cu_seqlens_q, *seq_slot, *context_lens, *block_tables, *paths;
+  uint8_t *arrays[4];
+  int64_t row_bytes[4];
+  int64_t total_q, num_blocks;
+  int32_t num_seqs, max_slots, max_blocks_per_slot, block_size, num_kv_heads, max_path, num_arrays;
+  uint32_t *status;
+};
+cudaError_t launch_accept_rows(const AcceptArgs &a, cudaStream_t stream);
 
 // `beside_chunk`: the chunk kernel of the same step runs at the same time
 // (head_dim 128 takes the small per-SM footprint described below).
@@ -193,5 +266,13 @@ cudaError_t allow_smem_once(Kernel *kernel, int smem, std::atomic<uint64_t> &don
 
 // Positions per prefill tile: whole GQA groups fit one 128-row MMA tile.
 inline int32_t prefill_rows_per_tile(int32_t group) { return 128 / group; }
+
+// Trees (pkv_tree.cu): keys come in tiles of 128; a CTA takes two query tiles where some segment of the step has
+// more than one, else one. Spans of kTreeMinSpanTiles to kTreeSpanTiles tiles.
+constexpr int kTreeTileKeys = 128, kTreeMinSpanTiles = 2, kTreeSpanTiles = 32;
+inline int32_t tree_tiles_per_cta(int32_t rows_max, int32_t group) {
+  return rows_max > prefill_rows_per_tile(group) ? 2 : 1;
+}
+int64_t tree_span_tiles(int64_t tiles, int32_t q_tiles, int32_t max_slots, int32_t num_kv_heads);
 
 }  // namespace pkv

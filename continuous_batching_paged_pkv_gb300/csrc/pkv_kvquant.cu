@@ -402,7 +402,7 @@ __device__ __forceinline__ void key_offsets(float (&kinit)[D / 32][NT][4], const
     }
 }
 
-template <int D, int NT, bool MULTI, bool MOD, int NW, int BITS>
+template <int D, int NT, bool MULTI, int LIST, int NW, int BITS>
 __global__ void __launch_bounds__(NW * 32, 1)
     decode_quant_kernel(const __grid_constant__ CUtensorMap tmap_kc, const __grid_constant__ CUtensorMap tmap_vc,
                      const StepArgs a, const __nv_bfloat16 *__restrict__ k_scales,
@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   constexpr int NG2 = NG / 2;  // words of packed bf16 scales per key
   constexpr int NST = Cfg::kStages;
   constexpr int kMaxRows = MULTI ? 16 : 1;
+  constexpr bool MOD = LIST == kListMod, kListed = LIST != kListPlain;
   constexpr float kHeadroom = 7.f;  // log2 of the factor that lifts P' towards fp16's top
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -445,17 +446,18 @@ __global__ void __launch_bounds__(NW * 32, 1)
   // task counter) 3 stride + the counter's next value. A current, B
   // expanded, tC the task whose work item is in rawC.
   uint32_t *const counter = a.task_counter;
+  if constexpr (LIST == kListSparse) wait_once();  // the kernel before may have chosen the blocks
   Task A, B;
   int4 rawC = make_int4(0, 0, 0, 0);
-  expand<MOD>(A, t0, load_item(items, t0, hkv), a, lane);
+  expand<LIST>(A, t0, load_item(items, t0, hkv), a, lane);
   int tC;
   {
     const int t1 = t0 + stride;
-    expand<MOD>(B, t1 < num_tasks ? t1 : -1, t1 < num_tasks ? load_item(items, t1, hkv) : rawC, a, lane);
+    expand<LIST>(B, t1 < num_tasks ? t1 : -1, t1 < num_tasks ? load_item(items, t1, hkv) : rawC, a, lane);
     tC = t1 + stride;
     if (tC < num_tasks) rawC = load_item(items, tC, hkv);
   }
-  finalize<MOD>(A, a, lane, 8 * NT, kMaxRows);
+  finalize<LIST>(A, a, lane, 8 * NT, kMaxRows);
   uint32_t qA[NT][KT][2];
   float invA[NT];
   if (A.ok) load_q_quant<D, NT, MULTI, BITS>(qA, invA, A, a, lane);
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
     if (B.t >= 0) {
       if (!B.finalized) {
-        finalize<MOD>(B, a, lane, 8 * NT, kMaxRows);
+        finalize<LIST>(B, a, lane, 8 * NT, kMaxRows);
         if (B.ok) prefetch_q<D, NT, MULTI>(B, a, lane);  // loaded when B becomes current
       }
       if (pb < B.units) {
@@ -876,7 +878,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             } else {
               // span partials in the merge's units: sums of p dv code and of p
               constexpr float kDown = 1.f / 128.f;
-              const size_t pi = (static_cast<size_t>(A.pbase + (MOD ? 0 : A.span * nrows) + i) * a.num_q_heads + hbase + hh);
+              const size_t pi = (static_cast<size_t>(A.pbase + (kListed ? 0 : A.span * nrows) + i) * a.num_q_heads + hbase + hh);
               float *pacc = a.partial_acc + pi * D + 4 * r;
 #pragma unroll
               for (int g = 0; g < NG; ++g)
@@ -908,10 +910,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
     pa = pb;
     pb = 0;
     if (A.t >= 0) {
-      if (!A.finalized) finalize<MOD>(A, a, lane, 8 * NT, kMaxRows);
+      if (!A.finalized) finalize<LIST>(A, a, lane, 8 * NT, kMaxRows);
       if (A.ok) load_q_quant<D, NT, MULTI, BITS>(qA, invA, A, a, lane);
     }
-    expand<MOD>(B, next_t < num_tasks ? next_t : -1, rawC, a, lane);
+    expand<LIST>(B, next_t < num_tasks ? next_t : -1, rawC, a, lane);
     tC = after;
     if (tC < num_tasks) rawC = load_item(items, tC, hkv);
     while (P - C < NST && issue_next()) {
@@ -921,13 +923,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
   wait_once();
 }
 
-template <int D, int NT, bool MULTI, bool MOD, int NW, int BITS>
+template <int D, int NT, bool MULTI, int LIST, int NW, int BITS>
 cudaError_t launch_decode_quant_w(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv,
                                const void *k_scales, const void *v_scales, int32_t num_items, const int32_t *items,
                                int grid, cudaStream_t stream) {
   constexpr int smem = QuantCfg<D, NW, BITS>::kSmem;
   static std::atomic<uint64_t> configured{0};  // one bit per device
-  if (const cudaError_t e = allow_smem_once(decode_quant_kernel<D, NT, MULTI, MOD, NW, BITS>, smem, configured);
+  if (const cudaError_t e = allow_smem_once(decode_quant_kernel<D, NT, MULTI, LIST, NW, BITS>, smem, configured);
       e != cudaSuccess)
     return e;
   const int64_t tasks = static_cast<int64_t>(num_items) * a.num_kv_heads;
@@ -938,7 +940,7 @@ cudaError_t launch_decode_quant_w(const StepArgs &a, const CUtensorMap &tk, cons
   } else {
     b.task_counter = nullptr;
   }
-  return launch_pdl(decode_quant_kernel<D, NT, MULTI, MOD, NW, BITS>, dim3(grid), dim3(NW * 32), smem, stream, tk, tv, b,
+  return launch_pdl(decode_quant_kernel<D, NT, MULTI, LIST, NW, BITS>, dim3(grid), dim3(NW * 32), smem, stream, tk, tv, b,
                     static_cast<const __nv_bfloat16 *>(k_scales), static_cast<const __nv_bfloat16 *>(v_scales),
                     items, num_items);
 }
@@ -948,7 +950,7 @@ cudaError_t launch_decode_quant_w(const StepArgs &a, const CUtensorMap &tk, cons
 // tasks run 12 warps instead: the code conversions make a warp's sub-tile a
 // long dependent chain, and more warps per scheduler hide it once every warp
 // has work (a small step's few busy warps stream faster through deeper rings).
-template <int D, int NT, bool MULTI, bool MOD, int BITS>
+template <int D, int NT, bool MULTI, int LIST, int BITS>
 cudaError_t launch_decode_quant_t(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv,
                                const void *k_scales, const void *v_scales, int32_t num_items, const int32_t *items,
                                cudaStream_t stream) {
@@ -959,10 +961,10 @@ cudaError_t launch_decode_quant_t(const StepArgs &a, const CUtensorMap &tk, cons
   const int grid = static_cast<int>(tasks < sms ? tasks : sms);
   if constexpr (D == 128 && NT == 1 && !MULTI) {
     if (tasks > 3ll * grid * 12)
-      return launch_decode_quant_w<D, NT, MULTI, MOD, 12, BITS>(a, tk, tv, k_scales, v_scales, num_items, items, grid,
+      return launch_decode_quant_w<D, NT, MULTI, LIST, 12, BITS>(a, tk, tv, k_scales, v_scales, num_items, items, grid,
                                                          stream);
   }
-  return launch_decode_quant_w<D, NT, MULTI, MOD, kWarpsQuant, BITS>(a, tk, tv, k_scales, v_scales, num_items, items, grid,
+  return launch_decode_quant_w<D, NT, MULTI, LIST, kWarpsQuant, BITS>(a, tk, tv, k_scales, v_scales, num_items, items, grid,
                                                            stream);
 }
 
@@ -1014,7 +1016,7 @@ cudaError_t launch_widen_quant(const StepArgs &a, const void *k_codes, const voi
   return launch_pdl(kernel, grid, dim3(256), 0, stream, a, items, kc, ksc, vc, vsc, ko, vo, scratch_table, scratch_blocks);
 }
 
-template <bool MOD>
+template <int LIST>
 static cudaError_t launch_decode_quant_m(const StepArgs &a, const CUtensorMap &tk, const CUtensorMap &tv,
                                          const void *k_scales, const void *v_scales, int32_t num_items,
                                          const int32_t *items, int32_t bits, cudaStream_t stream) {
@@ -1023,21 +1025,21 @@ static cudaError_t launch_decode_quant_m(const StepArgs &a, const CUtensorMap &t
   const int v = (wide ? 2 : 0) + (multi ? 1 : 0);
   if (bits == 4) {  // head_dim 128 only
     switch (v) {
-      case 0: return launch_decode_quant_t<128, 1, false, MOD, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-      case 1: return launch_decode_quant_t<128, 1, true, MOD, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-      case 2: return launch_decode_quant_t<128, 2, false, MOD, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-      default: return launch_decode_quant_t<128, 2, true, MOD, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+      case 0: return launch_decode_quant_t<128, 1, false, LIST, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+      case 1: return launch_decode_quant_t<128, 1, true, LIST, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+      case 2: return launch_decode_quant_t<128, 2, false, LIST, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+      default: return launch_decode_quant_t<128, 2, true, LIST, 4>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
     }
   }
   switch (v + (a.head_dim == 128 ? 4 : 0)) {
-    case 0: return launch_decode_quant_t<64, 1, false, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 1: return launch_decode_quant_t<64, 1, true, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 2: return launch_decode_quant_t<64, 2, false, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 3: return launch_decode_quant_t<64, 2, true, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 4: return launch_decode_quant_t<128, 1, false, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 5: return launch_decode_quant_t<128, 1, true, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    case 6: return launch_decode_quant_t<128, 2, false, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
-    default: return launch_decode_quant_t<128, 2, true, MOD, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 0: return launch_decode_quant_t<64, 1, false, LIST, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 1: return launch_decode_quant_t<64, 1, true, LIST, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 2: return launch_decode_quant_t<64, 2, false, LIST, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 3: return launch_decode_quant_t<64, 2, true, LIST, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 4: return launch_decode_quant_t<128, 1, false, LIST, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 5: return launch_decode_quant_t<128, 1, true, LIST, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    case 6: return launch_decode_quant_t<128, 2, false, LIST, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
+    default: return launch_decode_quant_t<128, 2, true, LIST, 8>(a, tk, tv, k_scales, v_scales, num_items, items, stream);
   }
 }
 
@@ -1045,8 +1047,12 @@ cudaError_t launch_decode_quant(const StepArgs &a, const CUtensorMap &tk, const 
                              const void *v_scales, int32_t num_items, const int32_t *items, int32_t bits,
                              cudaStream_t stream) {
   if (num_items <= 0) return cudaSuccess;
-  return a.modified ? launch_decode_quant_m<true>(a, tk, tv, k_scales, v_scales, num_items, items, bits, stream)
-                    : launch_decode_quant_m<false>(a, tk, tv, k_scales, v_scales, num_items, items, bits, stream);
+  switch (a.modified) {
+    case kListMod: return launch_decode_quant_m<kListMod>(a, tk, tv, k_scales, v_scales, num_items, items, bits, stream);
+    case kListSparse:
+      return launch_decode_quant_m<kListSparse>(a, tk, tv, k_scales, v_scales, num_items, items, bits, stream);
+    default: return launch_decode_quant_m<kListPlain>(a, tk, tv, k_scales, v_scales, num_items, items, bits, stream);
+  }
 }
 
 }  // namespace pkv

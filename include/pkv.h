@@ -158,6 +158,16 @@ pkv_status pkv_pool_release(pkv_pool *pool, int32_t slot);
 pkv_status pkv_pool_adopt(pkv_pool *pool, int32_t slot, int32_t donor_slot, int64_t num_tokens,
                           int64_t reserve_tokens);
 
+/*
+ * Cut live slot `slot` to its first `num_tokens` tokens (at most its length): the
+ * rest -- rejected drafts -- is overwritten by the next rows. Its blocks stay in
+ * its table, as reserved ones do; but from the first whole block behind the cut
+ * on that another table holds too, they are given back, the first of them on top.
+ * Errors: PKV_ERR_OUT_OF_RANGE (bad slot), PKV_ERR_INVALID_ARG (slot not live,
+ * num_tokens negative or beyond its length).
+ */
+pkv_status pkv_pool_truncate(pkv_pool *pool, int32_t slot, int64_t num_tokens);
+
 /* Tables currently holding `block` (0 if free), or -1 for a bad block ID. */
 int32_t pkv_pool_block_refs(const pkv_pool *pool, int32_t block);
 
@@ -261,7 +271,7 @@ typedef struct pkv_work_info {
     int64_t scratch_blocks;    /* bf16 scratch blocks those items widen the chunks' histories into */
     uint64_t workspace_bytes_q8; /* device workspace pkv_attention_q8 needs (may be 0) */
     int32_t num_long_combine_items; /* the first merge items, whose rows have more than 64 spans */
-    int32_t modified;               /* 1: a list of pkv_plan_work_mod, for pkv_attention_mod and its kin alone */
+    int32_t modified;               /* the planner, and so the calls that take the list: 0 pkv_plan_work, 1 _mod, 2 _sparse, 3 _tree */
 } pkv_work_info;
 
 /*
@@ -683,6 +693,195 @@ pkv_status pkv_attention_mod_q4(const void *q, const int32_t *cu_seqlens_q, int3
                                 int32_t head_dim, float scale, const pkv_score_mod *mod, const int32_t *work,
                                 const pkv_work_info *info, void *out, void *workspace, uint64_t workspace_bytes,
                                 uint32_t *device_status, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Block-sparse attention. The pages serve long histories whole; models whose
+ * attention falls on few keys need only the blocks that hold them. A step that
+ * reads part of its history keeps, beside the pool, the bounds of every block's
+ * keys, chooses blocks by them, and attends the chosen ones:
+ *   pkv_key_bounds       after the cache write, on the blocks that it touched
+ *   pkv_plan_work_sparse (host) the work list of the next two calls
+ *   pkv_select_blocks    per segment and kv head, the blocks to read
+ *   pkv_attention_sparse attention over those
+ * Bounds (device): bf16 [num_blocks][num_kv_heads][2][head_dim], the smallest and
+ * the largest value of each channel over the block's keys; one more array of the
+ * pool for pkv_copy_blocks.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Bounds of the blocks that `slot_mapping` (device, int64 [num_tokens], as for
+ * pkv_cache_write; < 0 is skipped) names: a token that is the last of its block
+ * in the step (the next token lies in another block) has the block's rows 0 to
+ * its own reduced to their bounds, whatever they were before. So rows behind it
+ * -- rejected drafts, an earlier owner's keys -- never count. The tokens of a
+ * block have to stand one behind the other in the order of their rows, as
+ * pkv_plan_lower leaves them; where a block is named in two places of the
+ * mapping, which of its ends wins is undefined. Exact: a bound is one of the
+ * keys' values. The keys have to be finite. Rows >= num_blocks * block_size are
+ * skipped and set PKV_DEV_BAD_SLOT_MAPPING. Run behind the cache write, on its
+ * stream; pointers 16-byte aligned.
+ */
+pkv_status pkv_key_bounds(const int64_t *slot_mapping, int64_t num_tokens, const void *k_pool, int64_t num_blocks,
+                          int32_t block_size, int32_t num_kv_heads, int32_t head_dim, void *bounds,
+                          uint32_t *device_status, pkv_stream_t stream);
+
+/* The same over the keys of an 8-bit and of a 4-bit pool (the values the codes stand for, bf16 numbers). */
+pkv_status pkv_key_bounds_q8(const int64_t *slot_mapping, int64_t num_tokens, const int8_t *k_codes,
+                             const void *k_scales, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                             int32_t head_dim, void *bounds, uint32_t *device_status, pkv_stream_t stream);
+pkv_status pkv_key_bounds_q4(const int64_t *slot_mapping, int64_t num_tokens, const uint8_t *k_codes,
+                             const void *k_scales, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                             int32_t head_dim, void *bounds, uint32_t *device_status, pkv_stream_t stream);
+
+/*
+ * Which blocks a segment reads (n rows, context L, B = ceil(L / block_size)
+ * blocks): all of them if B <= top_blocks; else top_blocks, namely the first
+ * keep_first blocks, those from floor((L - n) / block_size) - keep_last on (the
+ * step's own rows and keep_last blocks before them), and the best of the others.
+ */
+typedef struct pkv_sparse {
+    int32_t top_blocks; /* >= 1 */
+    int32_t keep_first; /* >= 0 */
+    int32_t keep_last;  /* >= 0 */
+} pkv_sparse;
+
+/*
+ * pkv_plan_work for a block-sparse step. Every segment has at most
+ * 16 / (num_q_heads / num_kv_heads) rows, at least 1 for group sizes above 16 / 2
+ * (PKV_ERR_UNSUPPORTED otherwise: prompt chunks take pkv_attention). The segments
+ * may be the last ones of a packed step: cu_seqlens_q then starts above 0.
+ * PKV_ERR_INVALID_ARG where the blocks that are always kept are more than
+ * top_blocks. Otherwise the validation, sizes and errors of pkv_plan_work; one
+ * workspace of info->workspace_bytes serves both calls, one behind the other.
+ *
+ * Item words: decode (segment, slot, span | first 16-key sub-tile << 23 |
+ * sub-tiles << 27 over the segment's list of blocks, the span's first partial or
+ * -1); prefill: per segment (segment, slot, first candidate of its scores,
+ * candidates); merge as for pkv_plan_work; scratch: 128 candidates to score
+ * (segment, slot, first of them, the segment's first candidate).
+ */
+pkv_status pkv_plan_work_sparse(const int32_t *cu_seqlens_q, int32_t num_seqs, const int32_t *seq_slot,
+                                const int32_t *context_lens, int32_t max_slots, int32_t max_blocks_per_slot,
+                                int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                const pkv_sparse *sparse, int32_t *work, int64_t work_capacity, pkv_work_info *info);
+
+/*
+ * Choose the blocks. A candidate block's score for a segment and kv head is the
+ * largest, over the segment's rows and the head's group of q heads, of
+ *   sum over d of max(q_d lo_d, q_d hi_d),
+ * which no q . k of the block exceeds. Scores are compared as the exact sums (in
+ * 64 bits where 32 cannot tell them apart); of equal ones the lower block goes
+ * first. A score that is not a number ranks last; q and bounds that hold
+ * infinities leave the order of their blocks open.
+ *   selected  int32 [num_seqs][num_kv_heads][top_blocks]  device: the blocks'
+ *             places in the slot's table, growing; -1 behind the last
+ * Same metadata, device status and stream behaviour as pkv_attention; `work` and
+ * `info` from pkv_plan_work_sparse for these metadata, shapes and `sparse`.
+ */
+pkv_status pkv_select_blocks(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                             const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                             int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size, const void *bounds,
+                             int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                             const pkv_sparse *sparse, const int32_t *work, const pkv_work_info *info,
+                             int32_t *selected, void *workspace, uint64_t workspace_bytes, uint32_t *device_status,
+                             pkv_stream_t stream);
+
+/*
+ * pkv_attention of rows that see, of the keys before them, only those in the
+ * blocks of `selected` (from pkv_select_blocks, or a list of the caller's own: the
+ * places in growing order, as many as the segment reads, its newest blocks last --
+ * the block that holds its first row and all behind it). Same arguments, results,
+ * workspace and ordering rules as pkv_attention; `work` and `info` from
+ * pkv_plan_work_sparse. A place outside the slot's blocks or a block outside the
+ * pool is skipped and sets PKV_DEV_BAD_BLOCK. A value that is not finite may reach
+ * other rows of its segment.
+ */
+pkv_status pkv_attention_sparse(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                                const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                                int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size, const void *k_pool,
+                                const void *v_pool, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float scale, const pkv_sparse *sparse, const int32_t *selected,
+                                const int32_t *work, const pkv_work_info *info, void *out, void *workspace,
+                                uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream);
+
+/* The same over an 8-bit and over a 4-bit pool (PKV_ERR_UNSUPPORTED unless head_dim is 128); the workspace is
+ * info->workspace_bytes here too. */
+pkv_status pkv_attention_sparse_q8(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                                   const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                                   int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size,
+                                   const int8_t *k_codes, const void *k_scales, const int8_t *v_codes,
+                                   const void *v_scales, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, float scale, const pkv_sparse *sparse, const int32_t *selected,
+                                   const int32_t *work, const pkv_work_info *info, void *out, void *workspace,
+                                   uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream);
+pkv_status pkv_attention_sparse_q4(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                                   const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                                   int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size,
+                                   const uint8_t *k_codes, const void *k_scales, const uint8_t *v_codes,
+                                   const void *v_scales, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, float scale, const pkv_sparse *sparse, const int32_t *selected,
+                                   const int32_t *work, const pkv_work_info *info, void *out, void *workspace,
+                                   uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Trees of drafted tokens. The pages verify drafts in a line (pkv_attention's
+ * short causal runs); a drafter that proposes several continuations has them
+ * verified as a tree. A segment's n rows are the tree's nodes, appended behind
+ * the slot's history like any rows (node i at place L - n + i of the slot), a
+ * node behind its parent; rotary positions are L - n + the node's depth. After
+ * the step the accepted path's rows move to the front (pkv_accept_rows) and the
+ * slot is cut there (pkv_pool_truncate).
+ * ---------------------------------------------------------------------- */
+#define PKV_TREE_MAX_ROWS 256
+
+/*
+ * Ancestor masks and depths (host only) of the trees of a packed step:
+ * parents[r] is the parent of packed row r as an index into its own segment,
+ * smaller than the row's own, or -1 for a root. `masks` (nullable) receives
+ * uint32 [cu_seqlens_q[num_seqs]][mask_words]: bit j % 32 of word j / 32 is set
+ * where node j is the row itself or one of its ancestors. `depths` (nullable,
+ * int32, one per packed row): 0 for a root. Rows before cu_seqlens_q[0] are left
+ * as they are, and so is parents there. PKV_ERR_INVALID_ARG for a parent that is
+ * not before its node, PKV_ERR_OUT_OF_RANGE for a segment of more than
+ * 32 * mask_words rows.
+ */
+pkv_status pkv_tree_masks(const int32_t *parents, const int32_t *cu_seqlens_q, int32_t num_seqs, int32_t mask_words,
+                          uint32_t *masks, int32_t *depths);
+
+/*
+ * pkv_plan_work for a step of trees: segments of 1 to PKV_TREE_MAX_ROWS rows
+ * (PKV_ERR_UNSUPPORTED beyond). They may be the last ones of a packed step:
+ * cu_seqlens_q then starts above 0. Otherwise the validation, sizes and errors
+ * of pkv_plan_work. The keys are cut into spans of whole 128-key tiles; the cut
+ * depends on the segment and on max_slots, not on the other segments.
+ *
+ * Item words: decode (segment, 128-key tiles in the span, first tile | query tile
+ * << 24, the span's first partial or -1; the partial of row i is i further); merge
+ * as for pkv_plan_work.
+ */
+pkv_status pkv_plan_work_tree(const int32_t *cu_seqlens_q, int32_t num_seqs, const int32_t *seq_slot,
+                              const int32_t *context_lens, int32_t max_slots, int32_t max_blocks_per_slot,
+                              int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t *work, int64_t work_capacity, pkv_work_info *info);
+
+/*
+ * Move the rows of each segment's accepted path to its front: for d = 0, 1, ...
+ * while paths[s][d] >= 0, the pool rows at place L - n + paths[s][d] of the slot
+ * are copied to place L - n + d, in each of the `num_arrays` (1 to 4) pool arrays:
+ * arrays[a] (device, 16-byte aligned) is [num_blocks][num_kv_heads][block_size]
+ * rows of row_bytes[a] bytes (a multiple of 4) -- a bf16 pool's K and V, or codes
+ * and scales. Bit-exact; the metadata is the step's, with the lengths that
+ * pkv_plan_lower gave (before pkv_pool_truncate).
+ *   paths  int32 [num_seqs][max_path]  device; growing, each below n
+ * A path that does not grow or leaves the segment ends there and sets
+ * PKV_DEV_BAD_SEGMENT; a block outside the pool is skipped (PKV_DEV_BAD_BLOCK).
+ * Two segments of one slot race. `arrays` and `row_bytes` are host arrays.
+ */
+pkv_status pkv_accept_rows(const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q, const int32_t *seq_slot,
+                           const int32_t *context_lens, const int32_t *block_tables, int32_t max_slots,
+                           int32_t max_blocks_per_slot, int32_t block_size, int32_t num_kv_heads,
+                           const int32_t *paths, int32_t max_path, void *const *arrays, const int64_t *row_bytes,
+                           int32_t num_arrays, int64_t num_blocks, uint32_t *device_status, pkv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Host-staged step: a whole step from host memory in one call.
