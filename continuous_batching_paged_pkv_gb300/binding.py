@@ -162,6 +162,8 @@ def _lib():
             "pkv_tree_masks": ([p, p, i32, i32, p, p], ctypes.c_int),
             "pkv_plan_work_tree": ([p, i32, p, p, i32, i32, i32, i32, i32, i32, p, i64, ctypes.POINTER(WorkInfo)],
                                    ctypes.c_int),
+            "pkv_attention_tree": ([p, p, i32, i64, p, p, p, i32, i32, i32, p, p, i64, i32, i32, i32, f32, p, i32, p,
+                                    ctypes.POINTER(WorkInfo), p, p, u64, p, p], ctypes.c_int),
             "pkv_accept_rows": ([p, i32, i64, p, p, p, i32, i32, i32, i32, p, i32, ctypes.POINTER(ctypes.c_void_p),
                                  ctypes.POINTER(ctypes.c_int64), i32, i64, p, p], ctypes.c_int),
             "pkv_stage_layout_init": ([ctypes.POINTER(StageLayout), i64, i32, i32, i32, i32, i32, i32], ctypes.c_int),
@@ -898,6 +900,38 @@ def pkv_attention_sparse_q4(q, cu_seqlens_q, seq_slot, context_lens, block_table
     AttentionSparseCall(q, cu_seqlens_q, seq_slot, context_lens, block_tables, (k_codes, k_scales, v_codes, v_scales),
                         selected, work, info, out, workspace, sparse=sparse, kv="q4", scale=scale,
                         device_status=device_status, stream=stream)()
+
+
+class AttentionTreeCall(_BoundCall):
+    """``pkv_attention_tree`` bound once. ``pool`` = (k_pool, v_pool); ``masks``: int32 (the bits of ``pkv_tree_masks``)
+    [rows, words]."""
+
+    def __init__(self, q, cu_seqlens_q, seq_slot, context_lens, block_tables, pool, masks, work, info: WorkInfo, out,
+                 workspace=None, *, scale: float = 0.0, device_status=None, stream=None):
+        nb, hkv, bs, d = _need_pool(pool, "bf16")
+        segs, ms, mbps = _need_step(q, cu_seqlens_q, seq_slot, context_lens, block_tables, work, info, d, hkv)
+        _need(out, "torch.bfloat16", "out")
+        _need(masks, "torch.int32", "masks")
+        info = WorkInfo.from_buffer_copy(info)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if masks.dim() != 2 or masks.shape[0] != q.shape[0]:
+            raise ValueError("masks must be [rows, words], one row per packed row")
+        _need_on(q.device, cu_seqlens_q, seq_slot, context_lens, block_tables, *pool, masks, work, out, workspace,
+                 device_status)
+        self._bind("pkv_attention_tree",
+                   (_t_ptr(q), _t_ptr(cu_seqlens_q), segs, q.shape[0], _t_ptr(seq_slot), _t_ptr(context_lens),
+                    _t_ptr(block_tables), ms, mbps, bs, *map(_t_ptr, pool), nb, q.shape[1], hkv, d, float(scale),
+                    _t_ptr(masks), masks.shape[1], _t_ptr(work), ctypes.byref(info), _t_ptr(out), _t_ptr(workspace),
+                    _bytes(workspace), _t_ptr(device_status)),
+                   (q, cu_seqlens_q, seq_slot, context_lens, block_tables, tuple(pool), masks, work, info, out,
+                    workspace, device_status), q.device, stream)
+
+
+def pkv_attention_tree(q, cu_seqlens_q, seq_slot, context_lens, block_tables, k_pool, v_pool, masks, work,
+                       info: WorkInfo, out, workspace=None, *, scale: float = 0.0, device_status=None, stream=None) -> None:
+    AttentionTreeCall(q, cu_seqlens_q, seq_slot, context_lens, block_tables, (k_pool, v_pool), masks, work, info, out,
+                      workspace, scale=scale, device_status=device_status, stream=stream)()
 
 
 class AcceptRowsCall(_BoundCall):

@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(PKG, "libpkv.so")
 
 SOURCES = ["pkv_host.cpp", "pkv_step.cpp", "pkv_accept.cu", "pkv_api.cu", "pkv_cache_write.cu", "pkv_decode.cu",
            "pkv_key_bounds.cu", "pkv_kvquant.cu", "pkv_plan_lists.cpp", "pkv_prefill.cu", "pkv_prefill_mod.cu",
-           "pkv_prefill_pair.cu", "pkv_rope.cu", "pkv_rope_plan.cpp", "pkv_select.cu", "pkv_static.cu"]
+           "pkv_prefill_pair.cu", "pkv_rope.cu", "pkv_rope_plan.cpp", "pkv_select.cu", "pkv_static.cu",
+           "pkv_tree.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -759,6 +759,45 @@ pkv_status pkv_attention_sparse_q4(const void *q, const int32_t *cu_seqlens_q, i
                           workspace_bytes, device_status, stream);
 }
 
+pkv_status pkv_attention_tree(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                              const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                              int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size, const void *k_pool,
+                              const void *v_pool, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_dim, float scale, const uint32_t *masks, int32_t mask_words,
+                              const int32_t *work, const pkv_work_info *info, void *out, void *workspace,
+                              uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream) {
+  pkv::StepArgs a{};
+  bool empty = false;
+  if (const pkv_status st = list_args(a, empty, pkv::kListTree, q, cu_seqlens_q, num_seqs, total_q, seq_slot,
+                                      context_lens, block_tables, max_slots, max_blocks_per_slot, block_size, num_blocks,
+                                      num_q_heads, num_kv_heads, head_dim, work, info, device_status);
+      st != PKV_OK || empty)
+    return st;
+  if (!k_pool || !v_pool || !masks || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(masks, 4) ||
+      mask_words < 1 || mask_words > PKV_TREE_MAX_ROWS / 32 || info->decode_rows_max > 32 * mask_words ||
+      info->num_prefill_items != 0 || info->num_scratch_items != 0)
+    return PKV_ERR_INVALID_ARG;
+  if (info->num_decode_items > INT32_MAX / num_kv_heads) return PKV_ERR_UNSUPPORTED;  // one grid
+  if (const pkv_status st = partial_args(a, scale, out, workspace, workspace_bytes); st != PKV_OK) return st;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.masks = masks;
+  a.mask_words = mask_words;
+  a.task_counter = nullptr;
+  const int64_t rows = num_blocks * num_kv_heads * block_size;
+  CUtensorMap tq, tk, tv;
+  if (!encode_q(&tq, q, total_q, num_q_heads, head_dim, a.group, pkv::prefill_rows_per_tile(a.group)) ||
+      !(head_dim == 128 ? encode_pool_subtiles(&tk, k_pool, num_blocks * num_kv_heads, block_size) &&
+                              encode_pool_subtiles(&tv, v_pool, num_blocks * num_kv_heads, block_size)
+                        : encode_pool(&tk, k_pool, rows, head_dim) && encode_pool(&tv, v_pool, rows, head_dim)))
+    return PKV_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int32_t *comb = work + static_cast<int64_t>(info->num_decode_items) * PKV_WORK_WORDS_PER_ITEM;
+  cudaError_t e = pkv::launch_tree(a, tq, tk, tv, info->num_decode_items, work, st);
+  if (e == cudaSuccess) e = pkv::launch_merge(a, info->num_combine_items, info->num_long_combine_items, comb, st);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 pkv_status pkv_check_device_status(uint32_t *device_status, pkv_stream_t stream, uint32_t *bits_out) {
   if (!device_status) return PKV_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -161,6 +161,10 @@ cudaError_t launch_key_bounds(const int64_t *slot_mapping, int64_t num_tokens, c
 cudaError_t launch_select_blocks(const StepArgs &a, const void *bounds, const pkv_work_info &info, void *workspace,
                                  int32_t *selected, cudaStream_t stream);
 
+// Trees (pkv_tree.cu).
+cudaError_t launch_tree(const StepArgs &a, const CUtensorMap &tmap_q, const CUtensorMap &tmap_k,
+                        const CUtensorMap &tmap_v, int32_t num_items, const int32_t *items, cudaStream_t stream);
+
 // Rows of accepted paths (pkv_accept.cu).
 struct AcceptArgs {
   const int32_t *cu_seqlens_q, *seq_slot, *context_lens, *block_tables, *paths;

@@ -865,6 +865,25 @@ pkv_status pkv_plan_work_tree(const int32_t *cu_seqlens_q, int32_t num_seqs, con
                               int32_t *work, int64_t work_capacity, pkv_work_info *info);
 
 /*
+ * pkv_attention of trees: row i of a segment sees the keys before the segment
+ * (0 .. L - n - 1) and those of the nodes j < n whose bit is set in its mask;
+ * masks uint32 [total_q][mask_words] (device, 1 to 8 words, 32 * mask_words >= the
+ * largest segment's rows). The masks need not be those of a tree: any set of the
+ * step's rows, itself or not. A row that sees nothing gives zeros. Same
+ * arguments, results, workspace and ordering rules as pkv_attention, but that the
+ * call waits for the kernel before it from the start; `work` and `info` from
+ * pkv_plan_work_tree. The keys and values of the slot's rows must be finite:
+ * through 0 * infinity a value may reach rows that do not see it.
+ */
+pkv_status pkv_attention_tree(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
+                              const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
+                              int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size, const void *k_pool,
+                              const void *v_pool, int64_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_dim, float scale, const uint32_t *masks, int32_t mask_words,
+                              const int32_t *work, const pkv_work_info *info, void *out, void *workspace,
+                              uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream);
+
+/*
  * Move the rows of each segment's accepted path to its front: for d = 0, 1, ...
  * while paths[s][d] >= 0, the pool rows at place L - n + paths[s][d] of the slot
  * are copied to place L - n + d, in each of the `num_arrays` (1 to 4) pool arrays:
