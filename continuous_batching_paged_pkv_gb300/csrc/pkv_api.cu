@@ -709,9 +709,9 @@ pkv_status pkv_select_blocks(const void *q, const int32_t *cu_seqlens_q, int32_t
     return st;
   if (const pkv_status st = sparse_args(a, sparse, info); st != PKV_OK) return st;
   if (!bounds || !selected || !aligned(bounds, 16) || !aligned(selected, 4) ||
-      (info->scratch_blocks > 0) != (info->num_scratch_items > 0))
+      info->scratch_blocks != static_cast<int64_t>(info->num_scratch_items) * pkv::kScoreBlocks)
     return PKV_ERR_INVALID_ARG;
-  const uint64_t need = pkv::select_layout(info->scratch_blocks, info->num_scratch_items, num_kv_heads).bytes;
+  const uint64_t need = pkv::select_layout(info->scratch_blocks, num_kv_heads).bytes;
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return PKV_ERR_WORKSPACE_TOO_SMALL;
   const cudaError_t e = pkv::launch_select_blocks(a, bounds, *info, workspace, selected, reinterpret_cast<cudaStream_t>(stream));

@@ -86,22 +86,24 @@ constexpr int kLongMergeSpans = 64;
 // Bytes of workspace after the span partials: the decode kernel's task counter.
 constexpr uint64_t kCounterBytes = 256;
 
-// Candidate blocks that one CTA of the selection scores.
-constexpr int kScoreBlocks = 128;
+// Candidate blocks of one scoring item of the selection, and those that a warp scores at once.
+constexpr int kScoreBlocks = 128, kScoreGroup = 16;
 
-// Workspace of pkv_select_blocks: scores (fp32) and exact scores (fp64) of every (candidate, kv head), and per
-// (scoring item, kv head) the largest sum of magnitudes. Offsets in bytes.
+// Workspace of pkv_select_blocks: exact scores (fp64) and scores (fp32) of every (candidate, kv head), and per
+// (group of candidates, kv head) the largest sum of magnitudes. A segment's candidates start at a multiple of
+// kScoreBlocks, and so do its parts of these arrays. Offsets in bytes.
 struct SelectLayout {
   uint64_t exact, scores, sums, bytes;
 };
-inline SelectLayout select_layout(int64_t candidates, int64_t score_items, int32_t num_kv_heads) {
+inline SelectLayout select_layout(int64_t candidates, int32_t num_kv_heads) {
   auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
+  const uint64_t n = static_cast<uint64_t>(candidates) * num_kv_heads;
   SelectLayout l;
   l.exact = 0;
-  l.scores = up(static_cast<uint64_t>(candidates) * num_kv_heads * 8);
-  l.sums = l.scores + up(static_cast<uint64_t>(candidates) * num_kv_heads * 4);
-  l.bytes = l.sums + up(static_cast<uint64_t>(score_items) * num_kv_heads * 4);
-  return candidates == 0 ? SelectLayout{0, 0, 0, 0} : l;
+  l.scores = up(n * 8);
+  l.sums = l.scores + up(n * 4);
+  l.bytes = l.sums + up(n / kScoreGroup * 4);
+  return l;
 }
 
 // Blocks of a slot of L keys, n of them this step's rows, in a block-sparse step: all of them, the candidates
@@ -109,8 +111,8 @@ inline SelectLayout select_layout(int64_t candidates, int64_t score_items, int32
 struct SparseBlocks {
   int64_t blocks, first, last, read;
 };
-inline __host__ __device__ SparseBlocks sparse_blocks(int64_t L, int64_t n, int32_t block_size, int32_t top,
-                                                      int32_t keep_first, int32_t keep_last) {
+inline SparseBlocks sparse_blocks(int64_t L, int64_t n, int32_t block_size, int32_t top, int32_t keep_first,
+                                  int32_t keep_last) {
   SparseBlocks b;
   b.blocks = (L + block_size - 1) / block_size;
   b.last = (L - n) / block_size - keep_last;

@@ -76,7 +76,7 @@ pkv_status finish(std::vector<Item> &dec, std::vector<Item> &pre, std::vector<It
   if (info->num_scratch_items > 0)
     info->workspace_bytes = info->workspace_bytes_q8 =
         std::max(info->workspace_bytes,
-                 pkv::select_layout(info->scratch_blocks, info->num_scratch_items, sh.num_kv_heads).bytes);
+                 pkv::select_layout(info->scratch_blocks, sh.num_kv_heads).bytes);
   if (!work || work_capacity < info->work_words) return PKV_ERR_WORKSPACE_TOO_SMALL;
   for (const auto *v : {&dec, &pre, &comb, &scr})
     for (const Item &it : *v) {
@@ -106,11 +106,11 @@ pkv_status plan_sparse(const int32_t *cu, int32_t num_seqs, const int32_t *seq_s
     // selection: candidates only where not every block is read
     const int64_t cand = b.blocks > b.read ? b.last - b.first : 0;
     if (b.blocks > b.read && b.first + (b.blocks - b.last) > sp.top_blocks) return PKV_ERR_INVALID_ARG;
-    if (candidates + cand > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (candidates + cand > INT32_MAX - pkv::kScoreBlocks || cand > (1 << 20)) return PKV_ERR_UNSUPPORTED;
     pre.push_back({{s, slot, static_cast<int32_t>(candidates), static_cast<int32_t>(cand)}, cand});
     for (int64_t c = 0; c < cand; c += pkv::kScoreBlocks)
       scr.push_back({{s, slot, static_cast<int32_t>(c), static_cast<int32_t>(candidates)}, 0});
-    candidates += cand;
+    candidates += ceil_div(cand, pkv::kScoreBlocks) * pkv::kScoreBlocks;
     // attention: spans over the list of blocks, whose last one may be partly filled
     const int64_t keys = L - (b.blocks - b.read) * sh.block_size;
     const int32_t sk = pkv::span_keys(keys, sh.max_slots, sh.num_kv_heads);

@@ -756,9 +756,10 @@ typedef struct pkv_sparse {
  *
  * Item words: decode (segment, slot, span | first 16-key sub-tile << 23 |
  * sub-tiles << 27 over the segment's list of blocks, the span's first partial or
- * -1); prefill: per segment (segment, slot, first candidate of its scores,
- * candidates); merge as for pkv_plan_work; scratch: 128 candidates to score
- * (segment, slot, first of them, the segment's first candidate).
+ * -1); prefill: per segment (segment, slot, first candidate of its scores, a
+ * multiple of 128, candidates); merge as for pkv_plan_work; scratch: 128
+ * candidates to score (segment, slot, first of them, the segment's first
+ * candidate).
  */
 pkv_status pkv_plan_work_sparse(const int32_t *cu_seqlens_q, int32_t num_seqs, const int32_t *seq_slot,
                                 const int32_t *context_lens, int32_t max_slots, int32_t max_blocks_per_slot,

@@ -78,9 +78,10 @@ def test_sparse_list(seed):
         cand[s] = (sel[2], sel[3])
         parts = sorted(tuple(x) for x in scr[scr[:, 0] == s].tolist())
         assert [p[2] for p in parts] == list(range(0, sel[3], 128)) and all(p[3] == sel[2] for p in parts)
-    taken = sorted((f, f + c) for f, c in cand.values() if c)
-    assert all(x[1] == y[0] for x, y in zip(taken, taken[1:])) and info.scratch_blocks == sum(c for _, c in cand.values())
-    need = max(info.scratch_blocks * hkv * 12, 0)
+    taken = sorted((f, f + -(-c // 128) * 128) for f, c in cand.values() if c)
+    assert all(x[1] == y[0] for x, y in zip(taken, taken[1:])) and all(f % 128 == 0 for f, _ in taken)
+    assert info.scratch_blocks == sum(-(-c // 128) * 128 for _, c in cand.values()) == 128 * len(scr)
+    need = info.scratch_blocks * hkv * 12
     assert info.workspace_bytes >= need and (info.workspace_bytes == 0 or info.workspace_bytes >= 256)
 
 
