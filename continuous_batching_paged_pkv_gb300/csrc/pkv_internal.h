@@ -275,7 +275,8 @@ inline int32_t prefill_rows_per_tile(int32_t group) { return 128 / group; }
 
 // Trees (pkv_tree.cu): keys come in tiles of 128; a CTA takes two query tiles where some segment of the step has
 // more than one, else one. Spans of kTreeMinSpanTiles to kTreeSpanTiles tiles.
-constexpr int kTreeTileKeys = 128, kTreeMinSpanTiles = 2, kTreeSpanTiles = 32;
+constexpr int kTreeMaxKeys = INT32_MAX - 4096;  // so that a position behind the last tile is still a number
+constexpr int kTreeTileKeys = 128, kTreeMinSpanTiles = 2, kTreeSpanTiles = 64;
 inline int32_t tree_tiles_per_cta(int32_t rows_max, int32_t group) {
   return rows_max > prefill_rows_per_tile(group) ? 2 : 1;
 }

@@ -153,18 +153,17 @@ pkv_status plan_tree(const int32_t *cu, int32_t num_seqs, const int32_t *seq_slo
     int32_t n, slot, L;
     if (const pkv_status st = check_segment(cu, s, seq_slot, context_lens, sh, used, n, slot, L); st != PKV_OK) return st;
     if (n == 0) continue;
+    if (L > pkv::kTreeMaxKeys) return PKV_ERR_UNSUPPORTED;
     const int32_t q_tiles = static_cast<int32_t>(ceil_div(n, rows_per_tile));
     const int64_t tiles = ceil_div(L, pkv::kTreeTileKeys);
-    if (tiles >= (1 << 24)) return PKV_ERR_UNSUPPORTED;
     const int64_t span = pkv::tree_span_tiles(tiles, q_tiles, sh.max_slots, sh.num_kv_heads);
     const int64_t spans = ceil_div(tiles, span);
     if (spans >= (1 << 16) || partials + spans * n > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     for (int64_t i = 0; i < spans; ++i)
       for (int32_t t = 0; t < q_tiles; t += step) {
-        const int64_t count = std::min(span, tiles - i * span);
-        const uint32_t w = static_cast<uint32_t>(i * span) | static_cast<uint32_t>(t) << 24;
-        dec.push_back({{s, static_cast<int32_t>(count), static_cast<int32_t>(w),
-                        spans > 1 ? static_cast<int32_t>(partials + i * n) : -1}, count});
+        const uint32_t w = static_cast<uint32_t>(i) | static_cast<uint32_t>(span - 1) << 16 | static_cast<uint32_t>(t) << 24;
+        dec.push_back({{s, slot, static_cast<int32_t>(w), spans > 1 ? static_cast<int32_t>(partials + i * n) : -1},
+                       std::min(span, tiles - i * span)});
       }
     if (spans > 1) {
       for (int32_t i = 0; i < n; ++i)

@@ -856,9 +856,9 @@ pkv_status pkv_tree_masks(const int32_t *parents, const int32_t *cu_seqlens_q, i
  * of pkv_plan_work. The keys are cut into spans of whole 128-key tiles; the cut
  * depends on the segment and on max_slots, not on the other segments.
  *
- * Item words: decode (segment, 128-key tiles in the span, first tile | query tile
- * << 24, the span's first partial or -1; the partial of row i is i further); merge
- * as for pkv_plan_work.
+ * Item words: decode (segment, slot, span | (128-key tiles in a span - 1) << 16 |
+ * query tile << 24, the span's first partial or -1; the partial of row i is i
+ * further); merge as for pkv_plan_work.
  */
 pkv_status pkv_plan_work_tree(const int32_t *cu_seqlens_q, int32_t num_seqs, const int32_t *seq_slot,
                               const int32_t *context_lens, int32_t max_slots, int32_t max_blocks_per_slot,
@@ -871,9 +871,8 @@ pkv_status pkv_plan_work_tree(const int32_t *cu_seqlens_q, int32_t num_seqs, con
  * masks uint32 [total_q][mask_words] (device, 1 to 8 words, 32 * mask_words >= the
  * largest segment's rows). The masks need not be those of a tree: any set of the
  * step's rows, itself or not. A row that sees nothing gives zeros. Same
- * arguments, results, workspace and ordering rules as pkv_attention, but that the
- * call waits for the kernel before it from the start; `work` and `info` from
- * pkv_plan_work_tree. The keys and values of the slot's rows must be finite:
+ * arguments, results, workspace and ordering rules as pkv_attention (the masks are
+ * read at once, like q); `work` and `info` from pkv_plan_work_tree. The keys and values of the slot's rows must be finite:
  * through 0 * infinity a value may reach rows that do not see it.
  */
 pkv_status pkv_attention_tree(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,

@@ -100,15 +100,14 @@ def test_tree_list(seed):
     _merges(comb, info.num_partials)
     per = 128 // (hq // hkv)
     step = 2 if info.decode_rows_max > per else 1
-    assert (np.diff(dec[:, 1]) <= 0).all()  # longest first
     for s, (n, L) in enumerate(segs):
         mine = dec[dec[:, 0] == s]
         got = np.zeros((-(-n // per), -(-L // 128)), int)
-        for _, tiles, w, first in mine:
+        for _, slot, w, first in mine:
             w = int(w) & 0xFFFFFFFF
-            t0, q0 = w & 0xFFFFFF, w >> 24
-            got[q0:q0 + step, t0:t0 + tiles] += 1
-            assert first < 0 or first + n <= info.num_partials
+            span, q0 = (w >> 16 & 0xFF) + 1, w >> 24
+            got[q0:q0 + step, (w & 0xFFFF) * span:][:, :span] += 1
+            assert slot == ss[s] and (first < 0 or first + n <= info.num_partials)
         assert (got == 1).all()
 
 
