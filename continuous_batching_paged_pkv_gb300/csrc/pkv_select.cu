@@ -389,7 +389,8 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
                                                           const int32_t *__restrict__ items, int64_t candidates,
                                                           float *scores, const float *__restrict__ sums,
                                                           double *exact, int32_t *__restrict__ selected) {
-  grid_dependency_wait();
+  // The metadata and the list are final when this grid starts (the scoring kernel starts after everything before the
+  // call); only the scores need the scoring kernel to finish. Every path waits for it, so that the grid ends after it.
   launch_dependents();
   extern __shared__ uint32_t keys[];
   __shared__ uint32_t s_buf[2][32];
@@ -401,6 +402,7 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
   const int base = it.z, N = it.w;
   if (!(it.x >= 0 && it.x < a.num_seqs)) {
     if (tid == 0 && a.status && g == 0) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
+    grid_dependency_wait();
     return;
   }
   const Chosen c = chosen_segment(a, it.x, it.y, 16, __ldg(a.cu_seqlens_q + it.x), __ldg(a.cu_seqlens_q + it.x + 1),
@@ -411,13 +413,16 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
                   static_cast<int64_t>(base) + (N + kScoreBlocks - 1) / kScoreBlocks * kScoreBlocks <= candidates;
   if (!ok) {
     if (tid == 0 && a.status && g == 0) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
+    grid_dependency_wait();
     for (int i = tid; i < a.top_blocks; i += T) out[i] = -1;
     return;
   }
   if (N == 0) {  // every block
+    grid_dependency_wait();
     for (int i = tid; i < a.top_blocks; i += T) out[i] = i < c.blocks ? i : -1;
     return;
   }
+  grid_dependency_wait();
   // the blocks that are always read, and what is left empty
   const int tail = c.blocks - c.last;
   const uint32_t need = static_cast<uint32_t>(c.read - c.first - tail);
