@@ -18,16 +18,23 @@
 // to fp32 in an order of its own, within 17 * 2^-23 of the sum of their magnitudes;
 // two steps make a piece, whose sum (at most A of the piece, so 34 * 2^-23 A over all
 // of them) is added to the running one with at most 8 roundings of 2^-24 A: a score
-// is within 2^-17 A of the exact sum.
+// is within 38 * 2^-23 A of the exact sum, for which 64 * 2^-23 A is taken, and 2^-100
+// for products that are too small for fp32.
 //
 // Choosing kernel: a CTA per (segment, kv head), of 4 warps or, where segments have
-// many candidates, 32. The k-th largest fp32 score T comes from histograms of the
-// ordered scores' digits. With E the error bound, what is
-// above T + 2 E is in, what is below T - 2 E is out, and only the blocks between
-// are summed again, in fp64 (products of two bf16 are exact there), and ranked by
-// (score, lower place first). So the choice is that of the exact scores, whatever
-// the order of the sums, and every run gives the same. Then the chosen places are
-// written in growing order.
+// many candidates, 32. A bound T that exactly k scores reach, or else the k-th largest
+// score, comes from histograms of the ordered scores' digits. With E the error bound,
+// what is above T + 2 E is in (its exact score is above T + E, and fewer than k are),
+// what is below T - 2 E is out (k others have exact scores from T - E on), and only the
+// blocks between are summed again, in fp64 (products of two bf16 are exact there), and
+// ranked by (score, lower place first). So the choice is that of the exact scores,
+// whatever the order of the sums, and every run gives the same. Then the chosen places
+// are written in growing order.
+//
+// 256 slots x 8 heads of 512 to 16384 keys in blocks of 32, 64 chosen: 43 us, the
+// scores 29 of them (150 MB, 5.2 TB/s); five slots of up to 131072 keys in blocks of
+// 16, 128 chosen: 32 us, the scores 20. The rest is the choosing kernel's chain of
+// loads, histograms and, in a CTA of seven there, an exact sum (5 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -453,14 +460,20 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
   uint32_t mag = 0, least = ~0u, most = 0u;
   const float *group_sums = sums + sum_index(base, a.num_kv_heads, g, N);
   for (int i = tid; i < (N + kScoreGroup - 1) / kScoreGroup; i += T) mag = max(mag, __float_as_uint(__ldcg(group_sums + i)));
-  for (int j = w0 + lane; j < w1; j += 32) {
-    const uint32_t k = ordered(__ldcg(sc + j));
-    if (resident) keys[j] = k;
-    least = min(least, k), most = max(most, k);
+  for (int j0 = w0 + lane; j0 < w1; j0 += 8 * 32) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __ldcg(sc + min(j0 + i * 32, w1 - 1));  // past the last: that one again
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t k = ordered(v[i]);
+      if (resident && j0 + i * 32 < w1) keys[j0 + i * 32] = k;
+      least = min(least, k), most = max(most, k);
+    }
   }
   if (tid == 0) s_listed = 0;
   __syncthreads();
-  const float error = __uint_as_float(~block.least(~mag)) * kScoreError;
+  const float error = __uint_as_float(~block.least(~mag)) * kScoreError + 0x1p-100f;
   least = block.least(least);
   most = ~block.least(~most);
   // x: a bound that `need` candidates reach and no larger one does, or that exactly `need` reach. Eight bits at a
@@ -505,9 +518,7 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
     left = s_digit[1];
     if (s_digit[2] == left) break;
   }
-  uint32_t lowest = ~0u;
-  each([&](int, uint32_t k, bool live) { if (live && k >= x) lowest = min(lowest, k); });
-  const float T0 = unordered(block.least(lowest));
+  const float T0 = unordered(x);
   float low = __fsub_rd(T0, 2.f * error), high = __fadd_ru(T0, 2.f * error);
   if (!(low <= T0)) low = -INFINITY;    // infinities and NaN among the terms: all are summed again
   if (!(high >= T0)) high = INFINITY;
@@ -517,8 +528,9 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
     over += live && k > khigh;
     between += live && k >= klow && k <= khigh;
   });
+  uint32_t mine = over + between;  // of this thread, where all between the bounds are in
   over = block.sum(over);
-  const uint32_t m = block.sum(between), r = need - over;  // r of m, r >= 1
+  const uint32_t m = block.sum(between), r = need - over;  // r of m
   uint32_t from = klow;  // scores from here on are chosen
   if (m != r) {
     from = khigh + 1;  // what is settled is above or below
@@ -578,8 +590,10 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
     __syncthreads();
   }
   auto in = [&](uint32_t k, bool live) { return live && k >= from; };
-  uint32_t mine = 0;
-  each([&](int, uint32_t k, bool live) { mine += in(k, live); });
+  if (m != r) {
+    mine = 0;
+    each([&](int, uint32_t k, bool live) { mine += in(k, live); });
+  }
   uint32_t place = block.warps_before(mine);
   each([&](int j, uint32_t k, bool live) {
     const bool here = in(k, live);
