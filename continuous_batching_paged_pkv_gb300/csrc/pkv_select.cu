@@ -309,7 +309,6 @@ struct Block {
   template <typename Op>
   __device__ __forceinline__ uint32_t reduce(uint32_t x, uint32_t none, Op op) {
     const uint32_t w = op(x);
-    if constexpr (T == 32) return w;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     turn ^= 1;
     if (lane == 0) buf[turn][warp] = w;
@@ -324,7 +323,6 @@ struct Block {
   }
   // Sum over the warps before this one of x's sums over a warp.
   __device__ __forceinline__ uint32_t warps_before(uint32_t x) {
-    if constexpr (T == 32) return 0;
     const uint32_t w = __reduce_add_sync(kAll, x);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     turn ^= 1;

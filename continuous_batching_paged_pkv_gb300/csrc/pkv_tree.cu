@@ -32,7 +32,7 @@
 // takes it.
 //
 // Every mbarrier wait is bounded; on expiry the CTA records PKV_DEV_TIMEOUT,
-// drains its MMAs and frees its TMEM before it returns.
+// drains its MMAs, waits for its copies and frees its TMEM before it returns.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -45,6 +45,7 @@ namespace {
 
 constexpr int kTileKeys = kTreeTileKeys;  // spans are whole tiles
 constexpr int kUnitKeys = 64, kUnitSubs = kUnitKeys / kSubKeys;
+static_assert(kTreeMinSpanTiles * kTileKeys >= PKV_TREE_MAX_ROWS, "rows of a segment without a history are one span");
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t kFull = 0xffffffffu;
 
@@ -481,10 +482,8 @@ __global__ void __maxnreg__((Cfg<D, W>::kLaunchRegs))
               for (int v = 0; v < 4; ++v) store_32(dst + c * 32 + v * 8, ov + 8 * v);
           }
           if (stored) {
-            // a row that sees nothing at all: sums of 0 over a denominator that is not 0 merge to zeros
-            bool none = unseen && L == n;
-            for (int k = 0; none && k < a.mask_words; ++k) none = mask_word(mask, a.mask_words, n, k) == 0;
-            reinterpret_cast<float2 *>(a.partial_ml)[e] = none ? make_float2(0.f, 1.f) : make_float2(m_used, l);
+            // (what every span of a row leaves has a maximum: a segment of several spans has a history)
+            reinterpret_cast<float2 *>(a.partial_ml)[e] = make_float2(m_used, l);
           }
         }
       }
@@ -494,7 +493,15 @@ __global__ void __maxnreg__((Cfg<D, W>::kLaunchRegs))
   grid_dependency_wait();  // this grid ends after the kernel before it, whatever its roles did
   tc_fence_before();
   __syncthreads();
-  if (*abort_flag && threadIdx.x == 0 && a.status) atomicOr(a.status, PKV_DEV_TIMEOUT);
+  if (*abort_flag) {
+    if (threadIdx.x == 0 && a.status) atomicOr(a.status, PKV_DEV_TIMEOUT);
+    if (warp == C::kWarpProducer) {  // the copies in flight still write to this CTA's shared memory
+      int late = 0;
+      wait_or_abort(bar + C::kQFull, 0, &late);
+      for (int i = max(0, load.next - C::kSlots); i < load.next; ++i)
+        wait_or_abort(bar + C::kSlotFull + i % C::kSlots, (i / C::kSlots) & 1, &late);
+    }
+  }
   if (warp == C::kWarpScores) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);

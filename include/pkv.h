@@ -746,13 +746,14 @@ typedef struct pkv_sparse {
 } pkv_sparse;
 
 /*
- * pkv_plan_work for a block-sparse step. Every segment has at most
- * 16 / (num_q_heads / num_kv_heads) rows, at least 1 for group sizes above 16 / 2
- * (PKV_ERR_UNSUPPORTED otherwise: prompt chunks take pkv_attention). The segments
- * may be the last ones of a packed step: cu_seqlens_q then starts above 0.
- * PKV_ERR_INVALID_ARG where the blocks that are always kept are more than
- * top_blocks. Otherwise the validation, sizes and errors of pkv_plan_work; one
- * workspace of info->workspace_bytes serves both calls, one behind the other.
+ * pkv_plan_work for a block-sparse step. A segment has at most floor(16 / G) rows,
+ * G = num_q_heads / num_kv_heads (PKV_ERR_UNSUPPORTED otherwise: prompt chunks
+ * take pkv_attention), and at most 2^20 blocks to choose among
+ * (PKV_ERR_UNSUPPORTED). The segments may be the last ones of a packed step:
+ * cu_seqlens_q then starts above 0. PKV_ERR_INVALID_ARG where the blocks that are
+ * always kept are more than top_blocks. Otherwise the validation, sizes and errors
+ * of pkv_plan_work; one workspace of info->workspace_bytes serves both calls, one
+ * behind the other.
  *
  * Item words: decode (segment, slot, span | first 16-key sub-tile << 23 |
  * sub-tiles << 27 over the segment's list of blocks, the span's first partial or
@@ -775,7 +776,8 @@ pkv_status pkv_plan_work_sparse(const int32_t *cu_seqlens_q, int32_t num_seqs, c
  * first. A score that is not a number ranks last; q and bounds that hold
  * infinities leave the order of their blocks open.
  *   selected  int32 [num_seqs][num_kv_heads][top_blocks]  device: the blocks'
- *             places in the slot's table, growing; -1 behind the last
+ *             places in the slot's table, growing; -1 behind the last;
+ *             entries of segments without rows are left as they are
  * Same metadata, device status and stream behaviour as pkv_attention; `work` and
  * `info` from pkv_plan_work_sparse for these metadata, shapes and `sparse`.
  */
@@ -805,8 +807,8 @@ pkv_status pkv_attention_sparse(const void *q, const int32_t *cu_seqlens_q, int3
                                 const int32_t *work, const pkv_work_info *info, void *out, void *workspace,
                                 uint64_t workspace_bytes, uint32_t *device_status, pkv_stream_t stream);
 
-/* The same over an 8-bit and over a 4-bit pool (PKV_ERR_UNSUPPORTED unless head_dim is 128); the workspace is
- * info->workspace_bytes here too. */
+/* The same over an 8-bit pool, and over a 4-bit one (PKV_ERR_UNSUPPORTED unless head_dim is 128 there); the
+ * workspace is info->workspace_bytes here too. */
 pkv_status pkv_attention_sparse_q8(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
                                    const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
                                    int32_t max_slots, int32_t max_blocks_per_slot, int32_t block_size,
@@ -872,8 +874,9 @@ pkv_status pkv_plan_work_tree(const int32_t *cu_seqlens_q, int32_t num_seqs, con
  * largest segment's rows). The masks need not be those of a tree: any set of the
  * step's rows, itself or not. A row that sees nothing gives zeros. Same
  * arguments, results, workspace and ordering rules as pkv_attention (the masks are
- * read at once, like q); `work` and `info` from pkv_plan_work_tree. The keys and values of the slot's rows must be finite:
- * through 0 * infinity a value may reach rows that do not see it.
+ * read at once, like q); `work` and `info` from pkv_plan_work_tree. A key that is
+ * not finite reaches the rows that see it; values must be finite: through
+ * 0 * infinity one may reach rows of its segment that do not see it.
  */
 pkv_status pkv_attention_tree(const void *q, const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q,
                               const int32_t *seq_slot, const int32_t *context_lens, const int32_t *block_tables,
@@ -894,7 +897,10 @@ pkv_status pkv_attention_tree(const void *q, const int32_t *cu_seqlens_q, int32_
  *   paths  int32 [num_seqs][max_path]  device; growing, each below n
  * A path that does not grow or leaves the segment ends there and sets
  * PKV_DEV_BAD_SEGMENT; a block outside the pool is skipped (PKV_DEV_BAD_BLOCK).
- * Two segments of one slot race. `arrays` and `row_bytes` are host arrays.
+ * Two segments of one slot race. `arrays` and `row_bytes` are host arrays. Where
+ * bounds are kept (pkv_key_bounds), those of the blocks that rows moved into are
+ * made anew afterwards: pkv_key_bounds over the step's slot mapping with the
+ * entries behind each segment's accepted rows set to -1.
  */
 pkv_status pkv_accept_rows(const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q, const int32_t *seq_slot,
                            const int32_t *context_lens, const int32_t *block_tables, int32_t max_slots,

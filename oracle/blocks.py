@@ -12,8 +12,6 @@ from __future__ import annotations
 
 import numpy as np
 
-from oracle import scoremod as SM
-
 
 def bounds(k):
     """[2, Hkv, D]: smallest and largest value of each channel over the rows of k [rows, Hkv, D]."""
@@ -55,14 +53,30 @@ def tree_seen(parents, L):
 
 
 def attention(q, k, v, seen, scale, *, k_mag=None, v_mag=None):
-    """(out [n, Hq, D], tolerance) of q over k, v [L, Hkv, D], row i seeing the keys seen[i]."""
-    out, tol = np.zeros(q.shape), np.zeros(q.shape)
-    for i in range(q.shape[0]):
-        keys = np.flatnonzero(seen[i])
-        if not len(keys):
-            continue
-        pick = lambda x: None if x is None else x[keys]  # noqa: E731
-        o, t = SM.attention(q[i:i + 1], k[keys], v[keys], [len(keys) - 1], [0], [len(keys)], scale, k_mag=pick(k_mag),
-                            v_mag=pick(v_mag))
-        out[i], tol[i] = o[0], t[0]
+    """(out [n, Hq, D], tolerance) of q over k, v [L, Hkv, D], row i seeing the keys seen[i]. The tolerance is that of
+    ``oracle.scoremod.attention`` without a cap or a bias, its sums and maxima taken over the keys that a row sees."""
+    n, hq, d = q.shape
+    out, tol = np.zeros((n, hq, d)), np.zeros((n, hq, d))
+    q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
+    keys = np.flatnonzero(seen.any(0))
+    if not len(keys):
+        return out, tol
+    seen, k, v = seen[:, keys], k[keys], v[keys]
+    k_mag = np.abs(k) if k_mag is None else k_mag[keys]
+    for h in range(hq):
+        g = h // (hq // k.shape[1])
+        x = q[:, h] @ k[:, g].T * scale
+        e = np.abs(q[:, h]) @ k_mag[:, g].T * scale * d * 2.0 ** -23 + np.abs(x) * 2.0 ** -22
+        x = np.where(seen, x, -np.inf)
+        top = x.max(1, keepdims=True)
+        w = np.exp(x - np.where(np.isfinite(top), top, 0.0))
+        total = w.sum(1, keepdims=True)
+        u = w / np.where(total > 0, total, 1.0)
+        o, size = u @ v[:, g], u @ np.abs(v[:, g])
+        off = (u * e).sum(1, keepdims=True) + e.max(1, keepdims=True, where=seen, initial=0.0) \
+            + (seen.sum(1, keepdims=True) + 16) * 2.0 ** -24 + 2.0 ** -22
+        out[:, h] = o
+        tol[:, h] = 1.02 * (2.0 ** -8 * (size + 2 * np.abs(o)) + off * (size + np.abs(o)))
+        if v_mag is not None:
+            tol[:, h] += 2.0 ** -19 * (u @ v_mag[keys, g])
     return out, tol

@@ -197,6 +197,54 @@ def test_sparse_attention_refuses_other_lists():
                            1 << 30, None, None) == 1
 
 
+def test_sparse_list_limits():
+    """2^20 blocks to choose among are planned, more are refused."""
+    shape = dict(max_slots=1, max_blocks_per_slot=2 ** 21, block_size=16, num_q_heads=8, num_kv_heads=2, head_dim=64)
+    fixed = 2  # the first block and that of the step's row
+    for blocks, ok in ((2 ** 20 + fixed, True), (2 ** 20 + fixed + 1, False)):
+        args = ([0, 1], [0], np.array([blocks * 16], np.int32))
+        if ok:
+            info = B.pkv_plan_work_sparse(*args, **shape, sparse=B.Sparse(64, 1, 0))[1]
+            assert info.num_scratch_items == 2 ** 20 // 128
+            continue
+        with pytest.raises(B.PkvError) as e:
+            B.pkv_plan_work_sparse(*args, **shape, sparse=B.Sparse(64, 1, 0))
+        assert B.STATUS_NAMES[e.value.status] == "PKV_ERR_UNSUPPORTED"
+
+
+def test_tree_attention_refuses_what_does_not_fit():
+    """Other planners' lists, masks that are too narrow or too wide, missing or odd buffers: refused before any launch."""
+    L = B._lib()
+    ctx = np.full(9, 3000, np.int32)
+    info = B.pkv_plan_work_tree([0, 40], [0], ctx, **SHAPE)[1]
+    p = ctypes.c_void_p(1 << 20)  # never followed
+
+    def attend(info=info, q=p, k=p, v=p, masks=p, words=2, out=p, ws=p, ws_bytes=1 << 30, d=64, bs=16, hq=8, total=40, cu=p):
+        return B.STATUS_NAMES[L.pkv_attention_tree(q, cu, 1, total, p, p, p, 9, 200, bs, k, v, 4000, hq, 2, d, 0.0, masks, words,
+                                                   p, ctypes.byref(info), out, ws, ws_bytes, None, None)]
+
+    bad = "PKV_ERR_INVALID_ARG"
+    for other in (B.pkv_plan_work([0, 1], [0], ctx, **SHAPE)[1],
+                  B.pkv_plan_work_sparse([0, 1], [0], ctx, **SHAPE, sparse=B.Sparse(8))[1]):
+        assert attend(other) == bad
+    assert attend(words=1) == bad and attend(words=0) == bad and attend(words=9) == bad
+    for field in ("q", "k", "v", "masks", "out", "cu"):
+        assert attend(**{field: None}) == bad
+    for field in ("q", "k", "v", "out"):
+        assert attend(**{field: ctypes.c_void_p(1 << 20 | 8)}) == bad
+    assert attend(masks=ctypes.c_void_p(1 << 20 | 2)) == bad
+    assert attend(d=96) == "PKV_ERR_UNSUPPORTED" and attend(bs=8) == "PKV_ERR_UNSUPPORTED"
+    assert attend(ws=None) == "PKV_ERR_WORKSPACE_TOO_SMALL" and attend(ws_bytes=255) == "PKV_ERR_WORKSPACE_TOO_SMALL"
+    assert attend(ws=ctypes.c_void_p(1 << 20 | 16)) == "PKV_ERR_WORKSPACE_TOO_SMALL"
+    for field in ("num_decode_items", "num_prefill_items", "num_scratch_items", "num_partials", "decode_rows_max"):
+        wrong = B.WorkInfo.from_buffer_copy(info)
+        setattr(wrong, field, -1)
+        assert attend(wrong) == bad
+    assert attend(total=0) == "PKV_OK"
+    empty = B.pkv_plan_work_tree([0, 0], [0], ctx, **SHAPE)[1]
+    assert attend(empty, q=None, masks=None) == "PKV_OK"
+
+
 def test_bounds_and_accept_refusals():
     L = B._lib()
     p = ctypes.c_void_p(1 << 20)

@@ -366,6 +366,25 @@ def test_attention(kv, i):
             _check(ds, sel, f"{kv} {hq}/{hkv}/{d} {case} {sparse}")
 
 
+@pytest.mark.parametrize("kv", ["bf16", "q8"])
+def test_blocks_that_are_not_chosen_may_hold_anything(kv):
+    """Keys, values and scales that are no numbers in every block that the step does not read."""
+    w = W.random_step(17, [(1, 3000), (3, 1111), (1, 90)], num_q_heads=8, num_kv_heads=2, head_dim=128)
+    ds = R.prepare(w, kv=kv)
+    R.run_cache_write(ds)
+    sparse = B.Sparse(7, 1, 1)
+    sel = _any_choice(w, sparse, 3)
+    sel[:] = sel[:, :1]  # the same blocks for both heads
+    read = {int(w.blocks[s.slot][p]) for i, s in enumerate(w.segments) for p in sel[i, 0] if p >= 0}
+    rest = torch.tensor([b for b in range(w.num_blocks) if b not in read], device="cuda")
+    for a in _pool(ds):
+        a[rest] = float("nan") if a.is_floating_point() else 127
+    plan = _plan(ds, sparse)
+    _attend_call(ds, sparse, plan, torch.from_numpy(sel).cuda())()
+    assert B.pkv_check_device_status(ds.status) == 0
+    _check(ds, sel, kv)
+
+
 def test_all_blocks_are_plain_attention():
     w = W.random_step(9, [(1, 3000), (4, 777), (1, 1)], num_q_heads=32, num_kv_heads=8, head_dim=128)
     ds = R.prepare(w)

@@ -379,3 +379,98 @@ def test_a_verification_step():
     for o in (out[path], line):
         assert (np.abs(o.double().cpu().numpy() - want) <= tol).all()
     assert (depths[path] == np.arange(len(path))).all()
+
+
+def test_bounds_behind_an_accepted_path():
+    """A tree whose accepted rows move over block ends: bounds made anew for those rows, and the choice that follows."""
+    bs, hq, hkv, d, hist, n = 16, 8, 2, 128, 250, 40
+    path = [0, 2, 3, 9, 11, 12, 20, 21, 33, 39]
+    x = lambda *s: torch.randn(*s, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    k, v, q = x(hist + n + 1, hkv, d), x(hist + n + 1, hkv, d), x(1, hq, d)
+    kv, status = R.empty_pool(32, hkv, bs, d, "cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    bounds = torch.full((32, hkv, 2, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    pool = B.Pool(32, bs, 1, 20)
+    pool.admit(0, 0)
+
+    def write(first, count):
+        low = pool.lower([(0, count)])
+        m = dev(low.slot_mapping)
+        B.pkv_cache_write(k[first:first + count], v[first:first + count], m, *kv)
+        B.pkv_key_bounds(m, kv[0], bounds, device_status=status)
+        return low
+
+    write(0, hist)
+    low = write(hist, n)
+    meta = [dev(a) for a in (low.cu_seqlens_q, low.seq_slot, low.context_lens, pool.block_tables())]
+    B.pkv_accept_rows(*meta, torch.tensor([path + [-1]], dtype=torch.int32, device="cuda"), kv, total_q=n, device_status=status)
+    kept = low.slot_mapping.copy()
+    kept[len(path):] = -1
+    B.pkv_key_bounds(dev(kept), kv[0], bounds, device_status=status)
+    pool.truncate(0, hist + len(path))
+    low = write(hist + n, 1)
+    keys = k[list(range(hist)) + [hist + p for p in path] + [hist + n]].double().cpu().numpy()
+    want = np.stack([OB.bounds(keys[i:i + bs]) for i in range(0, len(keys), bs)])  # [blocks, 2, heads, D]
+    table = pool.block_tables()[0][: len(want)]
+    assert np.array_equal(bounds[torch.from_numpy(table).cuda().long()].double().cpu().numpy(), want.transpose(0, 2, 1, 3))
+
+    sparse = B.Sparse(6, 1, 1)
+    work, info = B.pkv_plan_work_sparse(low.cu_seqlens_q, low.seq_slot, low.context_lens, max_slots=1, max_blocks_per_slot=20,
+                                        block_size=bs, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, sparse=sparse)
+    sel = torch.empty(1, hkv, 6, dtype=torch.int32, device="cuda")
+    ws, out = torch.empty(info.workspace_bytes, dtype=torch.uint8, device="cuda"), torch.empty_like(q)
+    meta = [dev(a) for a in (low.cu_seqlens_q, low.seq_slot, low.context_lens, pool.block_tables())]
+    B.pkv_select_blocks(q, *meta, bounds, dev(work), info, sel, ws, sparse=sparse, block_size=bs, device_status=status)
+    B.pkv_attention_sparse(q, *meta, *kv, sel, dev(work), info, out, ws, sparse=sparse, device_status=status)
+    assert B.pkv_check_device_status(status) == 0
+    vals = v[list(range(hist)) + [hist + p for p in path] + [hist + n]].double().cpu().numpy()
+    q64, g = q.double().cpu().numpy(), hq // hkv
+    for h in range(hkv):
+        places = OB.choose(q64[:, h * g:(h + 1) * g], want[:, 0, h], want[:, 1, h], len(keys), bs, 6, 1, 1)
+        assert sel[0, h].tolist() == places
+        seen = np.isin(np.arange(len(keys)) // bs, places)[None]
+        o, tol = OB.attention(q64[:, h * g:(h + 1) * g], keys[:, h:h + 1], vals[:, h:h + 1], seen, d ** -0.5)
+        assert (np.abs(out[:, h * g:(h + 1) * g].double().cpu().numpy() - o) <= tol).all()
+
+
+def test_two_streams_at_once():
+    """Trees on one stream and a block-sparse step on another, each with a workspace of its own."""
+    w = W.random_step(14, [(16, 6000), (40, 3000)], num_q_heads=32, num_kv_heads=8, head_dim=128)
+    w1 = W.random_step(15, [(1, 9000), (2, 5000)], num_q_heads=32, num_kv_heads=8, head_dim=128)
+    ds, d1 = R.prepare(w), R.prepare(w1)
+    for s in (ds, d1):
+        R.run_cache_write(s)
+    masks, _ = B.pkv_tree_masks(_parents(np.random.default_rng(0), [16, 40]), ds.lowered.cu_seqlens_q)
+    tree, _ = _call(ds, masks)
+    low, sparse = d1.lowered, B.Sparse(64)
+    work, info = B.pkv_plan_work_sparse(low.cu_seqlens_q, low.seq_slot, low.context_lens, max_slots=w1.max_slots,
+                                        max_blocks_per_slot=w1.max_blocks_per_slot, block_size=16, num_q_heads=32,
+                                        num_kv_heads=8, head_dim=128, sparse=sparse)
+    bounds = torch.randn(w1.num_blocks, 8, 2, 128, device="cuda").sort(2).values.bfloat16()
+    sel = torch.empty(2, 8, 64, dtype=torch.int32, device="cuda")
+    ws, work = torch.empty(info.workspace_bytes, dtype=torch.uint8, device="cuda"), torch.from_numpy(work).cuda()
+    meta = (d1.cu_seqlens_q, d1.seq_slot, d1.context_lens, d1.block_tables)
+
+    def choose_and_attend():
+        B.pkv_select_blocks(d1.q, *meta, bounds, work, info, sel, ws, sparse=sparse, block_size=16, device_status=d1.status)
+        B.pkv_attention_sparse(d1.q, *meta, d1.k_pool, d1.v_pool, sel, work, info, d1.out, ws, sparse=sparse,
+                               device_status=d1.status)
+
+    tree()
+    choose_and_attend()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (ds.out, sel, d1.out)]
+    ds.out.fill_(9.0)
+    d1.out.fill_(9.0)
+    sel.fill_(0)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        with torch.cuda.stream(a):
+            tree()
+        with torch.cuda.stream(b):
+            choose_and_attend()
+    torch.cuda.synchronize()
+    for got, t in zip((ds.out, sel, d1.out), want):
+        assert torch.equal(got, t)
+    assert B.pkv_check_device_status(ds.status) == 0 and B.pkv_check_device_status(d1.status) == 0
