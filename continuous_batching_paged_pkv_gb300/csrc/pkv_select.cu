@@ -31,10 +31,11 @@
 // whatever the order of the sums, and every run gives the same. Then the chosen places
 // are written in growing order.
 //
-// 256 slots x 8 heads of 512 to 16384 keys in blocks of 32, 64 chosen: 43 us, the
-// scores 29 of them (150 MB, 5.2 TB/s); five slots of up to 131072 keys in blocks of
-// 16, 128 chosen: 32 us, the scores 20. The rest is the choosing kernel's chain of
-// loads, histograms and, in a CTA of seven there, an exact sum (5 us).
+// 256 slots x 8 heads of 512 to 16384 keys in blocks of 32, 64 chosen: 40.5 us, for
+// 150 MB of bounds; five slots of up to 131072 keys in blocks of 16, 128 chosen: 30
+// us, 86 MB (42.9 and 32.8 where the scoring warps look their first blocks up behind
+// the wait for the kernel before). The choosing kernel's chain of loads, histograms
+// and, in a CTA of seven there, an exact sum (5 us) is 12 to 14 us of them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -99,8 +100,6 @@ __global__ void __launch_bounds__(384, 1) score_blocks_kernel(const StepArgs a, 
                                                               const int32_t *__restrict__ items, int num_items,
                                                               int64_t candidates, float *__restrict__ scores,
                                                               float *__restrict__ sums) {
-  grid_dependency_wait();  // q and the bounds come from earlier work
-  launch_dependents();
   constexpr int P = D / 32;                          // 32-value pieces of a row of lo (or hi), and of q
   constexpr int kPerItem = kScoreBlocks / kScoreGroup;
   constexpr bool kQAhead = NT == 1;                  // two columns' q would not fit beside the bounds
@@ -202,6 +201,10 @@ __global__ void __launch_bounds__(384, 1) score_blocks_kernel(const StepArgs a, 
   Place ahead = at;
   advance(ahead);
   int4 next_item = item_of(ahead);
+  // The list, the metadata and the block tables are final when this grid starts; q and the bounds come from earlier
+  // work. The choosing kernel may start once that has finished.
+  grid_dependency_wait();
+  launch_dependents();
   load_half(lo, A, 0);
   load_half(hi, A, 1);
   if constexpr (kQAhead) load_q(qa[0], A, 0);
