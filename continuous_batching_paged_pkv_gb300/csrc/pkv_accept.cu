@@ -6,7 +6,7 @@
 // pool array, kv head), reads some rows before it writes any of them (four loads a
 // lane: eight bf16 rows of 128), and goes through the path in order; nothing else
 // touches these rows. Bound by latency (metadata, path, block table, row): a step
-// moves a few rows per slot. Up to 6 of 32 nodes in 256 slots x 8 heads: 3.8 us
+// moves a few rows per slot. Up to 6 of 32 nodes in 256 slots x 8 heads: 3.7 us
 // (5.8 with eight loads a lane, whose registers leave half as many warps to an SM).
 #include <cuda_runtime.h>
 
@@ -53,13 +53,16 @@ __device__ __forceinline__ void move_rows(uint8_t *base, int64_t row_bytes, int 
 
 __global__ void __launch_bounds__(128) accept_rows_kernel(const AcceptArgs a) {
   // The next kernel may read the rows that move here as history, before its own wait: it must not start before
-  // they are in place, so this one gives no early signal.
-  grid_dependency_wait();
+  // they are in place, so this one gives no early signal. The metadata and the paths are final when it starts; it
+  // waits for the kernel before it ahead of the rows, and before it ends.
   const int lane = threadIdx.x & 31;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
   const int per_seg = a.num_arrays * a.num_kv_heads;
   const int64_t seg = unit / per_seg;
-  if (seg >= a.num_seqs) return;
+  if (seg >= a.num_seqs) {
+    grid_dependency_wait();
+    return;
+  }
   const int arr = static_cast<int>(unit % per_seg) / a.num_kv_heads, h = static_cast<int>(unit % per_seg) % a.num_kv_heads;
   const bool reports = unit % per_seg == 0 && lane == 0 && a.status;
   const int row0 = __ldg(a.cu_seqlens_q + seg), n = __ldg(a.cu_seqlens_q + seg + 1) - row0, slot = __ldg(a.seq_slot + seg);
@@ -68,6 +71,7 @@ __global__ void __launch_bounds__(128) accept_rows_kernel(const AcceptArgs a) {
   ok = ok && n <= L && L <= static_cast<int64_t>(a.max_blocks_per_slot) * a.block_size;
   if (!ok) {
     if (reports) atomicOr(a.status, PKV_DEV_BAD_SEGMENT);
+    grid_dependency_wait();
     return;
   }
   const int32_t *path = a.paths + seg * a.max_path;
@@ -97,6 +101,7 @@ __global__ void __launch_bounds__(128) accept_rows_kernel(const AcceptArgs a) {
       }
     }
     if (bad && unit % per_seg == 0 && a.status) atomicOr(a.status, PKV_DEV_BAD_BLOCK);
+    if (d0 == 0) grid_dependency_wait();
     if (row_bytes % 16 == 0)
       move_rows<uint4>(base, row_bytes, count, lane, from, to);
     else if (row_bytes % 8 == 0)

@@ -13,8 +13,9 @@
 // a row over head_dim / 8 lanes, several rows per instruction, packed bf16 minima
 // and maxima, the lanes of one channel joined by shuffles. Block rows are read once
 // (they were written just before, and often come from L2). 24,500 packed tokens,
-// 8 heads of 128: 50 MB of keys in 11.8 us, bound by the ramp of one wave of warps
-// and then HBM; 64 tokens: 3.4 us, a launch and its chain (mapping, rows, store).
+// 8 heads of 128: 50 MB of keys in 11.0 us, bound by the ramp of one wave of warps
+// and then HBM; 64 tokens: 3.1 us, a launch and its chain (rows, store; 11.8 and 3.4
+// us where the mapping is read behind the wait for the kernel before).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -72,8 +73,6 @@ __global__ void __launch_bounds__(64) key_bounds_kernel(const int64_t *__restric
                                                          uint4 *__restrict__ bounds, int64_t pool_rows,
                                                          int32_t block_size, int32_t num_kv_heads, int32_t chunk,
                                                          uint32_t *__restrict__ status) {
-  grid_dependency_wait();  // the keys and the mapping come from earlier work
-  launch_dependents();     // as the cache write: everything before this kernel has finished
   constexpr int V = D / 8;          // 16-byte vectors of a row
   constexpr int R = 32 / V;         // rows per instruction
   constexpr int U = 8;              // loads in flight per lane
@@ -81,8 +80,7 @@ __global__ void __launch_bounds__(64) key_bounds_kernel(const int64_t *__restric
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
   const int64_t t0 = unit / num_kv_heads * chunk;
   const int h = static_cast<int>(unit % num_kv_heads);
-  if (t0 >= num_tokens) return;
-  const int count = static_cast<int>(min(static_cast<int64_t>(chunk), num_tokens - t0));
+  const int count = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(chunk), num_tokens - t0)));
   // lane l: token t0 + l, and whether its block's run ends with it
   int64_t s = -1;
   bool last = false;
@@ -95,6 +93,8 @@ __global__ void __launch_bounds__(64) key_bounds_kernel(const int64_t *__restric
     }
     last = s >= 0 && (next < 0 || next / block_size != s / block_size);
   }
+  grid_dependency_wait();  // the mapping is final when this grid starts, the keys come from earlier work
+  launch_dependents();     // as the cache write: everything before this kernel has finished
   for (uint32_t todo = __ballot_sync(kAll, last); todo; todo &= todo - 1) {
     const int64_t at = __shfl_sync(kAll, s, __ffs(todo) - 1);
     const int64_t bh = at / block_size * num_kv_heads + h;
@@ -130,7 +130,7 @@ cudaError_t launch_key_bounds(const int64_t *slot_mapping, int64_t num_tokens, c
                               int32_t head_dim, int32_t bits, uint32_t *status, cudaStream_t stream) {
   // Tokens per warp: one while that keeps the SMs from being full, up to 16 where most tokens do not end a block and
   // would only cost a warp each. CTAs of two warps, so that an SM's next ones start as soon as some end: 24,500
-  // tokens x 8 heads in blocks of 16 take 11.8 us (12.3 with eight warps; 12.6 with 32 tokens per warp).
+  // tokens x 8 heads in blocks of 16 took 11.8 us so (12.3 with eight warps; 12.6 with 32 tokens per warp).
   int32_t chunk = 1;
   while (chunk < 16 && num_tokens * num_kv_heads / chunk > 152 * 32) chunk *= 2;
   const int64_t units = (num_tokens + chunk - 1) / chunk * num_kv_heads;

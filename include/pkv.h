@@ -719,7 +719,8 @@ pkv_status pkv_attention_mod_q4(const void *q, const int32_t *cu_seqlens_q, int3
  * mapping, which of its ends wins is undefined. Exact: a bound is one of the
  * keys' values. The keys have to be finite. Rows >= num_blocks * block_size are
  * skipped and set PKV_DEV_BAD_SLOT_MAPPING. Run behind the cache write, on its
- * stream; pointers 16-byte aligned.
+ * stream; the mapping is read at once (as pkv_attention reads its metadata).
+ * Pointers 16-byte aligned.
  */
 pkv_status pkv_key_bounds(const int64_t *slot_mapping, int64_t num_tokens, const void *k_pool, int64_t num_blocks,
                           int32_t block_size, int32_t num_kv_heads, int32_t head_dim, void *bounds,
@@ -900,7 +901,9 @@ pkv_status pkv_attention_tree(const void *q, const int32_t *cu_seqlens_q, int32_
  * Two segments of one slot race. `arrays` and `row_bytes` are host arrays. Where
  * bounds are kept (pkv_key_bounds), those of the blocks that rows moved into are
  * made anew afterwards: pkv_key_bounds over the step's slot mapping with the
- * entries behind each segment's accepted rows set to -1.
+ * entries behind each segment's accepted rows set to -1. The metadata and the
+ * paths are read at once (as pkv_attention reads its metadata), the rows after
+ * the kernel before; the next kernel starts when they are in place.
  */
 pkv_status pkv_accept_rows(const int32_t *cu_seqlens_q, int32_t num_seqs, int64_t total_q, const int32_t *seq_slot,
                            const int32_t *context_lens, const int32_t *block_tables, int32_t max_slots,
