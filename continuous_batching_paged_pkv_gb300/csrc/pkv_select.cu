@@ -23,7 +23,8 @@
 //
 // Choosing kernel: a CTA per (segment, kv head), of 4 warps or, where segments have
 // many candidates, 32. A bound T that exactly k scores reach, or else the k-th largest
-// score, comes from histograms of the ordered scores' digits. With E the error bound,
+// score, comes from histograms of the ordered scores' digits and, as soon as few agree
+// with it so far, from their ranks. With E the error bound,
 // what is above T + 2 E is in (its exact score is above T + E, and fewer than k are),
 // what is below T - 2 E is out (k others have exact scores from T - E on), and only the
 // blocks between are summed again, in fp64 (products of two bf16 are exact there), and
@@ -31,11 +32,12 @@
 // whatever the order of the sums, and every run gives the same. Then the chosen places
 // are written in growing order.
 //
-// 256 slots x 8 heads of 512 to 16384 keys in blocks of 32, 64 chosen: 40.5 us, for
-// 150 MB of bounds; five slots of up to 131072 keys in blocks of 16, 128 chosen: 30
-// us, 86 MB (42.9 and 32.8 where the scoring warps look their first blocks up behind
-// the wait for the kernel before). The choosing kernel's chain of loads, histograms
-// and, in a CTA of seven there, an exact sum (5 us) is 12 to 14 us of them.
+// 256 slots x 8 heads of 512 to 16384 keys in blocks of 32, 64 chosen: 39.6 us, for
+// 150 MB of bounds; five slots of up to 131072 keys in blocks of 16, 128 chosen: 28.4
+// to 29.6 us, 86 MB (2.3 to 3 us more where the scoring warps look their first blocks
+// up behind the wait for the kernel before; 1 and 0.2 with digits alone). The choosing
+// kernel's chain of loads, histograms and, in a CTA of seven there, an exact sum (4
+// us) is 11 to 13 us of them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -304,34 +306,46 @@ __device__ __forceinline__ uint64_t ordered(double x) {
 
 constexpr int kListed = 256;  // blocks between the bounds that are ranked in shared memory
 
-// Sums and minima over T threads; two buffers, so that one barrier per sum is enough.
+// Sums and maxima over T threads, up to three of them behind one barrier; two buffers, so that one is enough.
 template <int T>
 struct Block {
-  uint32_t (*buf)[32];
+  uint32_t (*buf)[3][32];
   int turn;
-  template <typename Op>
-  __device__ __forceinline__ uint32_t reduce(uint32_t x, uint32_t none, Op op) {
-    const uint32_t w = op(x);
+  template <typename Op, typename... X>
+  __device__ __forceinline__ void reduce(Op op, X &...x) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     turn ^= 1;
-    if (lane == 0) buf[turn][warp] = w;
+    int i = 0;
+    (
+        [&] {
+          const uint32_t w = op(x);
+          if (lane == 0) buf[turn][i++][warp] = w;
+        }(),
+        ...);
     __syncthreads();
-    return op(lane < T / 32 ? buf[turn][lane] : none);
+    i = 0;
+    ((x = op(lane < T / 32 ? buf[turn][i++][lane] : 0u)), ...);
+  }
+  template <typename... X>
+  __device__ __forceinline__ void sums(X &...x) {
+    reduce([](uint32_t v) { return __reduce_add_sync(kAll, v); }, x...);
+  }
+  template <typename... X>
+  __device__ __forceinline__ void maxima(X &...x) {
+    reduce([](uint32_t v) { return __reduce_max_sync(kAll, v); }, x...);
   }
   __device__ __forceinline__ uint32_t sum(uint32_t x) {
-    return reduce(x, 0u, [](uint32_t v) { return __reduce_add_sync(kAll, v); });
-  }
-  __device__ __forceinline__ uint32_t least(uint32_t x) {
-    return reduce(x, ~0u, [](uint32_t v) { return __reduce_min_sync(kAll, v); });
+    sums(x);
+    return x;
   }
   // Sum over the warps before this one of x's sums over a warp.
   __device__ __forceinline__ uint32_t warps_before(uint32_t x) {
     const uint32_t w = __reduce_add_sync(kAll, x);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     turn ^= 1;
-    if (lane == 0) buf[turn][warp] = w;
+    if (lane == 0) buf[turn][0][warp] = w;
     __syncthreads();
-    return __reduce_add_sync(kAll, lane < warp ? buf[turn][lane] : 0u);
+    return __reduce_add_sync(kAll, lane < warp ? buf[turn][0][lane] : 0u);
   }
 };
 
@@ -401,10 +415,10 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
   // call); only the scores need the scoring kernel to finish. Every path waits for it, so that the grid ends after it.
   launch_dependents();
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t s_buf[2][32];
+  __shared__ uint32_t s_buf[2][3][32];
   __shared__ int s_list[kListed];
   __shared__ double s_exact[kListed];
-  __shared__ uint32_t s_listed, s_hist[256], s_digit[3];
+  __shared__ uint32_t s_listed, s_same, s_hist[256], s_digit[3];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.y;
   const int4 it = __ldg(reinterpret_cast<const int4 *>(items) + blockIdx.x);
   const int base = it.z, N = it.w;
@@ -457,8 +471,8 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
       sc[j] = __uint_as_float(chosen ? 0x7FFFFFFFu : ~0u);
   };
   Block<T> block{s_buf, 0};
-  // largest sum of magnitudes; least and largest score
-  uint32_t mag = 0, least = ~0u, most = 0u;
+  // largest sum of magnitudes; least (its complement) and largest score
+  uint32_t mag = 0, least = 0u, most = 0u;
   const float *group_sums = sums + sum_index(base, a.num_kv_heads, g, N);
   for (int i = tid; i < (N + kScoreGroup - 1) / kScoreGroup; i += T) mag = max(mag, __float_as_uint(__ldcg(group_sums + i)));
   for (int j0 = w0 + lane; j0 < w1; j0 += 8 * 32) {
@@ -469,18 +483,16 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
     for (int i = 0; i < 8; ++i) {
       const uint32_t k = ordered(v[i]);
       if (resident && j0 + i * 32 < w1) keys[j0 + i * 32] = k;
-      least = min(least, k), most = max(most, k);
+      least = max(least, ~k), most = max(most, k);
     }
   }
-  if (tid == 0) s_listed = 0;
-  __syncthreads();
-  const float error = __uint_as_float(~block.least(~mag)) * kScoreError + 0x1p-100f;
-  least = block.least(least);
-  most = ~block.least(~most);
+  if (tid == 0) s_listed = s_same = 0;
+  block.maxima(mag, least, most);
+  const float error = __uint_as_float(mag) * kScoreError + 0x1p-100f;
   // x: a bound that `need` candidates reach and no larger one does, or that exactly `need` reach. Eight bits at a
   // time below the bits that all share: a histogram of the candidates that agree with x so far, and the digit of
   // the `left`-th largest of them.
-  const int bits = 32 - __clz(least ^ most);
+  const int bits = 32 - __clz(~least ^ most);
   uint32_t x = bits == 32 ? 0u : most >> bits << bits, left = need;
   for (int shift = bits; shift > 0;) {
     const int width = min(shift, 8), top = shift;
@@ -517,7 +529,26 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
     __syncthreads();
     x |= s_digit[0] << shift;
     left = s_digit[1];
-    if (s_digit[2] == left) break;
+    const uint32_t same = s_digit[2];
+    if (same == left) break;
+    if (shift > 0 && same <= kListed) {  // few agree with x so far: ranked at once
+      each([&](int, uint32_t k, bool live) {
+        if (live && k >> shift == x >> shift) s_list[atomicAdd(&s_same, 1u)] = static_cast<int>(k);
+      });
+      __syncthreads();
+      for (uint32_t i = tid; i < same; i += T) {
+        const uint32_t k = static_cast<uint32_t>(s_list[i]);
+        uint32_t above = 0, reach = 0;
+        for (uint32_t o = 0; o < same; ++o) {
+          above += static_cast<uint32_t>(s_list[o]) > k;
+          reach += static_cast<uint32_t>(s_list[o]) >= k;
+        }
+        if (above < left && left <= reach) s_digit[0] = k;
+      }
+      __syncthreads();
+      x = s_digit[0];
+      break;
+    }
   }
   const float T0 = unordered(x);
   float low = __fsub_rd(T0, 2.f * error), high = __fadd_ru(T0, 2.f * error);
@@ -530,8 +561,8 @@ __global__ void __launch_bounds__(T) choose_blocks_kernel(const StepArgs a, cons
     between += live && k >= klow && k <= khigh;
   });
   uint32_t mine = over + between;  // of this thread, where all between the bounds are in
-  over = block.sum(over);
-  const uint32_t m = block.sum(between), r = need - over;  // r of m
+  block.sums(over, between);
+  const uint32_t m = between, r = need - over;  // r of m
   uint32_t from = klow;  // scores from here on are chosen
   if (m != r) {
     from = khigh + 1;  // what is settled is above or below
