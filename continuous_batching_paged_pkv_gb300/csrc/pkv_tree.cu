@@ -110,6 +110,16 @@ __device__ __forceinline__ uint32_t mask_word(const uint32_t *mask, int words, i
   return n - k * 32 >= 32 ? m : m & ((1u << (n - k * 32)) - 1u);
 }
 
+// Whether a row sees any of the places [r0, r1) among its segment's nodes, negative ones in the history. r1 - r0 is a
+// multiple of 32, or r1 is the segment's end.
+__device__ __forceinline__ bool sees_some(const uint32_t *mask, int words, int n, int r0, int r1) {
+  if (r0 < 0) return true;
+#pragma unroll 1
+  for (int r = r0; r < r1; r += 32)
+    if (__funnelshift_r(mask_word(mask, words, n, r >> 5), mask_word(mask, words, n, (r >> 5) + 1), r & 31)) return true;
+  return false;
+}
+
 // Position in the ring of slots.
 template <int N>
 struct Ring {
@@ -448,7 +458,10 @@ __global__ void __maxnreg__((Cfg<D, W>::kLaunchRegs))
         tc_fence_after();
         grid_dependency_wait();  // the kernel before may write the same output or use the same workspace
         const float l = l_sum + l_odd;
-        const bool unseen = m_used == -INFINITY;  // no key of the span: zeros, whatever O holds
+        // A row that sees no key of the span gives zeros, whatever O holds. Its maximum alone does not tell: scores that
+        // are all NaN leave it at -infinity too, and have to come through.
+        const bool unseen = m_used == -INFINITY && !sees_some(mask, a.mask_words, n, base - (L - n), kv_end - (L - n));
+        __syncwarp();
         const bool wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;  // rows of 128 or 256 bytes
         if (pbase < 0) {
           const float inv = unseen ? 0.f : 1.f / l;
@@ -487,7 +500,8 @@ __global__ void __maxnreg__((Cfg<D, W>::kLaunchRegs))
               for (int v = 0; v < 4; ++v) store_32(dst + c * 32 + v * 8, ov + 8 * v);
           }
           if (stored) {
-            // (what every span of a row leaves has a maximum: a segment of several spans has a history)
+            // (the first span of a row has a maximum, unless all its scores are NaN: a segment of several spans has a
+            // history. A later one of the segment's own keys alone may have none, and no weight in the merge.)
             reinterpret_cast<float2 *>(a.partial_ml)[e] = make_float2(m_used, l);
           }
         }

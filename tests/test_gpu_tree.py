@@ -474,3 +474,64 @@ def test_two_streams_at_once():
     for got, t in zip((ds.out, sel, d1.out), want):
         assert torch.equal(got, t)
     assert B.pkv_check_device_status(ds.status) == 0 and B.pkv_check_device_status(d1.status) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("slots", [1, 40])
+def test_keys_and_queries_that_are_not_numbers_reach_the_rows_that_see_them(slots, d):
+    """NaN exactly in the rows that see a NaN key or hold a NaN query, in one span and in several (a lone slot has
+    more); zeros in rows that see nothing, whatever their query; every other row as without them."""
+    rng = np.random.default_rng(d + slots)
+    shapes = [(9, 2500)] if slots == 1 else [(20, 20), (12, 3000), (40, 40), (256, 300), (1, 1)]
+    w = W.random_step(60 + slots, shapes, num_q_heads=8, num_kv_heads=2, head_dim=d, max_slots=slots)
+    sizes = [n for n, _ in shapes]
+    cu = np.concatenate([[0], np.cumsum(sizes)])
+    masks, _ = B.pkv_tree_masks(_parents(rng, sizes, "forest"), cu.astype(np.int32))
+    masks[rng.random(w.total_q) < 0.2] = 0  # rows that see the history alone, or nothing
+    q = W.bf16_bits_to_f32(w.q)
+    bad_q = rng.random(q.shape[:2]) < 0.1
+    clean = w.q.copy()
+    q[bad_q] = np.nan
+    w.q = W.f32_to_bf16_bits(q)
+    expect_nan = np.zeros(q.shape[:2], bool)
+    for i, (s, a) in enumerate(zip(w.segments, cu)):
+        seen = np.concatenate([np.ones((s.q_len, s.ctx - s.q_len), bool), _bits(masks[a:a + s.q_len], s.q_len)], 1)
+        # NaN in one channel of some of the step's own keys
+        bad_k = np.zeros((s.ctx, 2), bool)
+        bad_k[s.ctx - s.q_len:] = rng.random((s.q_len, 2)) < 0.15
+        k = W.bf16_bits_to_f32(w.hist_k[s.slot])
+        k[: s.ctx][bad_k, 5] = np.nan
+        w.hist_k[s.slot][...] = W.f32_to_bf16_bits(k)
+        reach = (seen.astype(int) @ bad_k.astype(int)) > 0  # [rows, kv heads]
+        expect_nan[a:a + s.q_len] = np.repeat(reach, 4, 1) | (bad_q[a:a + s.q_len] & seen.any(1)[:, None])
+    ds = R.prepare(w)
+    R.run_cache_write(ds)
+    call, info = _call(ds, masks)
+    assert info.num_combine_items > 0
+    call()
+    assert B.pkv_check_device_status(ds.status) == 0
+    got = R.out_f32(ds)
+    assert np.array_equal(np.isnan(got), np.repeat(expect_nan[..., None], d, 2))
+    w.q = clean
+    for slot in w.hist_k:  # no row compared below sees these
+        w.hist_k[slot][...] = W.f32_to_bf16_bits(np.nan_to_num(W.bf16_bits_to_f32(w.hist_k[slot])))
+    want, tol = _expect(w, masks)
+    rows = ~expect_nan & ~bad_q
+    assert expect_nan.any() and rows.any() and (np.abs(got - want) <= tol)[rows].all()
+    assert (got[bad_q & ~expect_nan] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_key_that_is_not_a_number_in_the_history_reaches_every_row(d):
+    """Alone in its span, at the end of one and in the middle of another."""
+    for at in (0, 255, 1100):
+        w = W.random_step(70, [(5, 1200), (3, 1200)], num_q_heads=4, num_kv_heads=2, head_dim=d)
+        k = W.bf16_bits_to_f32(w.hist_k[0])
+        k[at, 1] = np.nan
+        w.hist_k[0][...] = W.f32_to_bf16_bits(k)
+        ds = R.prepare(w)
+        R.run_cache_write(ds)
+        masks, _ = B.pkv_tree_masks(_parents(None, [5, 3], "star"), ds.lowered.cu_seqlens_q)
+        _call(ds, masks)[0]()
+        nan = np.isnan(R.out_f32(ds))
+        assert nan[:5, 2:].all() and not nan[:5, :2].any() and not nan[5:].any()
