@@ -277,8 +277,9 @@ inline int32_t prefill_rows_per_tile(int32_t group) { return 128 / group; }
 // more than one, else one: 64 slots x 32 nodes of 8 q heads a kv head (two tiles a tree), up to 8192 keys, take 149 us
 // (163 with one tile everywhere), one slot of 64 nodes of 4, 32,768 keys, 39.8 (42.3); where a tree is one tile, two
 // would leave half of a CTA idle. Spans of kTreeMinSpanTiles to kTreeSpanTiles tiles.
-constexpr int kTreeMaxKeys = INT32_MAX - 4096;  // so that a position behind the last tile is still a number
 constexpr int kTreeTileKeys = 128, kTreeMinSpanTiles = 2, kTreeSpanTiles = 64;
+constexpr int kTreeMaxSpans = 0xFFFF;  // what an item's span and a merge item's count hold
+constexpr int kTreeMaxKeys = kTreeMaxSpans * kTreeSpanTiles * kTreeTileKeys;  // the longest context, in the longest spans
 inline int32_t tree_tiles_per_cta(int32_t rows_max, int32_t group) {
   return rows_max > prefill_rows_per_tile(group) ? 2 : 1;
 }

@@ -158,7 +158,7 @@ pkv_status plan_tree(const int32_t *cu, int32_t num_seqs, const int32_t *seq_slo
     const int64_t tiles = ceil_div(L, pkv::kTreeTileKeys);
     const int64_t span = pkv::tree_span_tiles(tiles, q_tiles, sh.max_slots, sh.num_kv_heads);
     const int64_t spans = ceil_div(tiles, span);
-    if (spans >= (1 << 16) || partials + spans * n > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (spans > pkv::kTreeMaxSpans || partials + spans * n > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     for (int64_t i = 0; i < spans; ++i)
       for (int32_t t = 0; t < q_tiles; t += step) {
         const uint32_t w = static_cast<uint32_t>(i) | static_cast<uint32_t>(span - 1) << 16 | static_cast<uint32_t>(t) << 24;

@@ -854,9 +854,10 @@ pkv_status pkv_tree_masks(const int32_t *parents, const int32_t *cu_seqlens_q, i
 
 /*
  * pkv_plan_work for a step of trees: segments of 1 to PKV_TREE_MAX_ROWS rows,
- * contexts of at most 2^31 - 4097 keys (PKV_ERR_UNSUPPORTED beyond). They may be the last ones of a packed step:
- * cu_seqlens_q then starts above 0. Otherwise the validation, sizes and errors
- * of pkv_plan_work. The keys are cut into spans of whole 128-key tiles; the cut
+ * contexts of at most 536862720 keys, 65535 spans of 8192, and at most 2^31 - 1
+ * partials (spans times rows) in the step (PKV_ERR_UNSUPPORTED beyond either).
+ * They may be the last ones of a packed step: cu_seqlens_q then starts above 0.
+ * Otherwise the validation, sizes and errors of pkv_plan_work. The keys are cut into spans of whole 128-key tiles; the cut
  * depends on the segment and on max_slots, not on the other segments.
  *
  * Item words: decode (segment, slot, span | (128-key tiles in a span - 1) << 16 |

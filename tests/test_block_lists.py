@@ -357,3 +357,17 @@ def test_oracle_attention_by_hand():
     assert np.allclose(out[:, 0], [[3, 4], [0, 0], [2, 3]]) and (tol[1] == 0).all() and (tol[0] > 0).all()
     assert OB.tree_seen([-1, 0, 0, 2], 6).astype(int).tolist() == [
         [1, 1, 1, 0, 0, 0], [1, 1, 1, 1, 0, 0], [1, 1, 1, 0, 1, 0], [1, 1, 1, 0, 1, 1]]
+
+
+def test_tree_list_limits():
+    """Contexts of 65535 spans of 8192 keys are planned, longer ones refused; the spans cover the longest."""
+    shape = dict(max_slots=1, max_blocks_per_slot=2 ** 24, block_size=64, num_q_heads=8, num_kv_heads=2, head_dim=64)
+    longest = 65535 * 8192
+    work, info = B.pkv_plan_work_tree([0, 3], [0], np.array([longest], np.int32), **shape)
+    dec, _, comb, _ = _parts(work, info)
+    assert info.num_partials == 3 * 65535 and (comb[:, 2] & 0xFFFF == 65535).all()
+    assert (dec[:, 2] >> 16 == 63).all() and sorted(dec[:, 2] & 0xFFFF) == list(range(65535))
+    for keys in (longest + 1, 2 ** 30 - 1):
+        with pytest.raises(B.PkvError) as e:
+            B.pkv_plan_work_tree([0, 3], [0], np.array([keys], np.int32), **shape)
+        assert B.STATUS_NAMES[e.value.status] == "PKV_ERR_UNSUPPORTED"
