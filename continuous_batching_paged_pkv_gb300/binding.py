@@ -1047,10 +1047,11 @@ def pkv_copy_blocks(pairs, arrays, *, device_status=None, stream=None) -> None:
 
     ``pairs``: int32 device tensor ``[n, 2]``; ``arrays``: device tensors whose
     first dimension is the block (``[num_blocks, ...]``), all with the same
-    number of blocks (a bf16 pool's K and V, or an 8-bit pool's four arrays)."""
+    number of blocks (a bf16 pool's K and V, or an 8-bit pool's four arrays, and the
+    bounds of its keys)."""
     _need(pairs, "torch.int32", "pairs")
-    if not arrays or len(arrays) > 4:
-        raise ValueError("pkv_copy_blocks takes one to four pool arrays")
+    if not arrays or len(arrays) > 5:
+        raise ValueError("pkv_copy_blocks takes one to five pool arrays")
     nb = arrays[0].shape[0]
     for t in arrays:
         if not t.is_cuda or not t.is_contiguous() or t.shape[0] != nb:

@@ -307,7 +307,7 @@ extern "C" {
 pkv_status pkv_copy_blocks(const int32_t *pairs, int64_t num_pairs, void *const *arrays,
                            const int64_t *block_bytes, int32_t num_arrays, int64_t num_blocks,
                            uint32_t *device_status, pkv_stream_t stream) {
-  if (num_pairs < 0 || num_arrays < 1 || num_arrays > 4 || num_blocks <= 0 || !arrays || !block_bytes)
+  if (num_pairs < 0 || num_arrays < 1 || num_arrays > pkv::kCopyArrays || num_blocks <= 0 || !arrays || !block_bytes)
     return PKV_ERR_INVALID_ARG;
   if (num_pairs == 0) return PKV_OK;
   if (!pairs || !aligned(pairs, 8)) return PKV_ERR_INVALID_ARG;

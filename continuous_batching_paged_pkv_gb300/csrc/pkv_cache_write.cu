@@ -53,14 +53,14 @@ __global__ void __launch_bounds__(256) cache_write_kernel(
   }
 }
 
-// Copy-on-write: whole blocks, source -> destination, in up to four pool
-// arrays at once (mlxcel manual, "Continuous batching", §Paged KV cache and
-// prefix sharing: a shared block branches by copy when a sequence's contents
-// diverge from it). A block is contiguous in every pool array ([block][...]),
+// Copy-on-write: whole blocks, source -> destination, in up to five pool
+// arrays at once (codes and scales of K and V, and the bounds of the keys;
+// mlxcel manual, "Continuous batching", §Paged KV cache and prefix sharing: a
+// shared block branches by copy when a sequence's contents diverge from it). A block is contiguous in every pool array ([block][...]),
 // so one block is block_bytes[a] / 16 consecutive 16-byte vectors.
 struct CopyArrays {
-  uint4 *base[4];
-  int64_t vecs[4];  // 16-byte vectors per block
+  uint4 *base[kCopyArrays];
+  int64_t vecs[kCopyArrays];  // 16-byte vectors per block
   int32_t count;
 };
 

@@ -150,6 +150,7 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream);
 
+constexpr int kCopyArrays = 5;  // most pool arrays of one call
 cudaError_t launch_copy_blocks(const int32_t *pairs, int64_t num_pairs, void *const *arrays,
                                const int64_t *block_bytes, int32_t num_arrays, int64_t num_blocks, uint32_t *status,
                                cudaStream_t stream);

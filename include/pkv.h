@@ -525,10 +525,10 @@ pkv_status pkv_cache_write_q8(const void *k_new, const void *v_new, const int64_
  * Copy-on-write copies ([MX] §Paged KV cache and prefix sharing): for each
  * (source, destination) pair of `pairs` (device, int32 [num_pairs][2], from
  * pkv_pool_take_copies), copy the whole source block over the destination
- * block in each of the `num_arrays` (1 to 4) pool arrays: arrays[a] (device,
+ * block in each of the `num_arrays` (1 to 5) pool arrays: arrays[a] (device,
  * 16-byte aligned) holds num_blocks blocks of block_bytes[a] bytes (a
  * multiple of 16) each -- a bf16 pool's K and V, or an 8-bit pool's codes
- * and scales. `arrays` and `block_bytes` are host arrays. A pair naming a
+ * and scales, and the bounds of the keys where they are kept. `arrays` and `block_bytes` are host arrays. A pair naming a
  * block outside the pool (or the same block twice) is skipped and sets
  * PKV_DEV_BAD_BLOCK. Run before the step's cache write, on its stream.
  */

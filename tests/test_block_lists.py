@@ -371,3 +371,11 @@ def test_tree_list_limits():
         with pytest.raises(B.PkvError) as e:
             B.pkv_plan_work_tree([0, 3], [0], np.array([keys], np.int32), **shape)
         assert B.STATUS_NAMES[e.value.status] == "PKV_ERR_UNSUPPORTED"
+
+
+def test_blocks_are_copied_in_up_to_five_arrays():
+    """A quantised pool's four arrays and the bounds of its keys go in one call."""
+    L, p = B._lib(), ctypes.c_void_p(1 << 20)
+    for n, status in ((4, 0), (5, 0), (6, 1), (0, 1)):
+        arrays, sizes = (ctypes.c_void_p * 6)(*[1 << 20] * 6), (ctypes.c_int64 * 6)(*[1024] * 6)
+        assert L.pkv_copy_blocks(p, 0, arrays, sizes, n, 10, None, None) == status

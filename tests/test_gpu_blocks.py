@@ -621,3 +621,46 @@ def test_calls_refuse_what_does_not_fit():
         B.pkv_key_bounds(ds.slot_mapping, ds.k_pool, bounds[:, :, :, :32].contiguous())
     with pytest.raises(ValueError):
         B.pkv_accept_rows(*meta, torch.zeros(2, 4, dtype=torch.int32, device="cuda"), [ds.k_pool])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "q8", "q4"])
+def test_bounds_of_a_block_that_is_copied_on_write(kv):
+    """Bounds are one more array of the pool: a partly filled block is adopted and then branches. The copy has the
+    block's bounds; the step that follows makes those of its rows; the other table's block keeps its own."""
+    bs, hq, hkv, d, shared = 16, 8, 2, 128, 90
+    x = lambda n: torch.randn(n, hkv, d, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    arrays = R.empty_pool(40, hkv, bs, d, "cuda") if kv == "bf16" else R.empty_pool_q8(40, hkv, bs, d, "cuda", int(kv[1]))
+    bounds = torch.full((40, hkv, 2, d), 77.0, dtype=torch.bfloat16, device="cuda")
+    keys, status = arrays[: len(arrays) // 2], torch.zeros(1, dtype=torch.int32, device="cuda")
+    write = {"bf16": B.pkv_cache_write, "q8": B.pkv_cache_write_q8, "q4": B.pkv_cache_write_q4}[kv]
+    pool = B.Pool(40, bs, 3, 12)
+    pool.admit(0, 0)
+    stored = {}
+
+    def append(slot, n):
+        low = pool.lower([(slot, n)])
+        pairs = pool.take_copies()
+        if len(pairs):
+            B.pkv_copy_blocks(dev(pairs), [*arrays, bounds], device_status=status)
+            src, dst = pairs[0].tolist()
+            assert torch.equal(bounds[dst], bounds[src])
+        k, m = x(n), dev(low.slot_mapping)
+        write(k, x(n), m, *arrays, device_status=status)
+        B.KeyBoundsCall(m, keys, bounds, kv=kv, device_status=status)()
+        bits = k.view(torch.int16).cpu().numpy().view(np.uint16)
+        stored[slot] = np.concatenate([stored[slot], bits]) if slot in stored else bits
+        return len(pairs)
+
+    assert append(0, shared) == 0
+    pool.adopt(1, 0, shared)
+    stored[1] = stored[0].copy()
+    assert append(1, 30) == 1 and append(0, 3) == 0 and append(1, 1) == 0
+    for slot in (0, 1):
+        vals = W.bf16_bits_to_f32(stored[slot]) if kv == "bf16" else KQ.dequantize(*KQ.quantize(stored[slot], int(kv[1])))
+        vals = vals.astype(np.float64)
+        table = pool.block_tables()[slot]
+        for j in range(-(-len(vals) // bs)):
+            want = OB.bounds(vals[j * bs:(j + 1) * bs]).transpose(1, 0, 2)
+            assert np.array_equal(bounds[int(table[j])].double().cpu().numpy(), want), (slot, j)
+    assert B.pkv_check_device_status(status) == 0
