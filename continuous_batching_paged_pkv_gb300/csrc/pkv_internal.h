@@ -271,6 +271,18 @@ cudaError_t allow_smem_once(Kernel *kernel, int smem, std::atomic<uint64_t> &don
   return e;
 }
 
+// Tensor memory. An allocation waits, without a limit, until the SM has the columns. A kernel that lets the next one
+// start before it has allocated its own must therefore never share an SM with a CTA of that one which took them first:
+// it would wait for columns, and the other for its end. Shared memory keeps them apart. Every kernel that allocates
+// takes at least kTmemSmemLeast bytes, so that three CTAs never fit, and one with all 512 columns takes so much that
+// none fits beside it. (A kernel that allocates before it signals has nothing to fear.)
+constexpr int kSmSmem = 228 * 1024, kCtaSmem = 1024;  // of an SM; what each CTA takes beyond its own
+constexpr int kTmemSmemLeast = 99584;
+constexpr bool tmem_apart(int columns, int smem) {
+  return smem >= kTmemSmemLeast && 3 * (kTmemSmemLeast + kCtaSmem) > kSmSmem &&
+         (columns <= 256 || smem + kTmemSmemLeast + 2 * kCtaSmem > kSmSmem);
+}
+
 // Positions per prefill tile: whole GQA groups fit one 128-row MMA tile.
 inline int32_t prefill_rows_per_tile(int32_t group) { return 128 / group; }
 

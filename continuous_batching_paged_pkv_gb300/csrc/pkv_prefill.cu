@@ -128,7 +128,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = blockIdx.y;
-  launch_dependents();
   grid_dependency_wait();  // every input may come from the previous kernel in the stream
   const int4 it = reinterpret_cast<const int4 *>(items)[blockIdx.x];
   const int seg = it.x, slot = it.y, tile = it.z;
@@ -184,6 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Only now: a CTA of the next kernel beside this one could take the tensor memory first and then wait for this grid.
+  launch_dependents();
   const uint32_t tmem = *tmem_slot;
 
   if (warp < 2) {

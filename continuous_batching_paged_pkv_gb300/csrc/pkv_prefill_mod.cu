@@ -66,7 +66,8 @@ constexpr int kBarOffset = (1 + kKStages + kVStages) * kTileBytes;
 constexpr int kRampOffset = kBarOffset + 256;  // after the barriers and flags: the bias step's operands
 template <int MODE>
 constexpr int kSmem = kRampOffset + (ramp_mode(MODE) ? 2 * kRampBytes : 0) + 1024;  // + alignment slack
-static_assert(2 * (kSmem<kModBias> + 1024) <= 228 * 1024, "two CTAs per SM");
+static_assert(2 * (kSmem<kModBias> + 1024) <= kSmSmem, "two CTAs per SM");
+static_assert(tmem_apart(kTmemCols, kSmem<kModMask>), "beside a kernel that it lets start before it has its tensor memory");
 
 enum Bar : int {
   kQFull = 0,

@@ -118,6 +118,8 @@ struct Layout {
 constexpr int kPairStages = 6, kPairStagesTwoGroups = 5;
 static_assert(Layout<kPairStages>::kSmem<1> <= 232448 && Layout<kPairStagesTwoGroups>::kSmem<2> <= 232448,
               "dynamic shared memory per CTA");
+static_assert(tmem_apart(kTmemCols, Layout<kPairStagesBesideDecode>::kSmem<1>),
+              "beside a kernel that it lets start before it has its tensor memory");
 
 // Barrier indices for NST stages.
 template <int NST>

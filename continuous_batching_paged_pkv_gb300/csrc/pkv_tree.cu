@@ -77,7 +77,8 @@ struct Cfg {
   static constexpr int kPReady = kPVDone + 2 * W, kDrain = kPReady + 2 * W, kNumBars = kDrain + 2;
   static_assert(kNumBars * 8 + 8 <= 512, "barriers, TMEM address and abort flag fit their 512 bytes");
   static constexpr int kSmem = kBarOffset + 512;
-  static_assert((W == 1 ? 2 * (kSmem + 1024) : kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
+  static_assert((W == 1 ? 2 * (kSmem + 1024) : kSmem + 1024) <= kSmSmem, "shared memory of an SM");
+  static_assert(tmem_apart(kTmemCols, kSmem), "beside a kernel that it lets start before it has its tensor memory");
 };
 
 // Wait that also gives up as soon as another role of this CTA has aborted, or after a second. The clock is looked at

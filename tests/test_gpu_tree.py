@@ -535,3 +535,43 @@ def test_a_key_that_is_not_a_number_in_the_history_reaches_every_row(d):
         _call(ds, masks)[0]()
         nan = np.isnan(R.out_f32(ds))
         assert nan[:5, 2:].all() and not nan[:5, :2].any() and not nan[5:].any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunks_modified_chunks_and_trees_one_behind_another(d):
+    """Kernels of different shares of tensor memory start under one another's ends: small grids, no call in between."""
+    w = W.random_step(80, [(100, 700), (33, 2000), (256, 256)], num_q_heads=8, num_kv_heads=2, head_dim=d)
+    ds = R.prepare(w)
+    R.run_cache_write(ds)
+    low, meta = ds.lowered, (ds.cu_seqlens_q, ds.seq_slot, ds.context_lens, ds.block_tables, ds.k_pool, ds.v_pool)
+    shape = dict(max_slots=w.max_slots, max_blocks_per_slot=w.max_blocks_per_slot, block_size=16, num_q_heads=8, num_kv_heads=2,
+                 head_dim=d)
+    work, info = B.pkv_plan_work_mod(low.cu_seqlens_q, low.seq_slot, low.context_lens, window=300, **shape)
+    work = torch.from_numpy(work).cuda()
+    ws = torch.empty(max(256, info.workspace_bytes), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(ds.out) for _ in range(3)]
+    masks, _ = B.pkv_tree_masks(_parents(np.random.default_rng(0), [100, 33, 256]), low.cu_seqlens_q)
+    tree, _ = _call(ds, masks, out=outs[2])
+
+    def plain():
+        B.pkv_attention(ds.q, *meta, ds.work, ds.info, outs[0], ds.workspace, scale=ds.scale, device_status=ds.status)
+
+    def modified():
+        B.pkv_attention_mod(ds.q, *meta, work, info, outs[1], ws, mod=B.ScoreMod(window=300), scale=ds.scale,
+                            device_status=ds.status)
+
+    calls = (plain, modified, tree)
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    for order in ((0, 1, 2), (1, 0, 2), (0, 2, 1), (2, 0, 0, 1, 1, 2, 2)):
+        for o in outs:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for i in order:
+                calls[i]()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), order
+    assert B.pkv_check_device_status(ds.status) == 0
