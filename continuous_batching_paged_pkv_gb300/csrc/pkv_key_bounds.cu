@@ -156,6 +156,8 @@ pkv_status key_bounds(int32_t bits, const int64_t *slot_mapping, int64_t num_tok
       num_kv_heads > 65536 || num_blocks > INT64_MAX / block_size)
     return PKV_ERR_INVALID_ARG;
   if ((head_dim != 64 && head_dim != 128) || (bits == 4 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
+  // one grid of CTAs of two warps, 16 tokens a warp where there are so many
+  if ((num_tokens + 15) / 16 * num_kv_heads > 2ll * INT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (num_tokens == 0) return PKV_OK;
   if (!slot_mapping || !keys || (bits != 16 && !scales) || !bounds || !aligned16(keys) || !aligned16(scales) ||
       !aligned16(bounds) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7) != 0)

@@ -720,7 +720,8 @@ pkv_status pkv_attention_mod_q4(const void *q, const int32_t *cu_seqlens_q, int3
  * keys' values. The keys have to be finite. Rows >= num_blocks * block_size are
  * skipped and set PKV_DEV_BAD_SLOT_MAPPING. Run behind the cache write, on its
  * stream; the mapping is read at once (as pkv_attention reads its metadata).
- * Pointers 16-byte aligned.
+ * Pointers 16-byte aligned. PKV_ERR_UNSUPPORTED where ceil(num_tokens / 16) *
+ * num_kv_heads is above 2^32 - 2.
  */
 pkv_status pkv_key_bounds(const int64_t *slot_mapping, int64_t num_tokens, const void *k_pool, int64_t num_blocks,
                           int32_t block_size, int32_t num_kv_heads, int32_t head_dim, void *bounds,

@@ -379,3 +379,10 @@ def test_blocks_are_copied_in_up_to_five_arrays():
     for n, status in ((4, 0), (5, 0), (6, 1), (0, 1)):
         arrays, sizes = (ctypes.c_void_p * 6)(*[1 << 20] * 6), (ctypes.c_int64 * 6)(*[1024] * 6)
         assert L.pkv_copy_blocks(p, 0, arrays, sizes, n, 10, None, None) == status
+
+
+def test_bounds_refuse_more_warps_than_a_grid_holds():
+    """2^31 - 1 tokens of 65 heads would wrap to a small grid, those of 32 not launch at all."""
+    L, p = B._lib(), ctypes.c_void_p(1 << 20)
+    for heads in (32, 65, 65536):
+        assert B.STATUS_NAMES[L.pkv_key_bounds(p, 2 ** 31 - 1, p, 10, 16, heads, 64, p, None, None)] == "PKV_ERR_UNSUPPORTED"
