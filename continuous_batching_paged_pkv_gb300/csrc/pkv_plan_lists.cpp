@@ -221,8 +221,10 @@ pkv_status pkv_tree_masks(const int32_t *parents, const int32_t *cu, int32_t num
                           uint32_t *masks, int32_t *depths) {
   if (num_seqs < 0 || !cu || cu[0] < 0 || mask_words < 1 || mask_words > PKV_TREE_MAX_ROWS / 32)
     return PKV_ERR_INVALID_ARG;
+  for (int32_t s = 0; s < num_seqs; ++s)  // before `parents` is read: it has as many entries as the last offset says
+    if (cu[s + 1] < cu[s]) return PKV_ERR_INVALID_ARG;
   for (int32_t s = 0; s < num_seqs; ++s) {  // everything is checked before anything is written
-    if (cu[s + 1] < cu[s] || (cu[s + 1] > cu[s] && !parents)) return PKV_ERR_INVALID_ARG;
+    if (cu[s + 1] > cu[s] && !parents) return PKV_ERR_INVALID_ARG;
     if (cu[s + 1] - cu[s] > 32 * mask_words) return PKV_ERR_OUT_OF_RANGE;
     for (int32_t r = cu[s]; r < cu[s + 1]; ++r)
       if (parents[r] < -1 || parents[r] >= r - cu[s]) return PKV_ERR_INVALID_ARG;

@@ -386,3 +386,30 @@ def test_bounds_refuse_more_warps_than_a_grid_holds():
     L, p = B._lib(), ctypes.c_void_p(1 << 20)
     for heads in (32, 65, 65536):
         assert B.STATUS_NAMES[L.pkv_key_bounds(p, 2 ** 31 - 1, p, 10, 16, heads, 64, p, None, None)] == "PKV_ERR_UNSUPPORTED"
+
+
+def test_tree_masks_read_no_parents_behind_the_last_row():
+    """Offsets that fall again are refused before the rows that they seem to name are looked up: the parents stand at
+    the end of a page that nothing follows."""
+    code = """
+import ctypes, mmap
+import numpy as np
+from continuous_batching_paged_pkv_gb300 import binding as B
+page = mmap.PAGESIZE
+area = mmap.mmap(-1, 2 * page)
+at = ctypes.addressof(ctypes.c_char.from_buffer(area))
+libc = ctypes.CDLL(None)
+libc.mprotect.argtypes = [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int]
+assert libc.mprotect(at + page, page, 0) == 0
+parents = np.frombuffer(area, np.int32, page // 4)
+parents[:] = -1
+cu = np.array([0, 250, 2], np.int32)
+status = B._lib().pkv_tree_masks(at + page - 8, cu.ctypes.data, 2, 8, None, None)
+raise SystemExit(0 if status == 1 else 1)
+"""
+    import subprocess
+    import sys
+    from pathlib import Path
+
+    run = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parents[1], timeout=300)
+    assert run.returncode == 0
