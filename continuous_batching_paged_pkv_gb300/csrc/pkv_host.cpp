@@ -49,6 +49,23 @@ struct pkv_pool {
   std::vector<Slot> slots;
 };
 
+namespace {
+
+// A table lets go of block `b`. With its last reference the block goes on top of the free stack, and a copy into it
+// that has not been handed over is dropped: the block may be the destination of another copy by then.
+void give_back(pkv_pool *p, int32_t b) {
+  if (--p->refs[b] > 0) return;
+  p->free_stack.push_back(b);
+  p->on_free[b] = 1;
+  for (size_t i = 0; i < p->copies.size();)
+    if (p->copies[i + 1] == b)
+      p->copies.erase(p->copies.begin() + i, p->copies.begin() + i + 2);
+    else
+      i += 2;
+}
+
+}  // namespace
+
 extern "C" {
 
 const char *pkv_status_string(pkv_status s) {
@@ -174,11 +191,7 @@ pkv_status pkv_pool_release(pkv_pool *p, int32_t slot) {
   if (slot < 0 || slot >= p->max_slots) return PKV_ERR_OUT_OF_RANGE;
   pkv_pool::Slot &s = p->slots[slot];
   if (!s.live) return PKV_ERR_INVALID_ARG;
-  for (auto it = s.blocks.rbegin(); it != s.blocks.rend(); ++it) {
-    if (--p->refs[*it] > 0) continue;  // still in another table
-    p->free_stack.push_back(*it);
-    p->on_free[*it] = 1;
-  }
+  for (auto it = s.blocks.rbegin(); it != s.blocks.rend(); ++it) give_back(p, *it);
   s.blocks.clear();
   s.live = false;
   s.length = 0;
@@ -198,9 +211,7 @@ pkv_status pkv_pool_truncate(pkv_pool *p, int32_t slot, int64_t num_tokens) {
   while (s.blocks.size() > keep) {
     const int32_t b = s.blocks.back();
     s.blocks.pop_back();
-    if (--p->refs[b] > 0) continue;
-    p->free_stack.push_back(b);
-    p->on_free[b] = 1;
+    give_back(p, b);
   }
   return PKV_OK;
 }

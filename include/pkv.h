@@ -174,7 +174,8 @@ int32_t pkv_pool_block_refs(const pkv_pool *pool, int32_t block);
 /*
  * Hand over the copy-on-write copies recorded by pkv_plan_lower since the
  * last call: `pairs` receives 2 * num_pairs int32 (source block, destination
- * block); the list is then cleared. With too little `capacity` (in pairs)
+ * block); the list is then cleared. A copy whose destination went back on the
+ * free stack meanwhile (pkv_pool_release, pkv_pool_truncate) is not among them. With too little `capacity` (in pairs)
  * nothing is cleared and *num_pairs says how many there are
  * (PKV_ERR_WORKSPACE_TOO_SMALL). The copies must run (pkv_copy_blocks, same
  * stream) before the step's cache write.

@@ -413,3 +413,32 @@ raise SystemExit(0 if status == 1 else 1)
 
     run = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parents[1], timeout=300)
     assert run.returncode == 0
+
+
+@pytest.mark.parametrize("undo", ["truncate", "release"])
+def test_a_step_taken_back_before_its_copies_ran(undo):
+    """A copy into a block that was given back meanwhile is dropped, and no block is the destination of two; a copy
+    into a block that the slot keeps stays."""
+    pool = B.Pool(20, 16, 4, 8)
+    pool.admit(0, 0)
+    pool.lower([(0, 40)])
+    for cut in (35, 8):
+        pool.adopt(1, 0, 40)
+        pool.lower([(1, 1)])
+        (_, src), (_, dst) = pool.block_tables()[:2, 1:3].tolist()
+        if undo == "truncate":
+            pool.truncate(1, cut)
+        else:
+            pool.release(1)
+            pool.adopt(1, 0, 40)
+        keeps = undo == "truncate" and cut == 35
+        assert pool.slot_blocks(1) == (3 if keeps or undo == "release" else 1)
+        pool.adopt(2, 0, 40)
+        pool.lower([(2, 1)])
+        copies = pool.take_copies().tolist()
+        again = int(pool.block_tables()[2, 2])
+        assert copies == ([[src, dst], [src, again]] if keeps else [[src, again]]) and (again == dst) == (not keeps)
+        pool.release(1)
+        pool.release(2)
+    pool.release(0)
+    assert pool.stats().free_blocks == 20
