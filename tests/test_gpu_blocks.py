@@ -664,3 +664,103 @@ def test_bounds_of_a_block_that_is_copied_on_write(kv):
             want = OB.bounds(vals[j * bs:(j + 1) * bs]).transpose(1, 0, 2)
             assert np.array_equal(bounds[int(table[j])].double().cpu().numpy(), want), (slot, j)
     assert B.pkv_check_device_status(status) == 0
+
+
+@pytest.mark.parametrize("kind", ["any", "same", "few values"])
+@pytest.mark.parametrize("blocks", [2049, 2500, 12000])
+def test_choice_of_one_long_slot_among_short_ones(blocks, kind):
+    """The segments' mean sets the size of the CTAs: small ones then choose among more candidates than they hold, here
+    with and without scores that have to be told apart."""
+    rng = np.random.default_rng(_seed(blocks, kind))
+    hq, hkv, d, bs, slots, sparse = 8, 2, 64, 16, 40, B.Sparse(24, 1, 1)
+    counts = [30, 26, 1, blocks, 25] + [28] * 15
+    table = np.full((slots, blocks), -1, np.int32)
+    order, at, ss = rng.permutation(sum(counts)).astype(np.int32), 0, rng.permutation(slots)[: len(counts)].astype(np.int32)
+    for s, m in zip(ss, counts):
+        table[s, :m] = order[at:at + m]
+        at += m
+    lo = rng.standard_normal((at, hkv, d))
+    if kind != "any":
+        lo[:] = rng.choice([-1.0, -0.5], (at, hkv, 1)) if kind == "few values" else lo[0]
+    bounds = torch.from_numpy(np.stack([lo, lo + (rng.random(lo.shape) if kind == "any" else 1.0)], 2)).cuda().bfloat16()
+    q = torch.from_numpy(rng.standard_normal((len(counts), hq, d))).cuda().bfloat16()
+    if kind == "few values":
+        q[:] = 1
+    cu, ctx = np.arange(len(counts) + 1, dtype=np.int32), np.zeros(slots, np.int32)
+    ctx[ss] = np.array(counts) * bs - 3
+    work, info = B.pkv_plan_work_sparse(cu, ss, ctx, max_slots=slots, max_blocks_per_slot=blocks, block_size=bs,
+                                        num_q_heads=hq, num_kv_heads=hkv, head_dim=d, sparse=sparse)
+    assert info.scratch_blocks <= 1024 * info.num_prefill_items
+    sel = torch.full((len(counts), hkv, 24), -9, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.pkv_select_blocks(q, *(torch.from_numpy(x).cuda() for x in (cu, ss, ctx, table)), bounds, torch.from_numpy(work).cuda(),
+                        info, sel, torch.empty(info.workspace_bytes, dtype=torch.uint8, device="cuda"), sparse=sparse,
+                        block_size=bs, device_status=status)
+    assert B.pkv_check_device_status(status) == 0
+    q64, exact, got = q.double().cpu().numpy(), bounds.double().cpu().numpy(), sel.cpu().numpy()
+    for i, (s, m) in enumerate(zip(ss, counts)):
+        for h in range(hkv):
+            c = OB.choose(q64[i:i + 1, 4 * h:4 * h + 4], *exact[table[s, :m]][:, h].transpose(1, 0, 2), ctx[s], bs, 24, 1, 1)
+            assert got[i, h].tolist() == c + [-1] * (24 - len(c)), (i, h)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "q8", "q4"])
+def test_a_sparse_step_beside_idle_slots(kv):
+    """A server's slots are mostly more than a step's: the cut of the keys follows the slots, the results do not."""
+    w = W.random_step(43, [(1, 5000), (2, 900), (1, 40), (1, 1300)], num_q_heads=32, num_kv_heads=8, head_dim=128,
+                      max_slots=64, slots=[60, 3, 17, 34])
+    ds = R.prepare(w, kv=kv)
+    R.run_cache_write(ds)
+    bounds, sparse = _bounds(ds), B.Sparse(100, 1, 2)
+    plan = _plan(ds, sparse)
+    sel, call = _select_call(ds, sparse, plan, bounds)
+    call()
+    _attend_call(ds, sparse, plan, sel)()
+    assert B.pkv_check_device_status(ds.status) == 0
+    want = _want_choice(w, sparse, _lohi(ds, bounds))
+    assert np.array_equal(sel.cpu().numpy(), want)
+    _check(ds, want, kv)
+
+
+def test_attention_started_with_a_move_sees_every_moved_row():
+    """Long moves over rows that are new in every round, and attention that reads them as history: launched one behind
+    the other and in one graph, against the same calls with a synchronisation between them."""
+    w = W.random_step(32, [(1, 400)] * 60, num_q_heads=32, num_kv_heads=8, head_dim=128)
+    ds = R.prepare(w)
+    R.run_cache_write(ds)
+    cu = torch.arange(0, 60 * 140 + 1, 140, dtype=torch.int32, device="cuda")  # the last 140 rows of every slot
+    path = torch.arange(40, 130, dtype=torch.int32, device="cuda").expand(60, 90).contiguous()
+    move = B.AcceptRowsCall(cu, ds.seq_slot, ds.context_lens, ds.block_tables, path, [ds.k_pool, ds.v_pool],
+                            device_status=ds.status)
+    move()
+    R.run_attention(ds)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        move()
+        R.run_attention(ds)
+
+    def apart():
+        move()
+        torch.cuda.synchronize()
+        R.run_attention(ds)
+
+    def together():
+        move()
+        R.run_attention(ds)
+
+    for _ in range(4):
+        fresh = [torch.randn_like(t) for t in (ds.k_pool, ds.v_pool)]
+        results = []
+        for run in (apart, together, graph.replay):
+            for t, f in zip((ds.k_pool, ds.v_pool), fresh):
+                t.copy_(f)
+            ds.out.fill_(9.0)
+            torch.cuda.synchronize()
+            run()
+            torch.cuda.synchronize()
+            results.append([t.clone() for t in (ds.out, ds.k_pool, ds.v_pool)])
+        for other in results[1:]:
+            assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+    assert B.pkv_check_device_status(ds.status) == 0

@@ -575,3 +575,16 @@ def test_chunks_modified_chunks_and_trees_one_behind_another(d):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), order
     assert B.pkv_check_device_status(ds.status) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_trees_beside_idle_slots(d):
+    """Few live slots of many: longer spans, the same attention."""
+    shapes = [(8, 8200), (64, 9000), (1, 30), (33, 2000)]
+    w = W.random_step(90, shapes, num_q_heads=8, num_kv_heads=2, head_dim=d, max_slots=64, slots=[63, 0, 31, 8])
+    ds = R.prepare(w)
+    R.run_cache_write(ds)
+    masks, _ = B.pkv_tree_masks(_parents(np.random.default_rng(0), [n for n, _ in shapes]), ds.lowered.cu_seqlens_q)
+    _call(ds, masks)[0]()
+    assert B.pkv_check_device_status(ds.status) == 0
+    _check(ds, masks, f"idle {d}")
