@@ -494,6 +494,12 @@ def timed_calls(flush, stream, fns, n):
     return out
 
 
+def timed_alone(flush, stream, fn):
+    """Device time of one call in ms: the median of three, since a launch that comes late (the host was held up) would
+    count as kernel time."""
+    return statistics.median(timed_calls(flush, stream, [fn], 3)[0])
+
+
 def measure_step(name, w, dev, **kw):
     """Device and end-to-end timings of one synthetic step (see the module docstring)."""
     with gc_paused():
@@ -865,8 +871,8 @@ def run_churn(args, rank, world, local_rank):
                 # breakdown: the two calls apart, then the chunk kernel alone and the decode + merge kernels alone
                 w_ms, a_ms = timed_calls(flush, stream, [write, attend], 1)
                 cw, dw = R.split_work(v["work"], info)
-                c_ms = timed_calls(flush, stream, [lambda: attend(cw[0], cw[1], None)], 1)[0] if cw else []
-                d_ms = timed_calls(flush, stream, [lambda: attend(dw[0], dw[1], ws)], 1)[0] if dw else []
+                c_ms = [timed_alone(flush, stream, lambda: attend(cw[0], cw[1], None))] if cw else []
+                d_ms = [timed_alone(flush, stream, lambda: attend(dw[0], dw[1], ws))] if dw else []
             torch.cuda.synchronize()
             if B.pkv_check_device_status(status) != 0:
                 raise RuntimeError(f"device status reported an error at churn step {step}")
@@ -909,7 +915,7 @@ def run_churn(args, rank, world, local_rank):
                             "algorithmic_flop_per_launch": sum(chunk_fl) / len(chunk_fl),
                             "mean_launch_ms": mean(chunk_ms), "launches": len(chunk_ms),
                             "total_ms": sum(chunk_ms),
-                            "peak_source": f"{peak_src} bf16 burst (the chunk kernel is timed alone, per step)"}
+                            "peak_source": f"{peak_src} bf16 burst (the chunk kernel is timed alone, per step, median of 3)"}
     if dec_ms:
         ach = sum(dec_bytes) / (sum(dec_ms) / 1e3) / 1e9
         kernels["decode"] = {"bound": "hbm", "kernel": "decode_kernel + span merge (merge_small/merge_wide)",
@@ -918,7 +924,7 @@ def run_churn(args, rank, world, local_rank):
                              "algorithmic_bytes_per_launch": sum(dec_bytes) / len(dec_bytes),
                              "mean_launch_ms": mean(dec_ms), "launches": len(dec_ms), "total_ms": sum(dec_ms),
                              "peak_source": f"{peak_src} HBM copy bandwidth (decode and merge kernels timed "
-                                            f"alone, per step)"}
+                                            f"alone, per step, median of 3)"}
     dominant = max(kernels, key=lambda k: kernels[k]["total_ms"]) if kernels else None
     roofline = dict(kernels[dominant]) if dominant else {
         "bound": "hbm", "kernel": "whole step", "achieved": value / world, "peak": hbm, "unit": "GB/s",

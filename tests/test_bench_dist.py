@@ -115,3 +115,11 @@ def test_a_failed_config_is_reported_not_fatal(monkeypatch):
     out = bench.run_configs(args, 0, 1, "cpu", flush=None)
     assert set(out) == {n if kv == "bf16" else f"{n}_{kv}" for n, kv in bench.EXTRA_CONFIGS}
     assert out["decode256_q8"]["error"] == "MemoryError: no room for the q8 pool of decode256"
+
+
+def test_a_late_launch_is_no_kernel_time(monkeypatch):
+    """A kernel timed alone is the median of three launches, not the one that the host held up."""
+    import bench
+
+    monkeypatch.setattr(bench, "timed_calls", lambda flush, stream, fns, n: [[0.05, 1.25, 0.06][:n] for _ in fns])
+    assert bench.timed_alone(None, None, lambda: None) == 0.06
