@@ -289,7 +289,8 @@ inline int32_t prefill_rows_per_tile(int32_t group) { return 128 / group; }
 // Trees (pkv_tree.cu): keys come in tiles of 128; a CTA takes two query tiles where some segment of the step has
 // more than one, else one: 64 slots x 32 nodes of 8 q heads a kv head (two tiles a tree), up to 8192 keys, take 149 us
 // (163 with one tile everywhere), one slot of 64 nodes of 4, 32,768 keys, 39.8 (42.3); where a tree is one tile, two
-// would leave half of a CTA idle. Spans of kTreeMinSpanTiles to kTreeSpanTiles tiles.
+// leave half of a CTA idle, which costs a mixed step nothing: 64 trees of 8 nodes of 8 take 142 us, 63 of them beside
+// one of 32 nodes 130 (L2 flushed before each call). Spans of kTreeMinSpanTiles to kTreeSpanTiles tiles.
 constexpr int kTreeTileKeys = 128, kTreeMinSpanTiles = 2, kTreeSpanTiles = 64;
 constexpr int kTreeMaxSpans = 0xFFFF;  // what an item's span and a merge item's count hold
 constexpr int kTreeMaxKeys = kTreeMaxSpans * kTreeSpanTiles * kTreeTileKeys;  // the longest context, in the longest spans

@@ -191,7 +191,10 @@ pkv_status no_throw(Fn fn, Args &&...args) {
 // Tiles of a span: as many spans as still leave one CTA to an SM (two where a segment's rows are one query tile)
 // if all slots were as long, and no span longer than kTreeSpanTiles, so that the slots' different lengths even
 // out (64 slots of up to 8192 keys: 154 us; 179 with spans of at most 32 tiles, whose starts and partials cost more).
-// It depends on the segment and the tables' shape, not on the rest of the step.
+// It depends on the segment and the tables' shape, not on the rest of the step. So a slot that stands idle counts as
+// one of the same length, and few live slots of many get longer spans and fewer CTAs than the GPU holds: 5 slots x 8
+// nodes of up to 8192 keys take 26.6 us with 5 slots in the tables, 45 with 16 and 74 with 64; one slot x 64 nodes,
+// 32,768 keys, 45 us alone and 113 beside 15 or 63 idle ones (L2 flushed before each call).
 int64_t pkv::tree_span_tiles(int64_t tiles, int32_t q_tiles, int32_t max_slots, int32_t num_kv_heads) {
   const int64_t ctas = q_tiles > 1 ? 152 : 304, units = ceil_div(q_tiles, 2);
   const int64_t spans = std::max<int64_t>(1, ctas / (static_cast<int64_t>(max_slots) * num_kv_heads * units));

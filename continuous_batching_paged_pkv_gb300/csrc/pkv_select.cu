@@ -666,7 +666,9 @@ cudaError_t launch_select_blocks(const StepArgs &a, const void *bounds, const pk
   };
   // Small CTAs where the segments have few candidates: 256 slots x 8 heads of 145 on average take 14.8 us with 128
   // threads, 16.0 with 64 (and 30 with one warp, whose longest segment sets the time); 5 slots x 8 heads of up to
-  // 8190 take 15.8 us with 1024.
+  // 8190 take 15.8 us with 1024. The mean decides, so a long segment among many short ones gets a small CTA that
+  // reads its scores from L2 in every pass: the whole selection of one slot of 8190 candidates among 63 of 254 takes
+  // 97 us, that of the one by itself 26, of the 63 36 (L2 flushed before each call).
   if (cand <= 1024ll * info.num_prefill_items)
     return a.head_dim == 128 ? go(choose_blocks_kernel<128, 128, 2048>, 128, 2048)
                              : go(choose_blocks_kernel<64, 128, 2048>, 128, 2048);

@@ -31,7 +31,7 @@
 // There are two issuers because an issue blocks its thread until the tensor core
 // takes it.
 //
-// Measured: 64 slots x 32 nodes, 64 + 8 heads of 128, up to 8192 keys: 149-154 us, 766
+// Measured: 64 slots x 32 nodes, 64 + 8 heads of 128, up to 8192 keys: 146-154 us, 766
 // MB of keys and values at 5.0 TB/s; a unit of two tiles takes 1370 cycles, HBM's share
 // of an SM is 1400, the rest is the CTAs' starts and ends (5 us each). One slot x 64
 // nodes, 32 + 8 heads, 32,768 keys: 39.5 us with the merge (8), 5 slots x 8 nodes 20.

@@ -860,7 +860,8 @@ pkv_status pkv_tree_masks(const int32_t *parents, const int32_t *cu_seqlens_q, i
  * partials (spans times rows) in the step (PKV_ERR_UNSUPPORTED beyond either).
  * They may be the last ones of a packed step: cu_seqlens_q then starts above 0.
  * Otherwise the validation, sizes and errors of pkv_plan_work. The keys are cut into spans of whole 128-key tiles; the cut
- * depends on the segment and on max_slots, not on the other segments.
+ * depends on the segment and on max_slots (idle slots count as long ones), not on
+ * the other segments.
  *
  * Item words: decode (segment, slot, span | (128-key tiles in a span - 1) << 16 |
  * query tile << 24, the span's first partial or -1; the partial of row i is i
